@@ -288,6 +288,177 @@ ps_status ps_factored_step(const ps_tensor* tensors, int32_t n_tensors, const ps
 ps_status ps_factored_step_noalloc(const ps_tensor* tensors, int32_t n_tensors, const ps_factored_hparams* hp,
                                    int64_t step, ps_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * AdamW over many tensors with 32-bit or 8-bit moments, and the global
+ * gradient norm that clips it: the step of mixed-precision training, where a
+ * model runs on 16-bit copies of fp32 master weights (or on bf16 weights, with
+ * a residual or stochastic rounding), its parameters fall into groups with
+ * hyperparameters of their own and its gradients are clipped by their norm.
+ *
+ * A PLAN is made once from the tensor list and then run every step. It reads
+ * and writes a workspace that the caller owns (device memory), so a run
+ * allocates nothing, copies nothing from the host and can be captured into a
+ * HIP graph.
+ * ------------------------------------------------------------------------- */
+
+/* Element types of parameters, gradients and copies. */
+enum { PS_TYPE_F32 = 0, PS_TYPE_BF16 = 1, PS_TYPE_F16 = 2 };
+/* Moment storage of a tensor.
+ *   PS_STATE_F32   m, v: float[numel]
+ *   PS_STATE_E4M3  m, v: one byte per element (OCP e4m3fn), one scale per 256
+ *                  elements; v holds sqrt(v). See ps_encode_fp8. */
+enum { PS_STATE_F32 = 0, PS_STATE_E4M3 = 1 };
+/* Rounding of the second moment's e4m3 codes. With beta2 = 0.999 a second
+ * moment whose gradient has become small shrinks by 0.05% of sqrt(v) a step,
+ * far less than half a code, so rounding to the nearest leaves it where it is
+ * until its block's scale changes; STOCHASTIC moves it by the right amount on
+ * average. */
+enum { PS_ROUND_NEAREST = 0, PS_ROUND_STOCHASTIC = 1 };
+
+#define PS_ADAMW_MAX_GROUPS 16
+
+/* One parameter tensor. Contiguous device arrays of numel elements, 16-byte
+ * aligned (scales: 4 bytes).
+ *   param     float (PS_TYPE_F32) or bf16 (PS_TYPE_BF16), read and written.
+ *             NULL: only the gradient counts (ps_adamw_grad_norm), the step
+ *             passes the tensor by
+ *   residual  PS_TYPE_BF16: the low halves of the fp32 master weights, as
+ *             ps_tensor.w_lo; may be NULL if the steps' split_mode is
+ *             STOCHASTIC. PS_TYPE_F32: NULL
+ *   copy      PS_TYPE_F32: array of copy_type (BF16 or F16) that each step
+ *             writes the new weights to, rounded to nearest even; NULL: none.
+ *             PS_TYPE_BF16: NULL
+ *   grad      array of grad_type, read only; NULL: the tensor is passed by
+ *             (a later ps_adamw_set_grads may give it one)
+ *   m, v      moments (state_type); m_scale, v_scale: PS_STATE_E4M3 only,
+ *             ceil(numel / 256) floats. All bytes zero is a fresh state
+ *   group     index of the tensor's hyperparameters in ps_adamw_step's groups
+ * A tensor with numel == 0 is passed by and its pointers are not read. */
+typedef struct ps_adamw_tensor {
+  void* param;
+  uint16_t* residual;
+  void* copy;
+  const void* grad;
+  void* m;
+  float* m_scale;
+  void* v;
+  float* v_scale;
+  int64_t numel;
+  int32_t param_type;
+  int32_t grad_type;
+  int32_t copy_type;
+  int32_t state_type;
+  int32_t group;
+  int32_t reserved; /* must be 0 */
+} ps_adamw_tensor;
+
+/* The first bytes of a plan's workspace, in device memory. ps_adamw_plan_create
+ * sets grad_mul = 1, lr_mul = 1 and the rest to 0; a caller may read and write
+ * them in stream order.
+ *   norm      last ps_adamw_grad_norm: grad_scale * (2-norm of all gradients)
+ *   grad_mul  last ps_adamw_grad_norm: what a clipped step multiplies the
+ *             gradients by
+ *   skip      last ps_adamw_grad_norm: 1 if a gradient was infinite or NaN; a
+ *             clipped step then changes nothing
+ *   skipped   number of ps_adamw_grad_norm calls that set skip
+ *   step      updates made so far by steps that count on the device
+ *   lr_mul    factor of the learning rate in steps that count on the device
+ *             (a schedule for captured graphs) */
+typedef struct ps_adamw_control {
+  float norm;
+  float grad_mul;
+  uint32_t skip;
+  uint32_t skipped;
+  int64_t step;
+  float lr_mul;
+  uint32_t reserved[9];
+} ps_adamw_control;
+
+typedef struct ps_adamw_plan ps_adamw_plan;
+
+/* ps_adamw_workspace_size - device workspace bytes of a plan over this list.
+ * Host only. Errors: PS_ERR_INVALID_ARG, PS_ERR_ALIGNMENT, PS_ERR_SHAPE. */
+ps_status ps_adamw_workspace_size(const ps_adamw_tensor* tensors, int32_t n_tensors, size_t* bytes);
+
+/* ps_adamw_plan_create - checks the list and lays it out in the workspace
+ * (256-byte aligned, at least ps_adamw_workspace_size bytes, on the current
+ * device; its contents on entry are ignored, and it belongs to the plan until
+ * the plan is destroyed and its last run has ended). Ordered on `stream`,
+ * which it synchronizes; PS_ERR_UNSUPPORTED while `stream` is being captured.
+ * The list itself is not kept. Arrays that are written (param, residual, copy,
+ * moments, scales) must not overlap each other or a gradient
+ * (PS_ERR_INVALID_ARG); gradients may. */
+ps_status ps_adamw_plan_create(const ps_adamw_tensor* tensors, int32_t n_tensors, void* workspace,
+                               size_t workspace_bytes, ps_stream_t stream, ps_adamw_plan** plan);
+
+/* ps_adamw_set_grads - new gradient arrays (types and sizes as before) for the
+ * plan's tensors, in list order, n_grads == n_tensors; NULL: the tensor is
+ * passed by from now on. Asynchronous, ordered on `stream`; the pointers are
+ * copied during the call and travel in kernel arguments. */
+ps_status ps_adamw_set_grads(ps_adamw_plan* plan, const void* const* grads, int32_t n_grads, ps_stream_t stream);
+
+/* ps_adamw_grad_norm - the 2-norm of all the plan's gradients and the factor
+ * that clips it, into the control block:
+ *   norm = fp32(n), n = grad_scale * sqrt(sum g^2)
+ *   grad_mul = fp32(grad_scale * min(1, max_norm / (n + 1e-6)))
+ *   skip = 1 if n is infinite or NaN (grad_mul is then 0), else 0
+ * Squares, sums and the formulas are in double, the sums in an order that
+ * depends on the list's sizes and types only. grad_scale: finite, > 0 (the inverse of a loss
+ * scale); max_norm: > 0, infinity for no clipping. */
+ps_status ps_adamw_grad_norm(ps_adamw_plan* plan, double max_norm, double grad_scale, ps_stream_t stream);
+
+/* ps_adamw_step - one (N)AdamW step over the plan's tensors.
+ * groups[0 .. n_groups-1]: the hyperparameters of each group, n_groups at most
+ * PS_ADAMW_MAX_GROUPS and above every tensor's group; algo and split_mode are
+ * the same in all groups. Per element:
+ *   g  = fp32(grad), times grad_mul if `clipped`
+ *   m  = B1*m0 + C1*g;  v = B2*v0 + C2*(g*g);  r = sqrt(v);  d = r*RS2 + EPS
+ *   ADAM: u = A*(m/d)             NADAM: u = (AG*g + AM*m)/d
+ *   u  = u + CWD*w;  w' = w - u
+ * Every operation is rounded to fp32 by itself (no fma); the scalars are those
+ * of ps_step_scalars. w is the fp32 parameter, the joined (bf16, residual)
+ * pair, or with split_mode STOCHASTIC the bf16 value alone; w' is stored as
+ * it is (and rounded to copy_type for the copy), split, or rounded
+ * stochastically, with the random bits of ps_hparams for the tensor's index in
+ * the plan's list. Moments are stored as fp32 or as ps_encode_fp8 would code m
+ * and v; the update uses this step's fp32 values.
+ *   step      >= 1: the update's number. 0: the number is counted in the
+ *             control block: each call that is not skipped adds 1 and uses the
+ *             sum, and the learning rate is lr * lr_mul (PS_ALGO_ADAM only;
+ *             the scalars are then computed in double on the device)
+ *   clipped   0 or 1: use the control block's grad_mul and skip
+ *   rounding  PS_ROUND_*: the second moment's e4m3 codes. STOCHASTIC: the 16
+ *             random bits of element e come from the stream of list index
+ *             i + 2^31 (ps_hparams), fill the places below the last kept one
+ *             and are cut off with them:
+ *             code = floor(r/s in units of its last e4m3 place + bits / 2^16)
+ * A captured call replays with the same step, groups and rounding: capture
+ * calls with step = 0.
+ * Calls on one plan must be ordered by the caller, as two calls on one stream
+ * are; the current device must be the plan's (PS_ERR_INVALID_ARG).
+ * Errors: PS_ERR_INVALID_ARG, PS_ERR_UNSUPPORTED, PS_ERR_HIP. */
+ps_status ps_adamw_step(ps_adamw_plan* plan, const ps_hparams* groups, int32_t n_groups, int64_t step,
+                        int32_t clipped, int32_t rounding, ps_stream_t stream);
+
+/* Frees the host side of the plan. Waits for nothing: the workspace stays in
+ * use until the plan's last run has ended. */
+ps_status ps_adamw_plan_destroy(ps_adamw_plan* plan);
+
+/* ps_encode_fp8 / ps_decode_fp8 - the 8-bit moment codec: OCP e4m3fn codes with
+ * one fp32 scale per 256 elements (the last block covers n mod 256), a power of
+ * two.
+ * Encode, per block: y = x (SIGNED: a first moment) or sqrt(x) (UNSIGNED: a
+ * second moment, x >= 0); s = the smallest power of two >= 2^-126 with
+ * max|y| <= 448 s; code = y / s rounded to the nearest e4m3 value, ties to even;
+ * UNSIGNED codes of x > 0 are at least 2^-9, the smallest e4m3 value, so that
+ * no second moment above zero becomes zero.
+ * Decode: SIGNED x = code * s; UNSIGNED x = (code * s)^2. Since s is a power of
+ * two, SIGNED decode is exact and a block that is decoded and encoded again
+ * keeps its values. Arrays 16-byte aligned, scale 4-byte. */
+ps_status ps_encode_fp8(const float* x, uint8_t* code, float* scale, int64_t n, int32_t kind, ps_stream_t stream);
+ps_status ps_decode_fp8(const uint8_t* code, const float* scale, float* x, int64_t n, int32_t kind,
+                        ps_stream_t stream);
+
 /* Host-offload pipeline [NADAM, opening post: moments (and here the
  * residuals) live in host memory and cross PCIe every step].
  * A group is one set of tensors stepped together (e.g. one transformer

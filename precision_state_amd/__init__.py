@@ -39,12 +39,18 @@ SPLIT_TRUNC, SPLIT_NEAREST_AWAY, SPLIT_STOCHASTIC = 0, 1, 2
 MOMENT_SIGNED, MOMENT_UNSIGNED = 0, 1
 TENSOR_FP32_MOMENTS, TENSOR_FP32_PARAM, TENSOR_F24_MOMENTS = 1, 2, 4
 BLOCK = 256
+TYPE_F32, TYPE_BF16, TYPE_F16 = 0, 1, 2
+STATE_F32, STATE_E4M3 = 0, 1
+ROUND_NEAREST, ROUND_STOCHASTIC = 0, 1
+ADAMW_MAX_GROUPS = 16
 
 STATUS = {0: "PS_OK", 1: "PS_ERR_INVALID_ARG", 2: "PS_ERR_ALIGNMENT", 3: "PS_ERR_SHAPE",
           4: "PS_ERR_UNSUPPORTED", 5: "PS_ERR_HIP", 6: "PS_ERR_NO_MEMORY", 7: "PS_ERR_WORKSPACE"}
 
 EXPORTED = ["ps_opt_step_multi", "ps_step_scalars", "ps_split", "ps_join", "ps_encode_moments",
             "ps_decode_moments", "ps_factored_workspace_size", "ps_factored_step", "ps_factored_step_noalloc",
+            "ps_adamw_workspace_size", "ps_adamw_plan_create", "ps_adamw_set_grads", "ps_adamw_grad_norm",
+            "ps_adamw_step", "ps_adamw_plan_destroy", "ps_encode_fp8", "ps_decode_fp8",
             "ps_offload_plan_create", "ps_offload_plan_create_ex",
             "ps_offload_run", "ps_offload_bytes", "ps_offload_plan_destroy", "ps_status_string",
             "ps_last_error", "ps_version"]
@@ -77,6 +83,20 @@ class CFHParams(ctypes.Structure):
                 ("seed", ctypes.c_uint64)]
 
 
+class CAdamWTensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("copy", ctypes.c_void_p),
+                ("grad", ctypes.c_void_p), ("m", ctypes.c_void_p), ("m_scale", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("param_type", ctypes.c_int32), ("grad_type", ctypes.c_int32), ("copy_type", ctypes.c_int32),
+                ("state_type", ctypes.c_int32), ("group", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class CAdamWControl(ctypes.Structure):
+    _fields_ = [("norm", ctypes.c_float), ("grad_mul", ctypes.c_float), ("skip", ctypes.c_uint32),
+                ("skipped", ctypes.c_uint32), ("step", ctypes.c_int64), ("lr_mul", ctypes.c_float),
+                ("reserved", ctypes.c_uint32 * 9)]
+
+
 class COffloadGroup(ctypes.Structure):
     _fields_ = [("tensors", ctypes.POINTER(CTensor)), ("n_tensors", ctypes.c_int32)]
 
@@ -91,6 +111,7 @@ OFFLOAD_DEFAULT_CUS = 8
 
 
 _vp, _i64, _i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+_f64 = ctypes.c_double
 _sig = {
     "ps_opt_step_multi": [ctypes.POINTER(CTensor), _i32, ctypes.POINTER(CHParams), _i64, _vp],
     "ps_step_scalars": [ctypes.POINTER(CHParams), _i64, ctypes.POINTER(ctypes.c_float)],
@@ -101,6 +122,14 @@ _sig = {
     "ps_factored_workspace_size": [ctypes.POINTER(CTensor), _i32, ctypes.POINTER(ctypes.c_size_t)],
     "ps_factored_step": [ctypes.POINTER(CTensor), _i32, ctypes.POINTER(CFHParams), _i64, _vp, ctypes.c_size_t, _vp],
     "ps_factored_step_noalloc": [ctypes.POINTER(CTensor), _i32, ctypes.POINTER(CFHParams), _i64, _vp],
+    "ps_adamw_workspace_size": [ctypes.POINTER(CAdamWTensor), _i32, ctypes.POINTER(ctypes.c_size_t)],
+    "ps_adamw_plan_create": [ctypes.POINTER(CAdamWTensor), _i32, _vp, ctypes.c_size_t, _vp, ctypes.POINTER(_vp)],
+    "ps_adamw_set_grads": [_vp, ctypes.POINTER(_vp), _i32, _vp],
+    "ps_adamw_grad_norm": [_vp, _f64, _f64, _vp],
+    "ps_adamw_step": [_vp, ctypes.POINTER(CHParams), _i32, _i64, _i32, _i32, _vp],
+    "ps_adamw_plan_destroy": [_vp],
+    "ps_encode_fp8": [_vp, _vp, _vp, _i64, _i32, _vp],
+    "ps_decode_fp8": [_vp, _vp, _vp, _i64, _i32, _vp],
     "ps_offload_plan_create": [ctypes.POINTER(COffloadGroup), _i32, ctypes.POINTER(ctypes.c_void_p)],
     "ps_offload_plan_create_ex": [ctypes.POINTER(COffloadGroup), _i32, ctypes.POINTER(COffloadOptions),
                                   ctypes.POINTER(ctypes.c_void_p)],
@@ -366,6 +395,235 @@ class OffloadPlan:
         if self._h:
             _check(_lib.ps_offload_plan_destroy(self._h))
             self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _fp8_check(x, code, scale):
+    import torch
+    n = x.numel()
+    if x.dtype != torch.float32 or scale.dtype != torch.float32 or code.element_size() != 1:
+        raise ValueError("x and scale are float32, code has 1-byte elements")
+    if code.numel() != n or scale.numel() != (n + BLOCK - 1) // BLOCK:
+        raise ValueError("code needs x's size and scale one value for each 256 of them")
+    if not (x.is_contiguous() and code.is_contiguous() and scale.is_contiguous()):
+        raise ValueError("x, code and scale must be contiguous")
+    if not (x.device == code.device == scale.device):
+        raise ValueError("x, code and scale must be on one device")
+
+
+def encode_fp8(x, code, scale, kind, stream=None):
+    """float32 moments -> e4m3 codes and a power-of-two scale for each 256 (ps_encode_fp8); kind MOMENT_UNSIGNED
+    codes the square root. code: any 1-byte dtype, torch.float8_e4m3fn among them."""
+    _fp8_check(x, code, scale)
+    with _on(x.device):
+        _check(_lib.ps_encode_fp8(_ptr(x), _ptr(code), _ptr(scale), x.numel(), kind, _stream(stream)))
+
+
+def decode_fp8(code, scale, x, kind, stream=None):
+    """The float32 moments that e4m3 codes and scales stand for (ps_decode_fp8)."""
+    _fp8_check(x, code, scale)
+    with _on(x.device):
+        _check(_lib.ps_decode_fp8(_ptr(code), _ptr(scale), _ptr(x), x.numel(), kind, _stream(stream)))
+
+
+class _NoSwitch:
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+
+_NO_SWITCH = _NoSwitch()
+
+
+def _on(device):
+    """Makes `device` the current one; nothing to do where it is."""
+    import torch
+    if device.type != "cuda" or device.index is None or device.index == torch.cuda.current_device():
+        return _NO_SWITCH
+    return torch.cuda.device(device)
+
+
+@dataclass
+class AdamWTensor:
+    """One parameter of an AdamWPlan (see ps_adamw_tensor in include/ps.h).
+
+    param: float32, or bfloat16 (any other 2-byte dtype is read as bf16 bits);
+    None if only the gradient's norm is wanted. grad: float32, bfloat16 or
+    float16, or None. m, v: float32, or a 1-byte dtype (e4m3 codes) with m_scale
+    and v_scale. residual: a bf16 parameter's low halves. copy: bfloat16 or
+    float16, written with a float32 parameter's new values."""
+    param: object
+    grad: object
+    m: object = None
+    v: object = None
+    m_scale: object = None
+    v_scale: object = None
+    residual: object = None
+    copy: object = None
+    group: int = 0
+
+
+def _adamw_record(i, t):
+    import torch
+
+    def wrong(what):
+        return ValueError(f"tensor {i}: {what}")
+    ref = t.param if t.param is not None else t.grad
+    if ref is None:
+        raise wrong("param and grad are both None")
+    n = ref.numel()
+    types = {torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16, torch.float16: TYPE_F16}
+    rec = CAdamWTensor(numel=n, group=t.group)
+    nb = (n + BLOCK - 1) // BLOCK
+    for name, size in (("param", n), ("grad", n), ("m", n), ("v", n), ("residual", n), ("copy", n), ("m_scale", nb),
+                       ("v_scale", nb)):
+        x = getattr(t, name)
+        if x is None:
+            continue
+        if x.numel() != size:
+            raise wrong(f"{name} has {x.numel()} elements, not {size}")
+        if not x.is_contiguous():
+            raise wrong(f"{name} is not contiguous")
+        if x.device != ref.device:
+            raise wrong(f"{name} is on {x.device}, not on {ref.device}")
+        setattr(rec, name, x.data_ptr() if size else None)
+    if t.grad is not None:
+        if t.grad.dtype not in types:
+            raise wrong(f"grad has dtype {t.grad.dtype}")
+        rec.grad_type = types[t.grad.dtype]
+    elif t.param is not None:
+        rec.grad_type = types.get(t.param.dtype, TYPE_BF16)   # what a later gradient has to be
+    if t.param is None:
+        return rec
+    if t.m is None or t.v is None:
+        raise wrong("m and v are needed")
+    if t.param.dtype == torch.float32:
+        rec.param_type = TYPE_F32
+    elif t.param.dtype == torch.float16 or t.param.element_size() != 2:
+        raise wrong(f"param has dtype {t.param.dtype}")
+    else:
+        rec.param_type = TYPE_BF16
+    if t.residual is not None and t.residual.element_size() != 2:
+        raise wrong("residual has no 2-byte dtype")
+    if t.copy is not None:
+        if t.copy.dtype not in (torch.bfloat16, torch.float16):
+            raise wrong(f"copy has dtype {t.copy.dtype}")
+        rec.copy_type = types[t.copy.dtype]
+    if t.m.dtype == torch.float32 and t.v.dtype == torch.float32:
+        rec.state_type = STATE_F32
+        if t.m_scale is not None or t.v_scale is not None:
+            raise wrong("float32 moments have no scales")
+    elif t.m.element_size() == 1 and t.v.element_size() == 1:
+        rec.state_type = STATE_E4M3
+        if t.m_scale is None or t.v_scale is None:
+            raise wrong("e4m3 moments need m_scale and v_scale")
+        if t.m_scale.dtype != torch.float32 or t.v_scale.dtype != torch.float32:
+            raise wrong("scales are float32")
+    else:
+        raise wrong(f"m and v have dtypes {t.m.dtype} and {t.v.dtype}")
+    return rec
+
+
+class AdamWPlan:
+    """AdamW over a fixed list of tensors, and the norm of their gradients
+    (ps_adamw_*). Made once; every call then runs on the plan's device, on
+    `stream` or the device's current stream, with no allocation. The plan keeps
+    its tensors alive; a graph that captured its calls needs the plan.
+
+    The control block's fields are 0-dim tensors in device memory, read and
+    written in stream order: norm, grad_mul, skip, skipped, step, lr_mul."""
+
+    _h = None
+
+    def __init__(self, tensors: Sequence[AdamWTensor], device=None):
+        import torch
+        tensors = list(tensors)
+        recs = [_adamw_record(i, t) for i, t in enumerate(tensors)]
+        devices = {(t.param if t.param is not None else t.grad).device for t in tensors}
+        if len(devices) > 1:
+            raise ValueError("the tensors are on several devices")
+        self.device = devices.pop() if devices else torch.device(device or "cuda")
+        if self.device.type != "cuda":
+            raise ValueError("the tensors are not on a GPU")
+        self._sizes = [(r.numel, r.grad_type) for r in recs]
+        arr = (CAdamWTensor * max(1, len(recs)))(*recs)
+        size = ctypes.c_size_t(0)
+        _check(_lib.ps_adamw_workspace_size(arr, len(recs), ctypes.byref(size)))
+        with _on(self.device):
+            self._stream0 = torch.cuda.current_stream(self.device)
+            self.workspace = torch.empty(size.value, dtype=torch.uint8, device=self.device)
+            h = ctypes.c_void_p()
+            _check(_lib.ps_adamw_plan_create(arr, len(recs), self.workspace.data_ptr(), size.value,
+                                             _stream(self._stream0), ctypes.byref(h)))
+        self._h = h
+        self._tensors = tensors          # the arrays live as long as the plan
+        ctl = self.workspace[:ctypes.sizeof(CAdamWControl)]
+
+        def field(name, dtype):
+            o = getattr(CAdamWControl, name).offset
+            return ctl[o:o + dtype.itemsize].view(dtype).view(())
+        self.norm, self.grad_mul = field("norm", torch.float32), field("grad_mul", torch.float32)
+        self.skip, self.skipped = field("skip", torch.int32), field("skipped", torch.int32)
+        self.step_count, self.lr_mul = field("step", torch.int64), field("lr_mul", torch.float32)
+        self._groups = None
+
+    def _on_stream(self, stream):
+        import torch
+        if not self._h:
+            raise ValueError("the plan is closed")
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        if not isinstance(stream, int):
+            if stream != self._stream0 and not torch.cuda.is_current_stream_capturing():
+                self.workspace.record_stream(stream)   # the allocator must not hand it out before this stream is done
+            stream = stream.cuda_stream
+        return stream
+
+    def set_grads(self, grads, stream=None):
+        """New gradients for all tensors, in list order; None: the tensor is passed by."""
+        import torch
+        if len(grads) != len(self._sizes):
+            raise ValueError(f"{len(grads)} gradients for {len(self._sizes)} tensors")
+        types = (torch.float32, torch.bfloat16, torch.float16)
+        arr = (ctypes.c_void_p * max(1, len(grads)))()
+        for i, (g, (n, ty)) in enumerate(zip(grads, self._sizes)):
+            if g is None:
+                continue
+            if g.dtype != types[ty] or g.numel() != n or not g.is_contiguous() or g.device != self.device:
+                raise ValueError(f"tensor {i}: the gradient must be contiguous {types[ty]} on {self.device} with {n} elements")
+            arr[i] = g.data_ptr()
+        with _on(self.device):
+            _check(_lib.ps_adamw_set_grads(self._h, arr, len(grads), self._on_stream(stream)))
+        for t, g in zip(self._tensors, grads):
+            t.grad = g
+
+    def grad_norm(self, max_norm=float("inf"), grad_scale=1.0, stream=None):
+        """The gradients' global 2-norm and clip factor into the control block (ps_adamw_grad_norm)."""
+        with _on(self.device):
+            _check(_lib.ps_adamw_grad_norm(self._h, max_norm, grad_scale, self._on_stream(stream)))
+
+    def step(self, groups, step=0, clipped=False, rounding=ROUND_NEAREST, stream=None):
+        """One step (ps_adamw_step). groups: the HParams of each group. step: the update's number, from 1, or 0
+        to count on the device."""
+        key = [(g.algo, g.split_mode, g.lr, g.beta1, g.beta2, g.eps, g.weight_decay, g.momentum_decay, g.seed)
+               for g in groups]
+        if self._groups is None or self._groups[0] != key:
+            self._groups = key, (CHParams * max(1, len(key)))(*[CHParams(*k) for k in key])
+        with _on(self.device):
+            _check(_lib.ps_adamw_step(self._h, self._groups[1], len(key), step, int(clipped), rounding,
+                                      self._on_stream(stream)))
+
+    def close(self):
+        if self._h:
+            h, self._h = self._h, None
+            _check(_lib.ps_adamw_plan_destroy(h))
 
     def __del__(self):
         try:

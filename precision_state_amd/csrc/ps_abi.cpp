@@ -38,7 +38,7 @@ ps_status hip_check(hipError_t e, const char* what) {
 bool is_finite(double x) { return std::isfinite(x); }
 bool is_aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
 
-namespace {
+void clear_error() { g_err[0] = 0; }
 
 ps_status check_hparams(const ps_hparams* hp) {
   if (!hp) return fail(PS_ERR_INVALID_ARG, "hparams is NULL");
@@ -58,7 +58,7 @@ ps_status check_hparams(const ps_hparams* hp) {
   return PS_OK;
 }
 
-constexpr int64_t kMaxNumel = int64_t(1) << 40;
+namespace {
 
 ps_status check_array(const void* p, const char* what, int i, uintptr_t align) {
   if (!p) return fail(PS_ERR_INVALID_ARG, "tensor %d: %s is NULL", i, what);
@@ -179,6 +179,8 @@ ps_status get_table(const std::vector<DevTensor>& recs, const std::vector<uint32
   return PS_OK;
 }
 
+}  // namespace
+
 ps_status check_elementwise(int64_t n, std::initializer_list<std::pair<const void*, const char*>> arrays,
                             std::initializer_list<std::pair<const void*, const char*>> scales) {
   if (n < 0 || n > kMaxNumel) return fail(PS_ERR_SHAPE, "n = %lld out of range", (long long)n);
@@ -194,7 +196,6 @@ ps_status check_elementwise(int64_t n, std::initializer_list<std::pair<const voi
   return PS_OK;
 }
 
-}  // namespace
 }  // namespace ps
 
 using namespace ps;
