@@ -1,114 +1,163 @@
 // k_adamw.hip - AdamW over a plan's tensors with fp32 or e4m3 moments, the
 // global gradient norm, and the e4m3 moment codec.
 //
-// Step: one work item of 512 elements is one 64-lane wave; a moment block of
-// 256 elements belongs to 32 lanes, 8 consecutive elements each.
-#include "dev_common.h"
-#include "ps_internal.h"
+// Every kernel here streams its arrays through once and is bound by HBM, or by
+// the vector units where random bits are drawn. Step: one work item of 512
+// elements (two moment blocks) is one 64-lane wave in a workgroup of its own;
+// the item's tensor is found by a binary search over scalar loads.
+#include "dev_adamw.h"
+#include "ps_adamw.h"
 
 namespace ps {
 namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
+// Constant address space: wave-uniform reads through it are scalar loads. The
+// tables are written between kernels only.
+#define CONSTANT __attribute__((address_space(4)))
+
+template <class T>
+__device__ __forceinline__ T ld_const(const T* p) {
+  uint64_t w[sizeof(T) / 8];
+  static_assert(sizeof(T) % 8 == 0, "whole words");
+#pragma unroll
+  for (int k = 0; k < (int)(sizeof(T) / 8); ++k) w[k] = ((const CONSTANT uint64_t*)p)[k];
+  T t;
+  __builtin_memcpy(&t, w, sizeof(T));
+  return t;
+}
+
+typedef GLOBAL char* gptr;   // an address in HBM: a wave-uniform one in it keeps the lane offsets at 32 bits
+
+template <class T>
+__device__ __forceinline__ gptr global(T* p) { return (gptr)(GLOBAL T*)p; }
+template <class T>
+__device__ __forceinline__ gptr global(const T* p) { return (gptr)(GLOBAL T*)p; }
+
 template <class V>
-__device__ __forceinline__ V ld_nt(const void* p) {
+__device__ __forceinline__ V ld_nt(gptr p) {
   return __builtin_nontemporal_load((const GLOBAL V*)p);
 }
 template <class V>
-__device__ __forceinline__ void st_nt(void* p, V v) {
+__device__ __forceinline__ void st_nt(gptr p, V v) {
   __builtin_nontemporal_store(v, (GLOBAL V*)p);
 }
 
 // ---------------------------------------------------------------------------
-// Eight consecutive elements e .. e+7 of an array of n; elements at n and
-// beyond read as zero and are not written.
+// R consecutive elements (4 or 8) of a run that starts `off` elements behind a
+// wave-uniform pointer with `left` elements behind it; R divides off, and the
+// addresses are R-element aligned. FULL: all of them exist. Otherwise elements
+// at `left` and beyond read as zero and are not written.
 // ---------------------------------------------------------------------------
-
-__device__ __forceinline__ void ld8_f32(const void* p, int64_t e, int64_t n, float* d) {
-  const float* q = (const float*)p + e;
-  if (e + 8 <= n) {
-    const f32x4 a = ld_nt<f32x4>(q), b = ld_nt<f32x4>(q + 4);
-    d[0] = a.x; d[1] = a.y; d[2] = a.z; d[3] = a.w;
-    d[4] = b.x; d[5] = b.y; d[6] = b.z; d[7] = b.w;
+template <int R, bool FULL>
+__device__ __forceinline__ void ld_f32(gptr p, uint32_t off, uint32_t left, float* d) {
+  const gptr q = p + off * 4u;
+  if (FULL || off + R <= left) {
+#pragma unroll
+    for (int k = 0; k < R; k += 4) {
+      const f32x4 a = ld_nt<f32x4>(q + 4 * k);
+      d[k] = a.x; d[k + 1] = a.y; d[k + 2] = a.z; d[k + 3] = a.w;
+    }
     return;
   }
-  for (int j = 0; j < 8; ++j) d[j] = e + j < n ? ((const GLOBAL float*)q)[j] : 0.0f;
+  for (int j = 0; j < R; ++j) d[j] = off + j < left ? ((const GLOBAL float*)q)[j] : 0.0f;
 }
 
-__device__ __forceinline__ void st8_f32(void* p, int64_t e, int64_t n, const float* s) {
-  float* q = (float*)p + e;
-  if (e + 8 <= n) {
-    st_nt(q, f32x4{s[0], s[1], s[2], s[3]});
-    st_nt(q + 4, f32x4{s[4], s[5], s[6], s[7]});
+template <int R, bool FULL>
+__device__ __forceinline__ void st_f32(gptr p, uint32_t off, uint32_t left, const float* s) {
+  const gptr q = p + off * 4u;
+  if (FULL || off + R <= left) {
+#pragma unroll
+    for (int k = 0; k < R; k += 4) st_nt(q + 4 * k, f32x4{s[k], s[k + 1], s[k + 2], s[k + 3]});
     return;
   }
-  for (int j = 0; j < 8; ++j)
-    if (e + j < n) ((GLOBAL float*)q)[j] = s[j];
+  for (int j = 0; j < R; ++j)
+    if (off + j < left) ((GLOBAL float*)q)[j] = s[j];
 }
 
-__device__ __forceinline__ void ld8_u16(const void* p, int64_t e, int64_t n, uint32_t* d) {
-  const uint16_t* q = (const uint16_t*)p + e;
-  if (e + 8 <= n) {
-    const u32x4 a = ld_nt<u32x4>(q);
-    d[0] = a.x; d[1] = a.y; d[2] = a.z; d[3] = a.w;
+template <int R, bool FULL>
+__device__ __forceinline__ void ld_u16(gptr p, uint32_t off, uint32_t left, uint32_t* d) {
+  const gptr q = p + off * 2u;
+  if (FULL || off + R <= left) {
+    if (R == 8) {
+      const u32x4 a = ld_nt<u32x4>(q);
+      d[0] = a.x; d[1] = a.y; d[2] = a.z; d[3] = a.w;
+    } else {
+      const u32x2 a = ld_nt<u32x2>(q);
+      d[0] = a.x; d[1] = a.y;
+    }
     return;
   }
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t lo = e + 2 * j < n ? ((const GLOBAL uint16_t*)q)[2 * j] : 0u;
-    const uint32_t hi = e + 2 * j + 1 < n ? ((const GLOBAL uint16_t*)q)[2 * j + 1] : 0u;
+  for (int j = 0; j < R / 2; ++j) {
+    const uint32_t lo = off + 2 * j < left ? ((const GLOBAL uint16_t*)q)[2 * j] : 0u;
+    const uint32_t hi = off + 2 * j + 1 < left ? ((const GLOBAL uint16_t*)q)[2 * j + 1] : 0u;
     d[j] = lo | (hi << 16);
   }
 }
 
-__device__ __forceinline__ void st8_u16(void* p, int64_t e, int64_t n, const uint32_t* s) {
-  uint16_t* q = (uint16_t*)p + e;
-  if (e + 8 <= n) {
-    st_nt(q, u32x4{s[0], s[1], s[2], s[3]});
+template <int R, bool FULL>
+__device__ __forceinline__ void st_u16(gptr p, uint32_t off, uint32_t left, const uint32_t* s) {
+  const gptr q = p + off * 2u;
+  if (FULL || off + R <= left) {
+    if (R == 8)
+      st_nt(q, u32x4{s[0], s[1], s[2], s[3]});
+    else
+      st_nt(q, u32x2{s[0], s[1]});
     return;
   }
-  for (int j = 0; j < 8; ++j)
-    if (e + j < n) ((GLOBAL uint16_t*)q)[j] = (uint16_t)(s[j >> 1] >> (16 * (j & 1)));
+  for (int j = 0; j < R; ++j)
+    if (off + j < left) ((GLOBAL uint16_t*)q)[j] = (uint16_t)(s[j >> 1] >> (16 * (j & 1)));
 }
 
-__device__ __forceinline__ void ld8_u8(const void* p, int64_t e, int64_t n, uint32_t* d) {
-  const uint8_t* q = (const uint8_t*)p + e;
-  if (e + 8 <= n) {
-    const u32x2 a = ld_nt<u32x2>(q);
-    d[0] = a.x; d[1] = a.y;
+template <int R, bool FULL>
+__device__ __forceinline__ void ld_u8(gptr p, uint32_t off, uint32_t left, uint32_t* d) {
+  const gptr q = p + off;
+  if (FULL || off + R <= left) {
+    if (R == 8) {
+      const u32x2 a = ld_nt<u32x2>(q);
+      d[0] = a.x; d[1] = a.y;
+    } else {
+      d[0] = ld_nt<uint32_t>(q);
+    }
     return;
   }
-  d[0] = d[1] = 0u;
-  for (int j = 0; j < 8; ++j)
-    if (e + j < n) d[j >> 2] |= (uint32_t)((const GLOBAL uint8_t*)q)[j] << (8 * (j & 3));
+#pragma unroll
+  for (int k = 0; k < R / 4; ++k) d[k] = 0u;
+  for (int j = 0; j < R; ++j)
+    if (off + j < left) d[j >> 2] |= (uint32_t)((const GLOBAL uint8_t*)q)[j] << (8 * (j & 3));
 }
 
-__device__ __forceinline__ void st8_u8(void* p, int64_t e, int64_t n, const uint32_t* s) {
-  uint8_t* q = (uint8_t*)p + e;
-  if (e + 8 <= n) {
-    st_nt(q, u32x2{s[0], s[1]});
+template <int R, bool FULL>
+__device__ __forceinline__ void st_u8(gptr p, uint32_t off, uint32_t left, const uint32_t* s) {
+  const gptr q = p + off;
+  if (FULL || off + R <= left) {
+    if (R == 8)
+      st_nt(q, u32x2{s[0], s[1]});
+    else
+      st_nt(q, s[0]);
     return;
   }
-  for (int j = 0; j < 8; ++j)
-    if (e + j < n) ((GLOBAL uint8_t*)q)[j] = (uint8_t)(s[j >> 2] >> (8 * (j & 3)));
+  for (int j = 0; j < R; ++j)
+    if (off + j < left) ((GLOBAL uint8_t*)q)[j] = (uint8_t)(s[j >> 2] >> (8 * (j & 3)));
 }
 
 // Eight 16-bit floats (bf16, or fp16 if `half`) as fp32.
-__device__ __forceinline__ void unpack8(const uint32_t* w, bool half, float* d) {
+template <int N>
+__device__ __forceinline__ void unpack(const uint32_t* w, bool half, float* d) {
   if (half) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < N / 2; ++j) {
       const f16x2 h = __builtin_bit_cast(f16x2, w[j]);
       d[2 * j] = (float)h.x;
       d[2 * j + 1] = (float)h.y;
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < N / 2; ++j) {
       d[2 * j] = bf16_lo(w[j]);
       d[2 * j + 1] = bf16_hi(w[j]);
     }
@@ -116,51 +165,17 @@ __device__ __forceinline__ void unpack8(const uint32_t* w, bool half, float* d) 
 }
 
 // Eight fp32 values rounded to nearest even as bf16, or fp16 if `half`.
-__device__ __forceinline__ void pack8(const float* s, bool half, uint32_t* w) {
+template <int N>
+__device__ __forceinline__ void pack(const float* s, bool half, uint32_t* w) {
   if (half) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < N / 2; ++j)
       w[j] = __builtin_bit_cast(uint32_t, f16x2{(_Float16)s[2 * j], (_Float16)s[2 * j + 1]});
   } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < N / 2; ++j)
       w[j] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)s[2 * j], (__bf16)s[2 * j + 1]});
   }
-}
-
-// ---------------------------------------------------------------------------
-// e4m3 moments. The block's scale is the smallest power of two s >= 2^-126
-// with max <= 448 s (448 = 1.75 * 2^8 is the largest e4m3 value): adding the
-// mantissa bits above 1.75 carries into the exponent exactly when the
-// mantissa is larger than 1.75. Scaling by a power of two is exact, so a code
-// is one rounding of the moment, and the hardware conversion makes it.
-// ---------------------------------------------------------------------------
-__device__ __forceinline__ void e4m3_scale(uint32_t max_bits, float& s, float& inv) {
-  const int e = __builtin_elementwise_max((int)((max_bits + 0x1FFFFFu) >> 23) - 8, 1);
-  s = __uint_as_float((uint32_t)e << 23);
-  inv = __uint_as_float((uint32_t)(254 - e) << 23);
-}
-
-__device__ __forceinline__ void e4m3_unpack4(uint32_t c, float* d) {
-  const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, true);
-  d[0] = a.x; d[1] = a.y; d[2] = b.x; d[3] = b.y;
-}
-
-__device__ __forceinline__ uint32_t e4m3_pack4(const float* y) {
-  const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
-  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], lo, true);
-}
-
-constexpr float kMinCode = 0x1p-9f;   // smallest e4m3 value above zero
-
-// y in [0, 448] cut to e4m3 after adding 16 random bits below its last kept
-// place: values of 2^-6 and more keep 3 mantissa bits; smaller ones keep the
-// places of 2^-6, which adding 2^-6 lines up.
-__device__ __forceinline__ float e4m3_stochastic(float y, uint32_t r16) {
-  const bool small = y < 0x1p-6f;
-  const float z = small ? y + 0x1p-6f : y;
-  const float q = __uint_as_float((__float_as_uint(z) + (r16 << 4)) & 0xFFF00000u);
-  return small ? q - 0x1p-6f : q;
 }
 
 // ---------------------------------------------------------------------------
@@ -169,142 +184,263 @@ __device__ __forceinline__ float e4m3_stochastic(float y, uint32_t r16) {
 
 constexpr uint32_t kVStream = 0x80000000u;   // second moment's random streams: list index + 2^31
 
-template <int KIND, bool SR>
-__device__ __forceinline__ void adamw_item(const AwRec& T, int64_t elem0, const AwScalars& c, float mul, const AwRun& run) {
+// Lane layout of a kind: fp32 arrays (moments, or the weights beside 8-bit
+// moments) are read best by runs of 4, bf16 weights with 8-bit moments by runs
+// of 8. Layer of 202M parameters, fp32 weights, bf16 gradients and copy: fp32
+// moments 963 us by 4, 1130 us by 8; e4m3 moments 578 us by 4, 632 us by 8.
+// bf16 weights with residual and e4m3 moments, 514M: 1131 us by 8, 1146 us by 4.
+constexpr bool quad_lanes(int kind) { return !(kind & kAwE4m3) || !(kind & kAwBf16); }
+
+// Waves a SIMD runs at once, held down on purpose: with fewer waves in flight
+// the streams' reads and writes meet less in HBM, and as long as the
+// arithmetic stays hidden that is worth more than latency. The 202M layer with
+// fp32 moments took 1020, 890, 920, 946, 953 and 995 us at 1, 2, 3, 4, 5 and 8
+// waves; 514M bf16 weights with e4m3 moments 1459, 1188, 1138, 1150 and 1180 us at
+// 2, 3, 4, 5 and 8. Where weights are rounded stochastically beside e4m3
+// moments, integer work for the random bits fills the vector units and wants
+// all waves (42M parameters: 80 us at 7 and more, 83 at 5, 87 at 4).
+constexpr int waves_of(int kind, int split) {
+  const bool sr = (kind & kAwBf16) && split == PS_SPLIT_STOCHASTIC;
+  return kind & kAwE4m3 ? (sr ? 7 : 4) : (sr ? 3 : 2);
+}
+
+// Each XCD takes runs of this many consecutive items. At the waves above runs
+// of 256 to 1024 measured alike, 64 and 2048 2-4% slower.
+constexpr uint32_t kAwXcdChunk = 512;
+
+// A lane's 8 elements of a work item. QUAD: two runs of 4, one in each block,
+// so that 64 lanes read 1 KiB of fp32 in one contiguous access. Else one run of
+// 8, 32 lanes to a block. p0 is the item's first element of an array.
+template <bool QUAD, bool FULL>
+struct Lane {
+  static constexpr int R = QUAD ? 4 : 8;
+  static constexpr int kBlocks = QUAD ? 2 : 1;
+  static constexpr int block_of(int j) { return QUAD ? j / 4 : 0; }
+  uint32_t off, left;
+  __device__ __forceinline__ Lane(uint32_t left_) : off(threadIdx.x * R), left(left_) {}
+#define PS_EACH(CALL, D)                                                                 \
+  {                                                                                      \
+    CALL<R, FULL>(p0, off, left, d);                                                     \
+    if (QUAD) CALL<R, FULL>(p0, off + 256, left, d + D);                                 \
+  }
+  __device__ __forceinline__ void load_f32(gptr p0, float* d) const PS_EACH(ld_f32, 4)
+  __device__ __forceinline__ void store_f32(gptr p0, const float* d) const PS_EACH(st_f32, 4)
+  __device__ __forceinline__ void load_u16(gptr p0, uint32_t* d) const PS_EACH(ld_u16, 2)
+  __device__ __forceinline__ void store_u16(gptr p0, const uint32_t* d) const PS_EACH(st_u16, 2)
+  __device__ __forceinline__ void load_u8(gptr p0, uint32_t* d) const PS_EACH(ld_u8, 1)
+  __device__ __forceinline__ void store_u8(gptr p0, const uint32_t* d) const PS_EACH(st_u8, 1)
+#undef PS_EACH
+  // Block b of the lane: its index in the item, and whether it has elements.
+  __device__ __forceinline__ uint32_t block(int b) const { return QUAD ? (uint32_t)b : threadIdx.x >> 5; }
+  __device__ __forceinline__ bool exists(int b) const { return FULL || block(b) * kBlock < left; }
+  __device__ __forceinline__ uint32_t block_max(uint32_t x) const { return QUAD ? wave_max_u32(x) : row32_max_u32(x); }
+  __device__ __forceinline__ bool leads() const { return (threadIdx.x & (QUAD ? 63 : 31)) == 0; }
+};
+
+// Random bits of a lane's two quads: outputs e/4 of the stream (dev_common.h).
+// The stream's start and the item's part of the counter are wave-uniform.
+template <bool QUAD>
+__device__ __forceinline__ void random_quads(const AwScalars& c, uint32_t tid, int64_t elem0, uint64_t* z) {
+  const uint64_t base = sr_stream(c.sr_seed, c.sr_step, tid) + ((uint64_t)(elem0 >> 2) + 1) * kGolden;
+  const uint64_t x = base + (uint64_t)(threadIdx.x * (QUAD ? 1 : 2)) * kGolden;
+  z[0] = splitmix64_mix(x);
+  z[1] = splitmix64_mix(x + (QUAD ? 64 : 1) * kGolden);
+}
+__device__ __forceinline__ uint32_t random16(const uint64_t* z, int j) {
+  return (uint32_t)(z[j >> 2] >> (16 * (j & 3))) & 0xFFFFu;
+}
+
+// The item's elements elem0 .. elem0 + left - 1 of the tensor, left <= 512.
+template <int KIND, int SPLIT, bool NADAM, bool FULL>
+__device__ __forceinline__ void adamw_item(const AwRec& T, int64_t elem0, uint32_t left, const AwScalars& c, float mul,
+                                           const AwRun& run) {
   constexpr bool BF = KIND & kAwBf16, G32 = KIND & kAwGrad32, E8 = KIND & kAwE4m3, CP = KIND & kAwCopy;
-  const int lane = (int)threadIdx.x;
-  const int64_t n = T.n;
-  const int64_t e = elem0 + lane * 8;
-  const int64_t blk = (elem0 >> 8) + (lane >> 5);
+  constexpr bool SR = BF && SPLIT == PS_SPLIT_STOCHASTIC;
+  constexpr bool QUAD = quad_lanes(KIND);
+  using L = Lane<QUAD, FULL>;
+  const L at(left);
+  const gptr wp = global((char*)T.w) + elem0 * (BF ? 2 : 4);
+  const gptr lp = global((char*)T.lo) + elem0 * 2;
+  const gptr gp = global((const char*)T.g) + elem0 * (G32 ? 4 : 2);
+  const gptr mp = global((char*)T.m) + elem0 * (E8 ? 1 : 4);
+  const gptr vp = global((char*)T.v) + elem0 * (E8 ? 1 : 4);
+  GLOBAL float* const msp = (GLOBAL float*)T.ms + (elem0 >> 8);
+  GLOBAL float* const vsp = (GLOBAL float*)T.vs + (elem0 >> 8);
 
   float g[8], w[8], m[8], v[8];
   uint32_t gw[4], hw[4], lw[4], mc[2], vc[2];
-  float ms = 0.0f, vs = 0.0f;
+  float ms[2] = {0.0f, 0.0f}, vs[2] = {0.0f, 0.0f};
   if (G32)
-    ld8_f32(T.g, e, n, g);
+    at.load_f32(gp, g);
   else
-    ld8_u16(T.g, e, n, gw);
+    at.load_u16(gp, gw);
   if (E8) {
-    ld8_u8(T.m, e, n, mc);
-    ld8_u8(T.v, e, n, vc);
-    if (blk * kBlock < n) {
-      ms = ((const GLOBAL float*)T.ms)[blk];
-      vs = ((const GLOBAL float*)T.vs)[blk];
-    }
-  } else {
-    ld8_f32(T.m, e, n, m);
-    ld8_f32(T.v, e, n, v);
-  }
-  if (BF) {
-    ld8_u16(T.w, e, n, hw);
-    if (!SR) ld8_u16(T.lo, e, n, lw);
-  } else {
-    ld8_f32(T.w, e, n, w);
-  }
-
-  if (!G32) unpack8(gw, T.gtype == PS_TYPE_F16, g);
-  if (E8) {
-    e4m3_unpack4(mc[0], m);
-    e4m3_unpack4(mc[1], m + 4);
-    e4m3_unpack4(vc[0], v);
-    e4m3_unpack4(vc[1], v + 4);
+    at.load_u8(mp, mc);
+    at.load_u8(vp, vc);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      m[j] = m[j] * ms;
-      const float r = v[j] * vs;
-      v[j] = r * r;
-    }
-  }
-  if (BF) {
-    const uint32_t carry = run.nearest ? 0x8000u : 0u;   // nearest-away split: the residual's top bit was carried into hi
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (SR) {
-        w[j] = (j & 1) ? bf16_hi(hw[j >> 1]) : bf16_lo(hw[j >> 1]);
-      } else {
-        const uint32_t b = perm(hw[j >> 1], lw[j >> 1], (j & 1) ? kSelHiHalves : kSelLoHalves);
-        w[j] = __uint_as_float(b - ((b & carry) << 1));
+    for (int b = 0; b < L::kBlocks; ++b)
+      if (at.exists(b)) {
+        ms[b] = msp[at.block(b)];
+        vs[b] = vsp[at.block(b)];
       }
+  } else {
+    at.load_f32(mp, m);
+    at.load_f32(vp, v);
+  }
+  if (BF) {
+    at.load_u16(wp, hw);
+    if (!SR) at.load_u16(lp, lw);
+  } else {
+    at.load_f32(wp, w);
+  }
+
+  if (!G32) unpack<8>(gw, T.gtype == PS_TYPE_F16, g);
+  if (E8) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      e4m3_unpack4(mc[q], m + 4 * q);
+      e4m3_unpack4(vc[q], v + 4 * q);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      m[j] = m[j] * ms[L::block_of(j)];
+      const float r0 = v[j] * vs[L::block_of(j)];
+      v[j] = r0 * r0;
     }
   }
 
-  float r[8];
-  uint32_t mx_m = 0u, mx_r = 0u;
+  // Moments, and what decides whether the fast square root and quotient hold
+  // for the whole wave: the least and largest v and |numerator| above zero.
+  uint32_t mx_v[2] = {0u, 0u}, least_v = ~0u, least_a = ~0u;
+  float mx_m[2] = {0.0f, 0.0f}, mx_a = 0.0f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
+    const int b = L::block_of(j);
     const float gj = g[j] * mul;
     m[j] = c.B1 * m[j] + c.C1 * gj;
     v[j] = c.B2 * v[j] + c.C2 * (gj * gj);
-    r[j] = __builtin_sqrtf(v[j]);
-    const float d = r[j] * c.RS2 + c.EPS;
-    float u = run.nadam ? (c.AG * gj + c.AM * m[j]) / d : c.A * (m[j] / d);
-    u = u + c.CWD * w[j];
-    w[j] = w[j] - u;
-    if (E8) {
-      mx_m = __builtin_elementwise_max(mx_m, __float_as_uint(m[j]) & 0x7FFFFFFFu);
-      mx_r = __builtin_elementwise_max(mx_r, __float_as_uint(r[j]));
+    mx_v[b] = __builtin_elementwise_max(mx_v[b], __float_as_uint(v[j]));
+    least_v = __builtin_elementwise_min(least_v, __float_as_uint(v[j]) - 1u);
+    if (E8 || !NADAM) mx_m[b] = __builtin_fmaxf(mx_m[b], __builtin_fabsf(m[j]));
+    if (NADAM) {
+      g[j] = c.AG * gj + c.AM * m[j];   // the numerator
+      mx_a = __builtin_fmaxf(mx_a, __builtin_fabsf(g[j]));
+    }
+    least_a = __builtin_elementwise_min(least_a, (__float_as_uint(NADAM ? g[j] : m[j]) << 1) - 1u);
+  }
+  if (!NADAM) mx_a = __builtin_fmaxf(mx_m[0], mx_m[1]);
+  // v: 0 or in [2^-96, 2^60); a: 0 or |a| in [2^-60, 2^60). With EPS in
+  // [2^-60, 2^58] and RS2 <= 2^28 (run.fast) d stays in [2^-60, 2^60].
+  const bool out = least_v < ((127u - 96u) << 23) - 1u || least_a < ((127u - 60u) << 24) - 1u ||
+                   __builtin_elementwise_max(mx_v[0], mx_v[1]) >= ((127u + 60u) << 23) || !(mx_a < 0x1p60f);
+  const bool fast = run.fast && __builtin_amdgcn_ballot_w64(out) == 0;
+  if (BF) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      w[j] = SR ? ((j & 1) ? bf16_hi(hw[j >> 1]) : bf16_lo(hw[j >> 1]))
+                : __uint_as_float(join_pair_elem<SPLIT>(hw[j >> 1], lw[j >> 1], j & 1));
+  }
+  float vv[8];
+  if (!E8) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) vv[j] = v[j];
+  }
+  if (fast) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[j] = sqrt_fast(v[j]);
+      const float q = div_fast(NADAM ? g[j] : m[j], v[j] * c.RS2 + c.EPS);
+      w[j] = w[j] - ((NADAM ? q : c.A * q) + c.CWD * w[j]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      __builtin_amdgcn_sched_barrier(0);   // one element at a time: the rare path needs no registers of its own
+      v[j] = __builtin_sqrtf(v[j]);
+      const float q = (NADAM ? g[j] : m[j]) / (v[j] * c.RS2 + c.EPS);
+      w[j] = w[j] - ((NADAM ? q : c.A * q) + c.CWD * w[j]);
     }
   }
 
   if (BF) {
     uint32_t oh[4], ol[4];
     if (SR) {
-      uint64_t rnd[2];
-      sr_bits8(sr_stream(c.sr_seed, c.sr_step, T.tid), e, rnd);
+      uint64_t z[2];
+      random_quads<QUAD>(c, T.tid, elem0, z);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t b = (uint32_t)(rnd[q >> 1] >> (32 * (q & 1)));
-        oh[q] = sr_pair(__float_as_uint(w[2 * q]), __float_as_uint(w[2 * q + 1]), b & 0xFFFFu, b >> 16);
-      }
+      for (int q = 0; q < 4; ++q)
+        oh[q] = sr_pair(__float_as_uint(w[2 * q]), __float_as_uint(w[2 * q + 1]), random16(z, 2 * q), random16(z, 2 * q + 1));
     } else {
-      const uint32_t carry = run.nearest ? 0x8000u : 0u;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t a = __float_as_uint(w[2 * q]), b = __float_as_uint(w[2 * q + 1]);
-        ol[q] = perm(b, a, kSelLoHalves);
-        oh[q] = perm(b + carry, a + carry, kSelHiHalves);
-      }
-      st8_u16(T.lo, e, n, ol);
+      for (int q = 0; q < 4; ++q)
+        split_pair<SPLIT>(__float_as_uint(w[2 * q]), __float_as_uint(w[2 * q + 1]), oh[q], ol[q]);
+      at.store_u16(lp, ol);
     }
-    st8_u16(T.w, e, n, oh);
+    at.store_u16(wp, oh);
   } else {
-    st8_f32(T.w, e, n, w);
+    at.store_f32(wp, w);
     if (CP) {
       uint32_t oc[4];
-      pack8(w, T.ctype == PS_TYPE_F16, oc);
-      st8_u16(T.copy, e, n, oc);
+      pack<8>(w, T.ctype == PS_TYPE_F16, oc);
+      at.store_u16(global((char*)T.copy) + elem0 * 2, oc);
     }
   }
-
   if (!E8) {
-    st8_f32(T.m, e, n, m);
-    st8_f32(T.v, e, n, v);
+    at.store_f32(mp, m);
+    at.store_f32(vp, vv);
     return;
   }
-  float sm, inv_m, sv, inv_v;
-  e4m3_scale(row32_max_u32(mx_m), sm, inv_m);
-  e4m3_scale(row32_max_u32(mx_r), sv, inv_v);
+
+  // Block scales: the largest |m|, and the root of the largest v, which is the
+  // largest root.
+  float sm[2], sv[2], inv_m[2], inv_v[2];
+#pragma unroll
+  for (int b = 0; b < L::kBlocks; ++b) {
+    e4m3_scale(at.block_max(__float_as_uint(mx_m[b])), sm[b], inv_m[b]);
+    const float top = __uint_as_float(at.block_max(mx_v[b]));
+    e4m3_scale(__float_as_uint(fast ? sqrt_fast(top) : __builtin_sqrtf(top)), sv[b], inv_v[b]);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m[j] = m[j] * inv_m[L::block_of(j)];
+  const uint32_t om[2] = {e4m3_pack4(m), e4m3_pack4(m + 4)};
+  at.store_u8(mp, om);
   float y[8];
-  uint64_t rnd[2] = {0u, 0u};
-  if (run.round_sr) sr_bits8(sr_stream(c.sr_seed, c.sr_step, T.tid | kVStream), e, rnd);
+  float least_y = 448.0f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    m[j] = m[j] * inv_m;
-    y[j] = r[j] * inv_v;
-    if (run.round_sr) y[j] = e4m3_stochastic(y[j], (uint32_t)(rnd[j >> 2] >> (16 * (j & 3))) & 0xFFFFu);
-    y[j] = r[j] > 0.0f ? __builtin_fmaxf(y[j], kMinCode) : y[j];
+    y[j] = v[j] * inv_v[L::block_of(j)];
+    least_y = __builtin_fminf(least_y, y[j]);
   }
-  const uint32_t om[2] = {e4m3_pack4(m), e4m3_pack4(m + 4)}, ov[2] = {e4m3_pack4(y), e4m3_pack4(y + 4)};
-  st8_u8(T.m, e, n, om);
-  st8_u8(T.v, e, n, ov);
-  if ((lane & 31) == 0 && blk * kBlock < n) {
-    ((GLOBAL float*)T.ms)[blk] = sm;
-    ((GLOBAL float*)T.vs)[blk] = sv;
+  // Values below 2^-6, rare, take the general form.
+  const bool small = __builtin_amdgcn_ballot_w64(least_y < 0x1p-6f) != 0;
+  if (run.round_sr) {
+    uint64_t z[2];
+    random_quads<QUAD>(c, T.tid | kVStream, elem0, z);
+    if (small) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = e4m3_stochastic(y[j], random16(z, j));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = e4m3_cut(y[j], random16(z, j));
+    }
   }
+  if (small) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = v[j] > 0.0f ? __builtin_fmaxf(y[j], kMinCode) : y[j];
+  }
+  const uint32_t ov[2] = {e4m3_pack4(y), e4m3_pack4(y + 4)};
+  at.store_u8(vp, ov);
+#pragma unroll
+  for (int b = 0; b < L::kBlocks; ++b)
+    if (at.leads() && at.exists(b)) {
+      msp[at.block(b)] = sm[b];
+      vsp[at.block(b)] = sv[b];
+    }
 }
 
 // Index of the record that owns work item `item` (prefix ends, wave-uniform).
-__device__ __forceinline__ int find(const uint32_t* end, int n, uint32_t item) {
+__device__ __forceinline__ int find(const uint32_t* ends, int n, uint32_t item) {
+  const CONSTANT uint32_t* end = (const CONSTANT uint32_t*)ends;
   int lo = 0, hi = n - 1;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
@@ -316,20 +452,27 @@ __device__ __forceinline__ int find(const uint32_t* end, int n, uint32_t item) {
   return lo;
 }
 
-template <int KIND, bool SR>
-__global__ __launch_bounds__(64) void k_adamw_step(AwTable t, AwGroups sc, AwRun run) {
-  const uint32_t item = xcd_item<>(blockIdx.x, gridDim.x);
+template <int KIND, int SPLIT, bool NADAM>
+__global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(waves_of(KIND, SPLIT), waves_of(KIND, SPLIT))))
+ void k_adamw_step(AwTable t, AwGroups sc, AwRun run) {
+  const uint32_t item = xcd_item<kAwXcdChunk>(blockIdx.x, gridDim.x);
   const int i = find(t.item_end, t.n, item);
-  const AwRec& T = t.recs[i];
+  const AwRec T = ld_const(t.recs + i);
   if (!T.g) return;
   float mul = 1.0f;
   if (run.clipped) {
-    if (run.ctl->skip) return;
-    mul = run.ctl->grad_mul;
+    const CONSTANT ps_adamw_control* ctl = (const CONSTANT ps_adamw_control*)run.ctl;
+    if (ctl->skip) return;
+    mul = ctl->grad_mul;
   }
   const uint32_t begin = i ? t.item_end[i - 1] : 0u;
-  const AwScalars c = run.dev_sc ? run.dev_sc[T.group] : sc.g[T.group];
-  adamw_item<KIND, SR>(T, (int64_t)(item - begin) * kAwItemElems, c, mul, run);
+  const AwScalars c = run.dev_sc ? ld_const(run.dev_sc + T.group) : sc.g[T.group];
+  const int64_t elem0 = (int64_t)(item - begin) * kAwItemElems;
+  const int64_t left = T.n - elem0;
+  if (left >= kAwItemElems)
+    adamw_item<KIND, SPLIT, NADAM, true>(T, elem0, kAwItemElems, c, mul, run);
+  else
+    adamw_item<KIND, SPLIT, NADAM, false>(T, elem0, (uint32_t)left, c, mul, run);
 }
 
 // Step counted on the device: one lane per group computes the update's scalars
@@ -380,38 +523,71 @@ __device__ __forceinline__ double block_sum(double x) {
   return s;
 }
 
+// Adds the squares of eight gradients to four sums.
+__device__ __forceinline__ void add_squares(const float* g, double* s) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s[j & 3] = __builtin_fma((double)g[j], (double)g[j], s[j & 3]);
+}
+
+// A whole chunk's squares: every load is under way before the first is used.
+__device__ __forceinline__ void chunk_squares(gptr p, bool f32, bool half, double* s) {
+  constexpr int kLoads = kNormChunk / (8 * kNormThreads);   // of 8 elements
+  if (f32) {
+    f32x4 x[2 * kLoads];
+#pragma unroll
+    for (int k = 0; k < 2 * kLoads; ++k) x[k] = ld_nt<f32x4>(p + (threadIdx.x * 16u + k * (16u * kNormThreads)));
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) {
+      const float g[8] = {x[2 * k].x,     x[2 * k].y,     x[2 * k].z,     x[2 * k].w,
+                          x[2 * k + 1].x, x[2 * k + 1].y, x[2 * k + 1].z, x[2 * k + 1].w};
+      add_squares(g, s);
+    }
+  } else {
+    u32x4 x[kLoads];
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) x[k] = ld_nt<u32x4>(p + (threadIdx.x * 16u + k * (16u * kNormThreads)));
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) {
+      const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+      float g[8];
+      unpack<8>(w, half, g);
+      add_squares(g, s);
+    }
+  }
+}
+
 // Workgroup b sums the squares of the chunks b, b + gridDim.x, ... in double:
 // no finite gradient's square overflows or vanishes there, and a sum that is
 // not finite says that a gradient is not.
 __global__ __launch_bounds__(kNormThreads) void k_grad_sumsq(AwNormTable t, double* partials) {
-  double s0 = 0.0, s1 = 0.0;
+  double s[4] = {0.0, 0.0, 0.0, 0.0};
   for (uint32_t chunk = blockIdx.x; chunk < t.chunks; chunk += gridDim.x) {
     const int i = find(t.chunk_end, t.n, chunk);
-    const AwNormRec& T = t.recs[i];
+    const AwNormRec T = ld_const(t.recs + i);
     if (!T.g) continue;
-    const uint32_t begin = i ? t.chunk_end[i - 1] : 0u;
-    const int64_t e0 = (int64_t)(chunk - begin) * kNormChunk + threadIdx.x * 8;
-#pragma unroll
-    for (int k = 0; k < kNormChunk / (8 * kNormThreads); ++k) {
-      const int64_t e = e0 + k * (8 * kNormThreads);
-      if (e >= T.n) break;
+    const uint32_t begin = i ? ((const CONSTANT uint32_t*)t.chunk_end)[i - 1] : 0u;
+    const int64_t e0 = (int64_t)(chunk - begin) * kNormChunk;
+    const bool f32 = T.gtype == PS_TYPE_F32, half = T.gtype == PS_TYPE_F16;
+    const gptr p = global((const char*)T.g) + e0 * (f32 ? 4 : 2);
+    if (T.n - e0 >= kNormChunk) {
+      chunk_squares(p, f32, half, s);
+      continue;
+    }
+    const uint32_t left = (uint32_t)(T.n - e0);
+    for (uint32_t off = threadIdx.x * 8; off < left; off += 8 * kNormThreads) {
       float g[8];
-      if (T.gtype == PS_TYPE_F32) {
-        ld8_f32(T.g, e, T.n, g);
+      if (f32) {
+        ld_f32<8, false>(p, off, left, g);
       } else {
         uint32_t w[4];
-        ld8_u16(T.g, e, T.n, w);
-        unpack8(w, T.gtype == PS_TYPE_F16, g);
+        ld_u16<8, false>(p, off, left, w);
+        unpack<8>(w, half, g);
       }
-#pragma unroll
-      for (int j = 0; j < 8; j += 2) {
-        s0 = __builtin_fma((double)g[j], (double)g[j], s0);
-        s1 = __builtin_fma((double)g[j + 1], (double)g[j + 1], s1);
-      }
+      add_squares(g, s);
     }
   }
-  const double s = block_sum(s0 + s1);
-  if (threadIdx.x == 0) partials[blockIdx.x] = s;
+  const double sum = block_sum((s[0] + s[1]) + (s[2] + s[3]));
+  if (threadIdx.x == 0) partials[blockIdx.x] = sum;
 }
 
 __global__ __launch_bounds__(kNormThreads) void k_grad_norm(const double* partials, uint32_t n, ps_adamw_control* ctl,
@@ -443,70 +619,131 @@ __global__ __launch_bounds__(64) void k_set_grads(AwRec* recs, AwNormRec* nrecs,
 }
 
 // ---------------------------------------------------------------------------
-// e4m3 codec: one wave per 512 elements, laid out as the step's items
+// e4m3 codec, on the step's items and its lanes by runs of 4. Bound by HBM.
 // ---------------------------------------------------------------------------
-constexpr int kCodecThreads = 256;
-constexpr int kCodecElems = kCodecThreads * 8;
 
-template <int KIND>
-__global__ __launch_bounds__(kCodecThreads) void k_encode_fp8(const float* __restrict__ x, uint8_t* __restrict__ code,
-                                                              float* __restrict__ scale, int64_t n) {
-  const int64_t e = (int64_t)blockIdx.x * kCodecElems + threadIdx.x * 8;
-  float y[8];
-  ld8_f32(x, e, n, y);
-  uint32_t mx = 0u;
+// The encoder's wave takes this many items: 150M second moments 124 us with one,
+// 116 us with two (6.5 TB/s).
+constexpr int kEncodeItems = 2;
+
+// REP consecutive items, every load under way before the first use. The least
+// value above zero decides for the wave whether the fast root holds.
+template <int KIND, int REP, bool FULL>
+__device__ __forceinline__ void encode_items(gptr x, gptr code, GLOBAL float* scale, uint32_t left) {
+  using L = Lane<true, FULL>;
+  float y[REP][8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if (KIND == PS_MOMENT_UNSIGNED) y[j] = __builtin_sqrtf(y[j]);
-    mx = __builtin_elementwise_max(mx, __float_as_uint(y[j]) & 0x7FFFFFFFu);
-  }
-  float s, inv;
-  e4m3_scale(row32_max_u32(mx), s, inv);
+  for (int i = 0; i < REP; ++i) L(left).load_f32(x + i * (kAwItemElems * 4), y[i]);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float q = y[j] * inv;
-    y[j] = KIND == PS_MOMENT_UNSIGNED && y[j] > 0.0f ? __builtin_fmaxf(q, kMinCode) : q;
+  for (int i = 0; i < REP; ++i) {
+    const L at(left);
+    float* const v = y[i];
+    uint32_t mx[2] = {0u, 0u};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) mx[j / 4] = __builtin_elementwise_max(mx[j / 4], __float_as_uint(v[j]) & 0x7FFFFFFFu);
+    float s[2], inv[2];
+    float top[2] = {__uint_as_float(at.block_max(mx[0])), __uint_as_float(at.block_max(mx[1]))};
+    if (KIND == PS_MOMENT_UNSIGNED) {
+      uint32_t least = ~0u;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) least = __builtin_elementwise_min(least, __float_as_uint(v[j]) - 1u);
+      if (__builtin_amdgcn_ballot_w64(least < ((127u - 96u) << 23) - 1u) == 0) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = sqrt_fast(v[j]);
+        top[0] = sqrt_fast(top[0]);                     // the largest root
+        top[1] = sqrt_fast(top[1]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = __builtin_sqrtf(v[j]);
+        top[0] = __builtin_sqrtf(top[0]);
+        top[1] = __builtin_sqrtf(top[1]);
+      }
+    }
+    e4m3_scale(__float_as_uint(top[0]), s[0], inv[0]);
+    e4m3_scale(__float_as_uint(top[1]), s[1], inv[1]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float q = v[j] * inv[j / 4];
+      v[j] = KIND == PS_MOMENT_UNSIGNED && v[j] > 0.0f ? __builtin_fmaxf(q, kMinCode) : q;
+    }
+    const uint32_t c[2] = {e4m3_pack4(v), e4m3_pack4(v + 4)};
+    at.store_u8(code + i * kAwItemElems, c);
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+      if (at.leads() && at.exists(b)) scale[2 * i + b] = s[b];
   }
-  const uint32_t c[2] = {e4m3_pack4(y), e4m3_pack4(y + 4)};
-  st8_u8(code, e, n, c);
-  if ((threadIdx.x & 31) == 0 && e < n) ((GLOBAL float*)scale)[e >> 8] = s;
 }
 
 template <int KIND>
-__global__ __launch_bounds__(kCodecThreads) void k_decode_fp8(const uint8_t* __restrict__ code,
-                                                              const float* __restrict__ scale, float* __restrict__ x,
-                                                              int64_t n) {
-  const int64_t e = (int64_t)blockIdx.x * kCodecElems + threadIdx.x * 8;
-  if (e >= n) return;
+__global__ __launch_bounds__(64) void k_encode_fp8(const float* x, uint8_t* code, float* scale, int64_t n) {
+  const int64_t e0 = (int64_t)xcd_item<kAwXcdChunk>(blockIdx.x, gridDim.x) * (kEncodeItems * kAwItemElems);
+  gptr xp = global((const char*)x) + e0 * 4, cp = global((char*)code) + e0;
+  GLOBAL float* sp = (GLOBAL float*)scale + (e0 >> 8);
+  if (n - e0 >= kEncodeItems * kAwItemElems) {
+    encode_items<KIND, kEncodeItems, true>(xp, cp, sp, kAwItemElems);
+    return;
+  }
+  for (int64_t left = n - e0; left > 0; left -= kAwItemElems) {
+    encode_items<KIND, 1, false>(xp, cp, sp, (uint32_t)(left < kAwItemElems ? left : kAwItemElems));
+    xp += kAwItemElems * 4;
+    cp += kAwItemElems;
+    sp += kAwItemElems / kBlock;
+  }
+}
+
+template <int KIND, bool FULL>
+__device__ __forceinline__ void decode_item(gptr code, const GLOBAL float* scale, gptr x, uint32_t left) {
+  using L = Lane<true, FULL>;
+  const L at(left);
   uint32_t c[2];
+  at.load_u8(code, c);
+  float s[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int b = 0; b < L::kBlocks; ++b)
+    if (at.exists(b)) s[b] = scale[at.block(b)];
   float y[8];
-  ld8_u8(code, e, n, c);
-  const float s = ((const GLOBAL float*)scale)[e >> 8];
   e4m3_unpack4(c[0], y);
   e4m3_unpack4(c[1], y + 4);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    y[j] = y[j] * s;
+    y[j] = y[j] * s[L::block_of(j)];
     if (KIND == PS_MOMENT_UNSIGNED) y[j] = y[j] * y[j];
   }
-  st8_f32(x, e, n, y);
+  at.store_f32(x, y);
 }
 
-template <int KIND, bool SR>
+template <int KIND>
+__global__ __launch_bounds__(64) void k_decode_fp8(const uint8_t* code, const float* scale, float* x, int64_t n) {
+  const int64_t e0 = (int64_t)xcd_item<kAwXcdChunk>(blockIdx.x, gridDim.x) * kAwItemElems;
+  const gptr xp = global((char*)x) + e0 * 4, cp = global((const char*)code) + e0;
+  const GLOBAL float* const sp = (const GLOBAL float*)scale + (e0 >> 8);
+  if (n - e0 >= kAwItemElems)
+    decode_item<KIND, true>(cp, sp, xp, kAwItemElems);
+  else
+    decode_item<KIND, false>(cp, sp, xp, (uint32_t)(n - e0));
+}
+
+template <int KIND, int SPLIT>
 ps_status launch_t(const AwTable& t, uint32_t items, const AwGroups& sc, const AwRun& run, hipStream_t s) {
-  hipLaunchKernelGGL((k_adamw_step<KIND, SR>), dim3(items), dim3(64), 0, s, t, sc, run);
+  if (run.nadam)
+    hipLaunchKernelGGL((k_adamw_step<KIND, SPLIT, true>), dim3(items), dim3(64), 0, s, t, sc, run);
+  else
+    hipLaunchKernelGGL((k_adamw_step<KIND, SPLIT, false>), dim3(items), dim3(64), 0, s, t, sc, run);
   return hip_check(hipGetLastError(), "k_adamw_step launch");
 }
 
 }  // namespace
 
-ps_status launch_adamw_step(int kind, bool sr, const AwTable& t, uint32_t items, const AwGroups& sc, const AwRun& run,
+ps_status launch_adamw_step(int kind, int split, const AwTable& t, uint32_t items, const AwGroups& sc, const AwRun& run,
                             hipStream_t s) {
   switch (kind) {
 #define PS_KIND(K) \
-  case K: return launch_t<K, false>(t, items, sc, run, s);
-#define PS_KIND_BF16(K) \
-  case K: return sr ? launch_t<K, true>(t, items, sc, run, s) : launch_t<K, false>(t, items, sc, run, s);
+  case K: return launch_t<K, PS_SPLIT_TRUNC>(t, items, sc, run, s);
+#define PS_KIND_BF16(K)                                                                          \
+  case K:                                                                                        \
+    return split == PS_SPLIT_STOCHASTIC     ? launch_t<K, PS_SPLIT_STOCHASTIC>(t, items, sc, run, s)   \
+           : split == PS_SPLIT_NEAREST_AWAY ? launch_t<K, PS_SPLIT_NEAREST_AWAY>(t, items, sc, run, s) \
+                                            : launch_t<K, PS_SPLIT_TRUNC>(t, items, sc, run, s);
     PS_KIND(0)
     PS_KIND(kAwGrad32)
     PS_KIND(kAwE4m3)
@@ -556,17 +793,17 @@ ps_status launch_set_grads(AwRec* recs, AwNormRec* nrecs, const uint32_t* slot, 
 
 // Codec launches cover at most kCodecMax elements each (a launch has fewer
 // than 2^32 lanes); longer arrays take several.
-constexpr int64_t kCodecMax = (int64_t)kCodecElems << 23;
+constexpr int64_t kCodecMax = (int64_t)kAwItemElems << 25;
 
 ps_status launch_encode_fp8(const float* x, uint8_t* code, float* scale, int64_t n, int kind, hipStream_t s) {
   for (int64_t o = 0; o < n; o += kCodecMax) {
     const int64_t k = n - o < kCodecMax ? n - o : kCodecMax;
-    const dim3 grid((uint32_t)((k + kCodecElems - 1) / kCodecElems));
+    const dim3 grid((uint32_t)((k + kEncodeItems * kAwItemElems - 1) / (kEncodeItems * kAwItemElems)));
     if (kind == PS_MOMENT_SIGNED)
-      hipLaunchKernelGGL(k_encode_fp8<PS_MOMENT_SIGNED>, grid, dim3(kCodecThreads), 0, s, x + o, code + o,
+      hipLaunchKernelGGL(k_encode_fp8<PS_MOMENT_SIGNED>, grid, dim3(64), 0, s, x + o, code + o,
                          scale + o / kBlock, k);
     else
-      hipLaunchKernelGGL(k_encode_fp8<PS_MOMENT_UNSIGNED>, grid, dim3(kCodecThreads), 0, s, x + o, code + o,
+      hipLaunchKernelGGL(k_encode_fp8<PS_MOMENT_UNSIGNED>, grid, dim3(64), 0, s, x + o, code + o,
                          scale + o / kBlock, k);
     if (ps_status st = hip_check(hipGetLastError(), "k_encode_fp8 launch")) return st;
   }
@@ -576,12 +813,12 @@ ps_status launch_encode_fp8(const float* x, uint8_t* code, float* scale, int64_t
 ps_status launch_decode_fp8(const uint8_t* code, const float* scale, float* x, int64_t n, int kind, hipStream_t s) {
   for (int64_t o = 0; o < n; o += kCodecMax) {
     const int64_t k = n - o < kCodecMax ? n - o : kCodecMax;
-    const dim3 grid((uint32_t)((k + kCodecElems - 1) / kCodecElems));
+    const dim3 grid((uint32_t)((k + kAwItemElems - 1) / kAwItemElems));
     if (kind == PS_MOMENT_SIGNED)
-      hipLaunchKernelGGL(k_decode_fp8<PS_MOMENT_SIGNED>, grid, dim3(kCodecThreads), 0, s, code + o, scale + o / kBlock,
+      hipLaunchKernelGGL(k_decode_fp8<PS_MOMENT_SIGNED>, grid, dim3(64), 0, s, code + o, scale + o / kBlock,
                          x + o, k);
     else
-      hipLaunchKernelGGL(k_decode_fp8<PS_MOMENT_UNSIGNED>, grid, dim3(kCodecThreads), 0, s, code + o,
+      hipLaunchKernelGGL(k_decode_fp8<PS_MOMENT_UNSIGNED>, grid, dim3(64), 0, s, code + o,
                          scale + o / kBlock, x + o, k);
     if (ps_status st = hip_check(hipGetLastError(), "k_decode_fp8 launch")) return st;
   }

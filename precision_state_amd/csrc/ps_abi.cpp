@@ -7,7 +7,7 @@
 #include <cstring>
 #include <vector>
 
-#include "ps_internal.h"
+#include "ps_adamw.h"
 
 namespace ps {
 

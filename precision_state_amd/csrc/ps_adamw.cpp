@@ -12,7 +12,7 @@
 #include <new>
 #include <vector>
 
-#include "ps_internal.h"
+#include "ps_adamw.h"
 
 using namespace ps;
 
@@ -311,9 +311,13 @@ ps_status step(ps_adamw_plan* p, const ps_hparams* groups, int32_t n_groups, int
     }
     p->last_step = step;
   }
-  const bool sr = groups[0].split_mode == PS_SPLIT_STOCHASTIC;
+  // RS2 = 1 / sqrt(1 - beta2^t) is largest at t = 1; below 2^28 for every
+  // double beta2 < 1 except the few next to 1.
+  bool fast = true;
+  for (int32_t i = 0; i < n_groups; ++i)
+    fast &= groups[i].eps >= 0x1p-60 && groups[i].eps <= 0x1p58 && 1.0 - groups[i].beta2 >= 0x1p-56;
   const AwRun run{p->ctl, step == 0 ? p->dev_sc : nullptr, clipped, groups[0].algo == PS_ALGO_NADAM,
-                  groups[0].split_mode == PS_SPLIT_NEAREST_AWAY, rounding == PS_ROUND_STOCHASTIC};
+                  rounding == PS_ROUND_STOCHASTIC, fast};
   if (step == 0) {
     AwTick tick = {};
     for (int32_t i = 0; i < n_groups; ++i) {
@@ -328,7 +332,7 @@ ps_status step(ps_adamw_plan* p, const ps_hparams* groups, int32_t n_groups, int
   }
   for (int kind = 0; kind < kAwKinds; ++kind) {
     if (p->items[kind] == 0) continue;
-    if (ps_status st = launch_adamw_step(kind, sr, p->table[kind], p->items[kind], p->sc, run, s)) return st;
+    if (ps_status st = launch_adamw_step(kind, groups[0].split_mode, p->table[kind], p->items[kind], p->sc, run, s)) return st;
   }
   return PS_OK;
 }
