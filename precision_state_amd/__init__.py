@@ -177,6 +177,13 @@ def _stream(stream):
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
+def _current_raw_stream(index):
+    """The device's current stream as an integer (without the Stream object, whose making takes 2 us)."""
+    import torch
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(index) if get is not None else torch.cuda.current_stream(index).cuda_stream
+
+
 @dataclass
 class HParams:
     algo: int = ALGO_NADAM
@@ -403,6 +410,12 @@ class OffloadPlan:
             pass
 
 
+def _raw_stream(device, stream):
+    if stream is not None:
+        return stream if isinstance(stream, int) else stream.cuda_stream
+    return _current_raw_stream(device.index)
+
+
 def _fp8_check(x, code, scale):
     import torch
     n = x.numel()
@@ -414,6 +427,8 @@ def _fp8_check(x, code, scale):
         raise ValueError("x, code and scale must be contiguous")
     if not (x.device == code.device == scale.device):
         raise ValueError("x, code and scale must be on one device")
+    if x.device.type != "cuda":
+        raise ValueError("x, code and scale are not on a GPU")
 
 
 def encode_fp8(x, code, scale, kind, stream=None):
@@ -421,14 +436,14 @@ def encode_fp8(x, code, scale, kind, stream=None):
     codes the square root. code: any 1-byte dtype, torch.float8_e4m3fn among them."""
     _fp8_check(x, code, scale)
     with _on(x.device):
-        _check(_lib.ps_encode_fp8(_ptr(x), _ptr(code), _ptr(scale), x.numel(), kind, _stream(stream)))
+        _check(_lib.ps_encode_fp8(_ptr(x), _ptr(code), _ptr(scale), x.numel(), kind, _raw_stream(x.device, stream)))
 
 
 def decode_fp8(code, scale, x, kind, stream=None):
     """The float32 moments that e4m3 codes and scales stand for (ps_decode_fp8)."""
     _fp8_check(x, code, scale)
     with _on(x.device):
-        _check(_lib.ps_decode_fp8(_ptr(code), _ptr(scale), _ptr(x), x.numel(), kind, _stream(stream)))
+        _check(_lib.ps_decode_fp8(_ptr(code), _ptr(scale), _ptr(x), x.numel(), kind, _raw_stream(x.device, stream)))
 
 
 class _NoSwitch:
@@ -480,20 +495,21 @@ def _adamw_record(i, t):
         raise wrong("param and grad are both None")
     n = ref.numel()
     types = {torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16, torch.float16: TYPE_F16}
-    rec = CAdamWTensor(numel=n, group=t.group)
-    nb = (n + BLOCK - 1) // BLOCK
-    for name, size in (("param", n), ("grad", n), ("m", n), ("v", n), ("residual", n), ("copy", n), ("m_scale", nb),
-                       ("v_scale", nb)):
-        x = getattr(t, name)
+    nb, device, ptr = (n + BLOCK - 1) // BLOCK, ref.device, {}
+    for name, x, size in (("param", t.param, n), ("grad", t.grad, n), ("m", t.m, n), ("v", t.v, n),
+                          ("residual", t.residual, n), ("copy", t.copy, n), ("m_scale", t.m_scale, nb),
+                          ("v_scale", t.v_scale, nb)):
         if x is None:
             continue
         if x.numel() != size:
             raise wrong(f"{name} has {x.numel()} elements, not {size}")
         if not x.is_contiguous():
             raise wrong(f"{name} is not contiguous")
-        if x.device != ref.device:
-            raise wrong(f"{name} is on {x.device}, not on {ref.device}")
-        setattr(rec, name, x.data_ptr() if size else None)
+        if x.device != device:
+            raise wrong(f"{name} is on {x.device}, not on {device}")
+        if size:
+            ptr[name] = x.data_ptr()
+    rec = CAdamWTensor(numel=n, group=t.group, **ptr)
     if t.grad is not None:
         if t.grad.dtype not in types:
             raise wrong(f"grad has dtype {t.grad.dtype}")
@@ -557,11 +573,12 @@ class AdamWPlan:
         size = ctypes.c_size_t(0)
         _check(_lib.ps_adamw_workspace_size(arr, len(recs), ctypes.byref(size)))
         with _on(self.device):
-            self._stream0 = torch.cuda.current_stream(self.device)
+            self.device = torch.device("cuda", torch.cuda.current_device())
+            self._stream0 = _current_raw_stream(self.device.index)
             self.workspace = torch.empty(size.value, dtype=torch.uint8, device=self.device)
             h = ctypes.c_void_p()
-            _check(_lib.ps_adamw_plan_create(arr, len(recs), self.workspace.data_ptr(), size.value,
-                                             _stream(self._stream0), ctypes.byref(h)))
+            _check(_lib.ps_adamw_plan_create(arr, len(recs), self.workspace.data_ptr(), size.value, self._stream0,
+                                             ctypes.byref(h)))
         self._h = h
         self._tensors = tensors          # the arrays live as long as the plan
         ctl = self.workspace[:ctypes.sizeof(CAdamWControl)]
@@ -578,13 +595,12 @@ class AdamWPlan:
         import torch
         if not self._h:
             raise ValueError("the plan is closed")
-        if stream is None:
-            stream = torch.cuda.current_stream(self.device)
-        if not isinstance(stream, int):
-            if stream != self._stream0 and not torch.cuda.is_current_stream_capturing():
-                self.workspace.record_stream(stream)   # the allocator must not hand it out before this stream is done
-            stream = stream.cuda_stream
-        return stream
+        raw = _raw_stream(self.device, stream)
+        if raw != self._stream0 and not torch.cuda.is_current_stream_capturing():
+            # the allocator must not hand the workspace out before this stream is done with it
+            self.workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
+                                         torch.cuda.ExternalStream(raw, device=self.device))
+        return raw
 
     def set_grads(self, grads, stream=None):
         """New gradients for all tensors, in list order; None: the tensor is passed by."""

@@ -1,8 +1,8 @@
 // ps_adamw.cpp - host side of the AdamW plan (ps_adamw_*): argument
 // validation, the plan's layout in the caller's workspace, and dispatch.
 //
-// Workspace: control block | scalars of device-counted steps | partial sums of
-// the norm | step records by kind | their item ends | norm records | their
+// Workspace: control block | scalars of device-counted steps | counts of the
+// norm's finished workgroups | their partial sums | step records by kind | their item ends | norm records | their
 // chunk ends | slot of each list index in the step records. The tables are
 // built once, on the host, and uploaded by ps_adamw_plan_create; afterwards
 // only k_set_grads writes to them.
@@ -32,6 +32,7 @@ struct ps_adamw_plan {
   ps_adamw_control* ctl = nullptr;
   AwScalars* dev_sc = nullptr;
   double* partials = nullptr;
+  uint32_t* counts = nullptr;   // the norm's finished workgroups; 0 between calls
   AwRec* recs = nullptr;
   AwNormRec* nrecs = nullptr;
   const uint32_t* slot = nullptr;
@@ -100,7 +101,7 @@ int kind_of(const ps_adamw_tensor& x) {
 
 // Where the tables lie in the workspace.
 struct Layout {
-  size_t scalars, partials, recs, ends, nrecs, nends, slot, bytes;
+  size_t scalars, counts, partials, recs, ends, nrecs, nends, slot, bytes;
   int64_t n_step = 0, n_norm = 0;
   uint64_t items[kAwKinds] = {};
   uint64_t chunks = 0;
@@ -128,6 +129,7 @@ ps_status lay_out(const ps_adamw_tensor* t, int32_t n, Layout& l) {
     return o;
   };
   l.scalars = take(sizeof(AwGroups));
+  l.counts = take(sizeof(uint32_t) * kNormCountStride * (1 + kNormCounts));
   l.partials = take(sizeof(double) * (size_t)std::min<uint64_t>(std::max<uint64_t>(l.chunks, 1), kNormMaxWg));
   l.recs = take(sizeof(AwRec) * (size_t)l.n_step);
   l.ends = take(sizeof(uint32_t) * (size_t)l.n_step);
@@ -254,6 +256,7 @@ ps_status create(const ps_adamw_tensor* t, int32_t n, void* workspace, size_t wo
   tmp.ctl = (ps_adamw_control*)w;
   tmp.dev_sc = (AwScalars*)(w + l.scalars);
   tmp.partials = (double*)(w + l.partials);
+  tmp.counts = (uint32_t*)(w + l.counts);
   tmp.recs = (AwRec*)(w + l.recs);
   tmp.nrecs = (AwNormRec*)(w + l.nrecs);
   tmp.slot = (const uint32_t*)(w + l.slot);
@@ -378,7 +381,7 @@ ps_status ps_adamw_grad_norm(ps_adamw_plan* plan, double max_norm, double grad_s
   if (!is_finite(grad_scale) || !(grad_scale > 0))
     return fail(PS_ERR_INVALID_ARG, "grad_scale must be finite and > 0");
   if (ps_status s = on_device(plan)) return s;
-  return launch_grad_norm(plan->norm, plan->partials, plan->ctl, max_norm, grad_scale, (hipStream_t)stream);
+  return launch_grad_norm(plan->norm, plan->partials, plan->counts, plan->ctl, max_norm, grad_scale, (hipStream_t)stream);
 }
 
 ps_status ps_adamw_step(ps_adamw_plan* plan, const ps_hparams* groups, int32_t n_groups, int64_t step_no,

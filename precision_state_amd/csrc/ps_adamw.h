@@ -12,7 +12,9 @@ namespace ps {
 constexpr int kAwItemElems = 512;     // step work item: one 64-lane wave, 8 elements per lane, two blocks
 constexpr uint32_t kAwMaxItems = 0xFFFFFFFFu / 64;   // a launch has fewer than 2^32 lanes
 constexpr int kNormChunk = 8192;      // norm work item: one 256-thread workgroup, 32 elements per thread
-constexpr int kNormMaxWg = 2048;      // norm workgroups (and partial sums) at most
+constexpr uint32_t kNormMaxWg = 1024;      // norm workgroups (and partial sums) at most
+constexpr uint32_t kNormCounts = 32;      // first-level counts of finished norm workgroups
+constexpr uint32_t kNormCountStride = 64; // words from one to the next: each on a cache line of its own
 constexpr int kAwGrads = 384;         // gradient pointers in one k_set_grads launch
 
 // Kinds of step tensors: each kind of the list is one launch of its own kernel.
@@ -82,8 +84,8 @@ ps_status launch_adamw_step(int kind, int split, const AwTable& t, uint32_t item
                             hipStream_t s);
 ps_status launch_adamw_tick(ps_adamw_control* ctl, AwScalars* sc, const AwTick& hp, int n_groups, int clipped,
                             hipStream_t s);
-ps_status launch_grad_norm(const AwNormTable& t, double* partials, ps_adamw_control* ctl, double max_norm,
-                           double grad_scale, hipStream_t s);
+ps_status launch_grad_norm(const AwNormTable& t, double* partials, uint32_t* counts, ps_adamw_control* ctl,
+                           double max_norm, double grad_scale, hipStream_t s);
 ps_status launch_set_grads(AwRec* recs, AwNormRec* nrecs, const uint32_t* slot, const void* const* grads, int32_t n,
                            hipStream_t s);
 ps_status launch_encode_fp8(const float* x, uint8_t* code, float* scale, int64_t n, int kind, hipStream_t s);
