@@ -415,8 +415,8 @@ ps_status ps_adamw_grad_norm(ps_adamw_plan* plan, double max_norm, double grad_s
  *   m  = B1*m0 + C1*g;  v = B2*v0 + C2*(g*g);  r = sqrt(v);  d = r*RS2 + EPS
  *   ADAM: u = A*(m/d)             NADAM: u = (AG*g + AM*m)/d
  *   u  = u + CWD*w;  w' = w - u
- * Every operation is rounded to fp32 by itself (no fma); the scalars are those
- * of ps_step_scalars. w is the fp32 parameter, the joined (bf16, residual)
+ * Every operation is rounded to fp32 by itself (no fma; the sign of a zero
+ * quotient is not specified); the scalars are those of ps_step_scalars. w is the fp32 parameter, the joined (bf16, residual)
  * pair, or with split_mode STOCHASTIC the bf16 value alone; w' is stored as
  * it is (and rounded to copy_type for the copy), split, or rounded
  * stochastically, with the random bits of ps_hparams for the tensor's index in

@@ -471,7 +471,8 @@ class AdamWTensor:
 
     param: float32, or bfloat16 (any other 2-byte dtype is read as bf16 bits);
     None if only the gradient's norm is wanted. grad: float32, bfloat16 or
-    float16, or None. m, v: float32, or a 1-byte dtype (e4m3 codes) with m_scale
+    float16, or None; grad_dtype says what a later one will be (param's dtype if
+    not given). m, v: float32, or a 1-byte dtype (e4m3 codes) with m_scale
     and v_scale. residual: a bf16 parameter's low halves. copy: bfloat16 or
     float16, written with a float32 parameter's new values."""
     param: object
@@ -483,6 +484,7 @@ class AdamWTensor:
     residual: object = None
     copy: object = None
     group: int = 0
+    grad_dtype: object = None
 
 
 def _adamw_record(i, t):
@@ -514,8 +516,14 @@ def _adamw_record(i, t):
         if t.grad.dtype not in types:
             raise wrong(f"grad has dtype {t.grad.dtype}")
         rec.grad_type = types[t.grad.dtype]
+        if t.grad_dtype not in (None, t.grad.dtype):
+            raise wrong(f"grad has dtype {t.grad.dtype}, not {t.grad_dtype}")
+    elif t.grad_dtype is not None:
+        if t.grad_dtype not in types:
+            raise wrong(f"grad_dtype is {t.grad_dtype}")
+        rec.grad_type = types[t.grad_dtype]
     elif t.param is not None:
-        rec.grad_type = types.get(t.param.dtype, TYPE_BF16)   # what a later gradient has to be
+        rec.grad_type = types.get(t.param.dtype, TYPE_BF16)
     if t.param is None:
         return rec
     if t.m is None or t.v is None:

@@ -196,12 +196,13 @@ constexpr bool quad_lanes(int kind) { return !(kind & kAwE4m3) || !(kind & kAwBf
 // arithmetic stays hidden that is worth more than latency. The 202M layer with
 // fp32 moments took 1020, 890, 920, 946, 953 and 995 us at 1, 2, 3, 4, 5 and 8
 // waves; 514M bf16 weights with e4m3 moments 1459, 1188, 1138, 1150 and 1180 us at
-// 2, 3, 4, 5 and 8. Where weights are rounded stochastically beside e4m3
-// moments, integer work for the random bits fills the vector units and wants
-// all waves (42M parameters: 80 us at 7 and more, 83 at 5, 87 at 4).
+// 2, 3, 4, 5 and 8: about 15 KB of loads in flight a SIMD for both. Where weights
+// are rounded stochastically beside e4m3 moments, integer work for the random
+// bits fills the vector units and wants as many waves as have registers (42M
+// parameters, both rounded so: 87, 83, 79 and 77 us at 4, 5, 6 and 7 waves; 8 spill,
+// 83 us).
 constexpr int waves_of(int kind, int split) {
-  const bool sr = (kind & kAwBf16) && split == PS_SPLIT_STOCHASTIC;
-  return kind & kAwE4m3 ? (sr ? 7 : 4) : (sr ? 3 : 2);
+  return !(kind & kAwE4m3) ? 2 : (kind & kAwBf16) && split == PS_SPLIT_STOCHASTIC ? 7 : 4;
 }
 
 // Each XCD takes runs of this many consecutive items. At the waves above runs
@@ -453,8 +454,8 @@ __device__ __forceinline__ int find(const uint32_t* ends, int n, uint32_t item) 
 }
 
 template <int KIND, int SPLIT, bool NADAM>
-__global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(waves_of(KIND, SPLIT), waves_of(KIND, SPLIT))))
- void k_adamw_step(AwTable t, AwGroups sc, AwRun run) {
+__global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(
+    waves_of(KIND, SPLIT), waves_of(KIND, SPLIT)))) void k_adamw_step(AwTable t, AwGroups sc, AwRun run) {
   const uint32_t item = xcd_item<kAwXcdChunk>(blockIdx.x, gridDim.x);
   const int i = find(t.item_end, t.n, item);
   const AwRec T = ld_const(t.recs + i);
@@ -591,9 +592,10 @@ __device__ __forceinline__ Chunk norm_chunk(const AwNormTable& t, uint32_t chunk
 // a second launch for the sum 18.0 us, this 17.8 us, and 17.2 us with 1024
 // workgroups of equal shares; 64 tensors of 8192 5.3, 7.0 and 4.9 us.) A chunk's
 // record is looked up while the loads of the one before are under way: 16.9 us,
-// and 296 us (6.9 TB/s) for 514M fp32 gradients, 301 us without. Partial
-// sums and counts cross XCDs: they go through agent-scope atomics, which write through
-// the XCD's L2, and a workgroup counts when its partial sum has arrived. The
+// and 296 us (6.9 TB/s) for 514M fp32 gradients, 301 us without. Partial sums and
+// counts cross XCDs: they go through agent-scope atomics, which write through
+// the XCD's L2, and a workgroup counts when its partial sum has arrived (a
+// release per workgroup, which writes the whole L2 back, cost 70 us more). The
 // last workgroup sets the counts back to 0.
 __global__ __launch_bounds__(kNormThreads) void k_grad_norm(AwNormTable t, double* partials, uint32_t* counts,
                                                             ps_adamw_control* ctl, double max_norm, double grad_scale) {
@@ -639,6 +641,7 @@ __global__ __launch_bounds__(kNormThreads) void k_grad_norm(AwNormTable t, doubl
     }
     __syncthreads();
     if (!last) return;
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
     sum = 0.0;
     for (uint32_t i = threadIdx.x; i < n; i += kNormThreads)
       sum += __hip_atomic_load(partials + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);

@@ -113,6 +113,35 @@ def test_step_over_gradient_magnitudes(level, state):
 
 
 @pytest.mark.parametrize("algo", [0, 1])
+@pytest.mark.parametrize("kw", [dict(eps=1e-40), dict(eps=1e20), dict(beta1=0.0), dict(beta2=0.0), dict(lr=0.0),
+                                dict(lr=50.0), dict(beta2=1 - 2.0 ** -50), dict(beta2=1 - 2.0 ** -53), dict(beta1=1e-30),
+                                dict(eps=2.0 ** -61), dict(wd=(100.0, 0.0))])
+def test_step_at_extreme_hyperparameters(algo, kw):
+    """Where the scalars leave the ranges of the fast quotient, at their ends, and where terms vanish."""
+    params = build([dict(param="f32", grad="f32", state=s) for s in ("f32", "e4m3")] +
+                   [dict(param="bf16", state="e4m3")], sizes=[5, 700, 1024])
+    dev, host = hps(algo, **kw)
+    run_steps(params, ps.AdamWPlan([p.tensor(ps) for p in params]), dev, host, 2, np.random.default_rng(50), first=2)
+
+
+def test_first_moments_that_have_decayed_away():
+    """First moments far below the fast quotient's range beside ordinary ones; second moments of zero and below 2^-96."""
+    rng = np.random.default_rng(51)
+    p = Param(4096, rng, param="f32", grad="f32", state="f32")
+    p.m = (p.m * np.exp(rng.uniform(-90, 0, p.n))).astype(np.float32)
+    p.v = np.where(rng.random(p.n) < 0.3, 0, p.v * np.exp(rng.uniform(-75, 0, p.n))).astype(np.float32)
+    g = np.where(rng.random(p.n) < 0.5, 0, p.g).astype(np.float32)
+    for k in ("m", "v"):
+        p.d[k].t.copy_(torch.from_numpy(getattr(p, k)))
+    p.new_grad(g)
+    for algo in (0, 1):
+        dev, host = hps(algo, wd=(0.1,))
+        ps.AdamWPlan([p.tensor(ps)]).step(dev, 3)
+        p.step(host[0], 3)
+        agree([p])
+
+
+@pytest.mark.parametrize("algo", [0, 1])
 def test_step_against_64_bits(algo):
     """fp32 weights and moments against the formula in 64 bits with the same fp32 scalars. Roundings, each at most half
     a step: m: two products and a sum; v: three products and a sum; r: half of v's and its own; d: two more; the quotient, the factor
@@ -369,6 +398,24 @@ def test_set_grads_over_many_tensors():
     for p in params:
         p.d["g"], p.gbits = None, None
     agree(params)
+
+
+def test_gradients_that_come_later():
+    """Tensors without a gradient at first, with the dtype the later one has."""
+    p = Param(700, np.random.default_rng(52), param="f32", grad="bf16", copy="bf16")
+    t = p.tensor(ps)
+    g, t.grad = t.grad, None
+    t.grad_dtype = torch.bfloat16
+    plan = ps.AdamWPlan([t])
+    dev, host = hps(wd=(0.1,))
+    plan.step(dev, 1)
+    agree([p])
+    plan.set_grads([g])
+    plan.step(dev, 1)
+    p.step(host[0], 1)
+    agree([p])
+    with pytest.raises(ValueError):
+        ps.AdamWPlan([ps.AdamWTensor(t.param, g, t.m, t.v, grad_dtype=torch.float16)])
 
 
 def test_side_streams_and_two_plans_at_once():
