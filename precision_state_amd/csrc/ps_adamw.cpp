@@ -47,6 +47,7 @@ struct ps_adamw_plan {
   std::vector<ps_hparams> last_groups;
   int64_t last_step = 0;
   AwGroups sc = {};
+  NadamProduct product[PS_ADAMW_MAX_GROUPS];
 };
 
 namespace {
@@ -309,7 +310,7 @@ ps_status step(ps_adamw_plan* p, const ps_hparams* groups, int32_t n_groups, int
     p->last_groups.assign(groups, groups + n_groups);
     for (int32_t i = 0; i < n_groups; ++i) {
       StepScalars c;
-      step_scalars(groups[i], step, &c);
+      step_scalars_with(groups[i], step, groups[i].algo == PS_ALGO_NADAM ? nadam_product(groups[i], step, &p->product[i]) : 0.0, &c);
       p->sc.g[i] = AwScalars{c.B1, c.C1, c.B2, c.C2, c.EPS, c.A, c.RS2, c.AG, c.AM, c.CWD, c.sr_step, 0, groups[i].seed};
     }
     p->last_step = step;

@@ -91,6 +91,18 @@ ps_status launch_set_grads(AwRec* recs, AwNormRec* nrecs, const uint32_t* slot, 
 ps_status launch_encode_fp8(const float* x, uint8_t* code, float* scale, int64_t n, int kind, hipStream_t s);
 ps_status launch_decode_fp8(const uint8_t* code, const float* scale, float* x, int64_t n, int kind, hipStream_t s);
 
+// ---- host scalars (ps_scalars.cpp) ----
+// P_t = mu_1 ... mu_t of NAdam, carried from one update to the next: a training
+// loop multiplies once per step where the product from the start takes hundreds
+// of pow() calls (the same factors in the same order, so the same double).
+struct NadamProduct {
+  double beta1 = 0, psi = 0;
+  int64_t t = -1;
+  double prod = 1.0;
+};
+double nadam_product(const ps_hparams& hp, int64_t t, NadamProduct* last);
+void step_scalars_with(const ps_hparams& hp, int64_t t, double prod, StepScalars* o);
+
 // ---- argument checks shared with the other entry points (ps_abi.cpp) ----
 ps_status check_hparams(const ps_hparams* hp);
 void clear_error();

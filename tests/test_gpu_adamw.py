@@ -124,6 +124,19 @@ def test_step_at_extreme_hyperparameters(algo, kw):
     run_steps(params, ps.AdamWPlan([p.tensor(ps) for p in params]), dev, host, 2, np.random.default_rng(50), first=2)
 
 
+def test_step_numbers_in_any_order():
+    """The plan carries NAdam's product from call to call: ascending, repeated, earlier and far steps, other schedules in
+    between, each as if it were the plan's first."""
+    p = Param(300, np.random.default_rng(53), param="f32", grad="f32", state="f32")
+    plan = ps.AdamWPlan([p.tensor(ps)])
+    for t, kw in ((5, {}), (6, {}), (6, {}), (7, dict(lr=5e-4)), (3, {}), (2000, {}), (2001, {}), (8, dict(beta1=0.8)),
+                  (9, dict(beta1=0.8)), (10, {}), (11, dict(beta1=0.999)), (12, dict(beta1=0.999)), (1, {})):
+        dev, host = hps(1, wd=(0.1,), **kw)
+        plan.step(dev, t)
+        p.step(host[0], t)
+        agree([p])
+
+
 def test_first_moments_that_have_decayed_away():
     """First moments far below the fast quotient's range beside ordinary ones; second moments of zero and below 2^-96."""
     rng = np.random.default_rng(51)
