@@ -30,7 +30,7 @@ if not os.path.exists(LIB_PATH):
 try:
     import torch  # noqa: F401
 except ImportError:
-    pass
+    torch = None
 
 _lib = ctypes.CDLL(LIB_PATH)
 
@@ -177,11 +177,9 @@ def _stream(stream):
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
-def _current_raw_stream(index):
-    """The device's current stream as an integer (without the Stream object, whose making takes 2 us)."""
-    import torch
-    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return get(index) if get is not None else torch.cuda.current_stream(index).cuda_stream
+# The device's current stream as an integer (without the Stream object, whose making takes 2 us).
+_current_raw_stream = getattr(getattr(torch, "_C", None), "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 @dataclass
@@ -417,7 +415,6 @@ def _raw_stream(device, stream):
 
 
 def _fp8_check(x, code, scale):
-    import torch
     n = x.numel()
     if x.dtype != torch.float32 or scale.dtype != torch.float32 or code.element_size() != 1:
         raise ValueError("x and scale are float32, code has 1-byte elements")
@@ -425,25 +422,27 @@ def _fp8_check(x, code, scale):
         raise ValueError("code needs x's size and scale one value for each 256 of them")
     if not (x.is_contiguous() and code.is_contiguous() and scale.is_contiguous()):
         raise ValueError("x, code and scale must be contiguous")
-    if not (x.device == code.device == scale.device):
+    device = x.device
+    if code.device != device or scale.device != device:
         raise ValueError("x, code and scale must be on one device")
-    if x.device.type != "cuda":
+    if device.type != "cuda":
         raise ValueError("x, code and scale are not on a GPU")
+    return n, device
 
 
 def encode_fp8(x, code, scale, kind, stream=None):
     """float32 moments -> e4m3 codes and a power-of-two scale for each 256 (ps_encode_fp8); kind MOMENT_UNSIGNED
     codes the square root. code: any 1-byte dtype, torch.float8_e4m3fn among them."""
-    _fp8_check(x, code, scale)
-    with _on(x.device):
-        _check(_lib.ps_encode_fp8(_ptr(x), _ptr(code), _ptr(scale), x.numel(), kind, _raw_stream(x.device, stream)))
+    n, device = _fp8_check(x, code, scale)
+    with _on(device):
+        _check(_lib.ps_encode_fp8(x.data_ptr(), code.data_ptr(), scale.data_ptr(), n, kind, _raw_stream(device, stream)))
 
 
 def decode_fp8(code, scale, x, kind, stream=None):
     """The float32 moments that e4m3 codes and scales stand for (ps_decode_fp8)."""
-    _fp8_check(x, code, scale)
-    with _on(x.device):
-        _check(_lib.ps_decode_fp8(_ptr(code), _ptr(scale), _ptr(x), x.numel(), kind, _raw_stream(x.device, stream)))
+    n, device = _fp8_check(x, code, scale)
+    with _on(device):
+        _check(_lib.ps_decode_fp8(code.data_ptr(), scale.data_ptr(), x.data_ptr(), n, kind, _raw_stream(device, stream)))
 
 
 class _NoSwitch:
@@ -459,7 +458,6 @@ _NO_SWITCH = _NoSwitch()
 
 def _on(device):
     """Makes `device` the current one; nothing to do where it is."""
-    import torch
     if device.type != "cuda" or device.index is None or device.index == torch.cuda.current_device():
         return _NO_SWITCH
     return torch.cuda.device(device)
@@ -488,8 +486,6 @@ class AdamWTensor:
 
 
 def _adamw_record(i, t):
-    import torch
-
     def wrong(what):
         return ValueError(f"tensor {i}: {what}")
     ref = t.param if t.param is not None else t.grad
@@ -567,7 +563,6 @@ class AdamWPlan:
     _h = None
 
     def __init__(self, tensors: Sequence[AdamWTensor], device=None):
-        import torch
         tensors = list(tensors)
         recs = [_adamw_record(i, t) for i, t in enumerate(tensors)]
         devices = {(t.param if t.param is not None else t.grad).device for t in tensors}
@@ -582,7 +577,8 @@ class AdamWPlan:
         _check(_lib.ps_adamw_workspace_size(arr, len(recs), ctypes.byref(size)))
         with _on(self.device):
             self.device = torch.device("cuda", torch.cuda.current_device())
-            self._stream0 = _current_raw_stream(self.device.index)
+            self._index = self.device.index
+            self._stream0 = _current_raw_stream(self._index)
             self.workspace = torch.empty(size.value, dtype=torch.uint8, device=self.device)
             h = ctypes.c_void_p()
             _check(_lib.ps_adamw_plan_create(arr, len(recs), self.workspace.data_ptr(), size.value, self._stream0,
@@ -600,19 +596,24 @@ class AdamWPlan:
         self._groups = None
 
     def _on_stream(self, stream):
-        import torch
         if not self._h:
             raise ValueError("the plan is closed")
-        raw = _raw_stream(self.device, stream)
+        raw = _current_raw_stream(self._index) if stream is None else _raw_stream(self.device, stream)
         if raw != self._stream0 and not torch.cuda.is_current_stream_capturing():
             # the allocator must not hand the workspace out before this stream is done with it
             self.workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
                                          torch.cuda.ExternalStream(raw, device=self.device))
         return raw
 
+    def _run(self, f, *args):
+        status = f(self._h, *args)
+        if status and torch.cuda.current_device() != self._index:   # refused, for that or for another reason
+            with torch.cuda.device(self.device):
+                status = f(self._h, *args)
+        _check(status)
+
     def set_grads(self, grads, stream=None):
         """New gradients for all tensors, in list order; None: the tensor is passed by."""
-        import torch
         if len(grads) != len(self._sizes):
             raise ValueError(f"{len(grads)} gradients for {len(self._sizes)} tensors")
         types = (torch.float32, torch.bfloat16, torch.float16)
@@ -623,15 +624,14 @@ class AdamWPlan:
             if g.dtype != types[ty] or g.numel() != n or not g.is_contiguous() or g.device != self.device:
                 raise ValueError(f"tensor {i}: the gradient must be contiguous {types[ty]} on {self.device} with {n} elements")
             arr[i] = g.data_ptr()
-        with _on(self.device):
-            _check(_lib.ps_adamw_set_grads(self._h, arr, len(grads), self._on_stream(stream)))
+        raw = self._on_stream(stream)
+        self._run(_lib.ps_adamw_set_grads, arr, len(grads), raw)
         for t, g in zip(self._tensors, grads):
             t.grad = g
 
     def grad_norm(self, max_norm=float("inf"), grad_scale=1.0, stream=None):
         """The gradients' global 2-norm and clip factor into the control block (ps_adamw_grad_norm)."""
-        with _on(self.device):
-            _check(_lib.ps_adamw_grad_norm(self._h, max_norm, grad_scale, self._on_stream(stream)))
+        self._run(_lib.ps_adamw_grad_norm, max_norm, grad_scale, self._on_stream(stream))
 
     def step(self, groups, step=0, clipped=False, rounding=ROUND_NEAREST, stream=None):
         """One step (ps_adamw_step). groups: the HParams of each group. step: the update's number, from 1, or 0
@@ -640,9 +640,7 @@ class AdamWPlan:
                for g in groups]
         if self._groups is None or self._groups[0] != key:
             self._groups = key, (CHParams * max(1, len(key)))(*[CHParams(*k) for k in key])
-        with _on(self.device):
-            _check(_lib.ps_adamw_step(self._h, self._groups[1], len(key), step, int(clipped), rounding,
-                                      self._on_stream(stream)))
+        self._run(_lib.ps_adamw_step, self._groups[1], len(key), step, int(clipped), rounding, self._on_stream(stream))
 
     def close(self):
         if self._h:

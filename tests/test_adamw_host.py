@@ -237,3 +237,27 @@ def test_reference_update_against_the_oracle_step():
         # u: m (3 h of its terms), r and d (5 h), quotient and factor (3 h); w' rounds the difference once
         scale = np.abs(c["A"] if algo == 0 else c["AG"] + c["AM"]) * (big_m + np.abs(g)) / (np.sqrt(v64) * c["RS2"])
         assert np.all(np.abs(w32 - w64) <= 16 * h * scale + 2 * h * np.abs(w64))
+
+
+@pytest.mark.parametrize("algo", [0, 1])
+def test_reference_update_is_the_optimizers_of_torch(algo):
+    """Twenty steps of the formula in 64 bits against torch.optim.AdamW and NAdam (decoupled decay). The scalars are
+    rounded to fp32: m, v and their roots are off by at most 2^-24 for each of the scalars that make them (2 in m and in
+    v a step, relative), the update by 2^-24 for each of its four more, so by (2 + 1 + 4) 2^-24 relative to its terms, and a
+    step's terms are at most lr (1 + wd |w|) times |m^| / sqrt(v^) <= 10, or 20 with the gradient's own term."""
+    torch = pytest.importorskip("torch")
+    rng = np.random.default_rng(3)
+    n, lr, wd, steps = 500, 1e-2, 0.1, 20
+    w = rng.normal(0, 0.5, n)
+    t = torch.tensor(w, requires_grad=True)
+    opt = torch.optim.NAdam([t], lr=lr, weight_decay=wd, decoupled_weight_decay=True, momentum_decay=4e-3) if algo else \
+        torch.optim.AdamW([t], lr=lr, weight_decay=wd)
+    m, v = np.zeros(n), np.zeros(n)
+    hp = oracle.HParams(algo=algo, lr=lr, weight_decay=wd)
+    for step in range(1, steps + 1):
+        g = rng.normal(0, 1e-2, n)
+        t.grad = torch.tensor(g)
+        opt.step()
+        w, m, v, _ = ref.update(w, g, m, v, oracle.coeffs(hp, step), 1.0, algo == 1, np.float64)
+        bound = step * 7 * 2.0 ** -24 * lr * (20 + wd * np.abs(w))
+        assert np.all(np.abs(w - t.detach().numpy()) <= bound), step

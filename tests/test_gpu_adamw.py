@@ -268,6 +268,42 @@ def test_large_tensors_pass_32_bit_offsets():
         assert np.array_equal(ms[b0:b1].cpu().numpy(), s[::256]) and np.array_equal(vs[b0:b1].cpu().numpy(), t[::256])
 
 
+def test_large_fp32_tensors_pass_32_bit_offsets():
+    """The other lane layout: fp32 weights and gradients with 8-bit moments and a copy, 2^30 + 777 elements (byte offsets
+    beyond 2^32), and the codec over arrays of that size."""
+    n = (1 << 30) + 777
+    nb, k = ref.blocks_of(n), 777 + 256
+    a = n - k                                               # the last blocks
+    dev = "cuda"
+    w, g = torch.full((n,), 0.02, device=dev), torch.full((n,), 1e-3, device=dev)
+    copy = torch.zeros(n, dtype=torch.float16, device=dev)
+    m, v = torch.zeros(n, dtype=torch.uint8, device=dev), torch.zeros(n, dtype=torch.uint8, device=dev)
+    ms, vs = torch.zeros(nb, device=dev), torch.zeros(nb, device=dev)
+    gg = np.random.default_rng(54).normal(0, 1e-3, k).astype(np.float32)
+    g[a:] = torch.from_numpy(gg).to(dev)
+    hd, ho = hps(wd=(0.1,))
+    ps.AdamWPlan([ps.AdamWTensor(w, g, m, v, ms, vs, copy=copy)]).step(hd, 3)
+    torch.cuda.synchronize()
+    z = np.zeros(k, np.float32)
+    w1, m1, v1, r1 = ref.update(np.full(k, 0.02, np.float32), gg, z, z, oracle.coeffs(ho[0], 3), 1.0, False, np.float32)
+    s, t = ref.block_scale(ref.per_block_max(m1)), ref.block_scale(ref.per_block_max(r1))
+    assert np.array_equal(w[a:].cpu().numpy(), w1)
+    assert np.array_equal(copy[a:].cpu().numpy(), w1.astype(np.float16))
+    assert np.array_equal(m[a:].cpu().numpy(), ref.e4m3_code(m1 / ref.spread(s, k)))
+    assert np.array_equal(v[a:].cpu().numpy(), ref.second_code(r1, ref.spread(t, k)))
+    assert np.array_equal(ms[a // 256:].cpu().numpy(), s) and np.array_equal(vs[a // 256:].cpu().numpy(), t)
+    assert float(w[0]) == float(w[a - 1]) and int(m[0]) == int(m[a - 1])
+    x = w
+    x.fill_(1e-6)
+    x[a:] = torch.from_numpy(v1).to(dev)
+    ps.encode_fp8(x, m, ms, ps.MOMENT_UNSIGNED)
+    c1, s1 = ref.encode(v1, False)
+    assert np.array_equal(m[a:].cpu().numpy(), c1) and np.array_equal(ms[a // 256:].cpu().numpy(), s1)
+    ps.decode_fp8(m, ms, g, ps.MOMENT_UNSIGNED)
+    assert np.array_equal(g[a:].cpu().numpy(), ref.decode(c1, s1, False))
+    assert float(g[0]) == float(g[a - 1]) == float(ref.decode(*ref.encode(np.full(256, 1e-6, np.float32), False), False)[0])
+
+
 # ---------------------------------------------------------------------------
 # gradient norm, clipping, skipped steps
 # ---------------------------------------------------------------------------
