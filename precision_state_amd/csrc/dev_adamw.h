@@ -7,6 +7,7 @@
 namespace ps {
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef short i16x2 __attribute__((ext_vector_type(2)));
 
 // ---------------------------------------------------------------------------
 // e4m3 moments. The block's scale is the smallest power of two s >= 2^-126
@@ -31,6 +32,21 @@ __device__ __forceinline__ uint32_t e4m3_pack4(const float* y) {
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], lo, true);
 }
 
+// The same with a power-of-two scale in the conversion: codes times s, and
+// codes of x / s.
+__device__ __forceinline__ void e4m3_unpack4(uint32_t c, float s, float* d) {
+  const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c, s, false),
+              b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c, s, true);
+  d[0] = a.x; d[1] = a.y; d[2] = b.x; d[3] = b.y;
+}
+
+__device__ __forceinline__ uint32_t e4m3_pack4(const float* x, float s) {
+  i16x2 c = {0, 0};
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(c, x[0], x[1], s, false);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(c, x[2], x[3], s, true);
+  return __builtin_bit_cast(uint32_t, c);
+}
+
 __device__ __forceinline__ uint32_t wave_max_u32(uint32_t x) {
   x = row32_max_u32(x);
   const auto p = __builtin_amdgcn_permlane32_swap(x, x, false, false);
@@ -39,14 +55,24 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t x) {
 
 constexpr float kMinCode = 0x1p-9f;   // smallest e4m3 value above zero
 
-// y in [0, 448] cut to e4m3 after adding 16 random bits below its last kept
-// place: values of 2^-6 and more keep 3 mantissa bits; smaller ones keep the
-// places of 2^-6, which adding 2^-6 lines up.
-__device__ __forceinline__ float e4m3_cut(float y, uint32_t r16) {
-  return __uint_as_float((__float_as_uint(y) + (r16 << 4)) & 0xFFF00000u);
+// The random 16 bits of element j (0..3) of a quad, from its 64 bits.
+__device__ __forceinline__ uint32_t random16(uint64_t z, int j) { return (uint32_t)(z >> (16 * j)) & 0xFFFFu; }
+
+// y >= 0 cut to 3 mantissa bits after adding 16 random bits below them (one
+// instruction: 16 times half of a word of the quad's bits, plus y).
+__device__ __forceinline__ float e4m3_cut(float y, uint64_t z, int j) {
+  const uint32_t w = (uint32_t)(z >> (32 * (j >> 1)));
+  uint32_t u;
+  if (j & 1)
+    asm("v_mad_u32_u16 %0, %1, 16, %2 op_sel:[1,0,0,0]" : "=v"(u) : "v"(w), "v"(y));
+  else
+    asm("v_mad_u32_u16 %0, %1, 16, %2" : "=v"(u) : "v"(w), "v"(y));
+  return __uint_as_float(u & 0xFFF00000u);
 }
-__device__ __forceinline__ float e4m3_stochastic(float y, uint32_t r16) {
-  return y < 0x1p-6f ? e4m3_cut(y + 0x1p-6f, r16) - 0x1p-6f : e4m3_cut(y, r16);
+// y in [0, 448] cut so to e4m3's values: below 2^-6 they keep the places of 2^-6,
+// which adding 2^-6 lines up.
+__device__ __forceinline__ float e4m3_stochastic(float y, uint64_t z, int j) {
+  return y < 0x1p-6f ? e4m3_cut(y + 0x1p-6f, z, j) - 0x1p-6f : e4m3_cut(y, z, j);
 }
 
 // ---------------------------------------------------------------------------

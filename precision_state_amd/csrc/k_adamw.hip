@@ -247,9 +247,6 @@ __device__ __forceinline__ void random_quads(const AwScalars& c, uint32_t tid, i
   z[0] = splitmix64_mix(x);
   z[1] = splitmix64_mix(x + (QUAD ? 64 : 1) * kGolden);
 }
-__device__ __forceinline__ uint32_t random16(const uint64_t* z, int j) {
-  return (uint32_t)(z[j >> 2] >> (16 * (j & 3))) & 0xFFFFu;
-}
 
 // The item's elements elem0 .. elem0 + left - 1 of the tensor, left <= 512.
 template <int KIND, int SPLIT, bool NADAM, bool FULL>
@@ -299,15 +296,11 @@ __device__ __forceinline__ void adamw_item(const AwRec& T, int64_t elem0, uint32
   if (E8) {
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      e4m3_unpack4(mc[q], m + 4 * q);
-      e4m3_unpack4(vc[q], v + 4 * q);
+      e4m3_unpack4(mc[q], ms[L::block_of(4 * q)], m + 4 * q);
+      e4m3_unpack4(vc[q], vs[L::block_of(4 * q)], v + 4 * q);
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      m[j] = m[j] * ms[L::block_of(j)];
-      const float r0 = v[j] * vs[L::block_of(j)];
-      v[j] = r0 * r0;
-    }
+    for (int j = 0; j < 8; ++j) v[j] = v[j] * v[j];
   }
 
   // Moments, and what decides whether the fast square root and quotient hold
@@ -370,7 +363,8 @@ __device__ __forceinline__ void adamw_item(const AwRec& T, int64_t elem0, uint32
       random_quads<QUAD>(c, T.tid, elem0, z);
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        oh[q] = sr_pair(__float_as_uint(w[2 * q]), __float_as_uint(w[2 * q + 1]), random16(z, 2 * q), random16(z, 2 * q + 1));
+        oh[q] = sr_pair(__float_as_uint(w[2 * q]), __float_as_uint(w[2 * q + 1]), random16(z[q >> 1], 2 * (q & 1)),
+                        random16(z[q >> 1], 2 * (q & 1) + 1));
     } else {
 #pragma unroll
       for (int q = 0; q < 4; ++q)
@@ -401,35 +395,42 @@ __device__ __forceinline__ void adamw_item(const AwRec& T, int64_t elem0, uint32
     const float top = __uint_as_float(at.block_max(mx_v[b]));
     e4m3_scale(__float_as_uint(fast ? sqrt_fast(top) : __builtin_sqrtf(top)), sv[b], inv_v[b]);
   }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) m[j] = m[j] * inv_m[L::block_of(j)];
-  const uint32_t om[2] = {e4m3_pack4(m), e4m3_pack4(m + 4)};
+  const uint32_t om[2] = {e4m3_pack4(m, sm[0]), e4m3_pack4(m + 4, sm[L::block_of(4)])};
   at.store_u8(mp, om);
-  float y[8];
-  float least_y = 448.0f;
+
+  // Roots below 2^-6 of their scale, rare, take the general form, as blocks do
+  // whose roots may be subnormal. The others are cut as they are: the scale
+  // moves only their exponent.
+  bool small = false;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    y[j] = v[j] * inv_v[L::block_of(j)];
-    least_y = __builtin_fminf(least_y, y[j]);
+  for (int b = 0; b < L::kBlocks; ++b) {
+    float least = v[4 * b];
+#pragma unroll
+    for (int j = 1; j < 8 / L::kBlocks; ++j) least = __builtin_fminf(least, v[4 * b + j]);
+    small |= least < 0x1p-6f * sv[b] || sv[b] < 0x1p-100f;
   }
-  // Values below 2^-6, rare, take the general form.
-  const bool small = __builtin_amdgcn_ballot_w64(least_y < 0x1p-6f) != 0;
-  if (run.round_sr) {
-    uint64_t z[2];
-    random_quads<QUAD>(c, T.tid | kVStream, elem0, z);
-    if (small) {
+  small = __builtin_amdgcn_ballot_w64(small) != 0;
+  uint64_t z[2] = {0u, 0u};
+  if (run.round_sr) random_quads<QUAD>(c, T.tid | kVStream, elem0, z);
+  uint32_t ov[2];
+  if (!small) {
+    if (run.round_sr) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = e4m3_stochastic(y[j], random16(z, j));
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = e4m3_cut(y[j], random16(z, j));
+      for (int j = 0; j < 8; ++j) v[j] = e4m3_cut(v[j], z[j >> 2], j & 3);
     }
-  }
-  if (small) {
+    ov[0] = e4m3_pack4(v, sv[0]);
+    ov[1] = e4m3_pack4(v + 4, sv[L::block_of(4)]);
+  } else {
+    float y[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = v[j] > 0.0f ? __builtin_fmaxf(y[j], kMinCode) : y[j];
+    for (int j = 0; j < 8; ++j) {
+      y[j] = v[j] * inv_v[L::block_of(j)];
+      if (run.round_sr) y[j] = e4m3_stochastic(y[j], z[j >> 2], j & 3);
+      y[j] = v[j] > 0.0f ? __builtin_fmaxf(y[j], kMinCode) : y[j];
+    }
+    ov[0] = e4m3_pack4(y);
+    ov[1] = e4m3_pack4(y + 4);
   }
-  const uint32_t ov[2] = {e4m3_pack4(y), e4m3_pack4(y + 4)};
   at.store_u8(vp, ov);
 #pragma unroll
   for (int b = 0; b < L::kBlocks; ++b)
