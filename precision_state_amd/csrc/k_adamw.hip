@@ -533,15 +533,20 @@ __device__ __forceinline__ void add_squares(const float* g, double* s) {
   for (int j = 0; j < 8; ++j) s[j & 3] = __builtin_fma((double)g[j], (double)g[j], s[j & 3]);
 }
 
+template <bool KEEP, class V>
+__device__ __forceinline__ V ld_norm(gptr p) {
+  return KEEP ? *(const GLOBAL V*)p : ld_nt<V>(p);
+}
+
 // A whole chunk's squares: every load is under way before the first is used,
-// and `meanwhile` runs while they are.
-template <class F>
+// and `meanwhile` runs while they are. KEEP: the loads may stay in the caches.
+template <bool KEEP, class F>
 __device__ __forceinline__ void chunk_squares(gptr p, bool f32, bool half, double* s, F meanwhile) {
   constexpr int kLoads = kNormChunk / (8 * kNormThreads);   // of 8 elements
   if (f32) {
     f32x4 x[2 * kLoads];
 #pragma unroll
-    for (int k = 0; k < 2 * kLoads; ++k) x[k] = ld_nt<f32x4>(p + (threadIdx.x * 16u + k * (16u * kNormThreads)));
+    for (int k = 0; k < 2 * kLoads; ++k) x[k] = ld_norm<KEEP, f32x4>(p + (threadIdx.x * 16u + k * (16u * kNormThreads)));
     meanwhile();
 #pragma unroll
     for (int k = 0; k < kLoads; ++k) {
@@ -552,7 +557,7 @@ __device__ __forceinline__ void chunk_squares(gptr p, bool f32, bool half, doubl
   } else {
     u32x4 x[kLoads];
 #pragma unroll
-    for (int k = 0; k < kLoads; ++k) x[k] = ld_nt<u32x4>(p + (threadIdx.x * 16u + k * (16u * kNormThreads)));
+    for (int k = 0; k < kLoads; ++k) x[k] = ld_norm<KEEP, u32x4>(p + (threadIdx.x * 16u + k * (16u * kNormThreads)));
     meanwhile();
 #pragma unroll
     for (int k = 0; k < kLoads; ++k) {
@@ -587,14 +592,20 @@ __device__ __forceinline__ Chunk norm_chunk(const AwNormTable& t, uint32_t chunk
 // the partial sums, in index order whichever it is, and writes the control
 // block, so that there is one launch.
 //
+// The gradients' last kNormKeepBytes are read without the non-temporal hint and
+// stay in the last-level cache; the step, whose own streams carry the hint,
+// finds them there (norm and step of a 202M layer with e4m3 moments: 576, 560, 553
+// and 549 us for 0, 128, 192 and 256 MiB). The others carry it: without any the norm
+// of 514M fp32 gradients takes 335 us, with all 296, with these 299.
+//
 // The last one is found by counting: each workgroup counts on one of kNormCounts
 // addresses, the last of those on a common one. (An address takes about 10 ns
 // for a count: 2048 workgroups on a single one took 36 us for 42M bf16 gradients,
 // a second launch for the sum 18.0 us, this 17.8 us, and 17.2 us with 1024
 // workgroups of equal shares; 64 tensors of 8192 5.3, 7.0 and 4.9 us.) A chunk's
 // record is looked up while the loads of the one before are under way: 16.9 us,
-// and 296 us (6.9 TB/s) for 514M fp32 gradients, 301 us without. Partial sums and
-// counts cross XCDs: they go through agent-scope atomics, which write through
+// and 296 us for 514M fp32 gradients, 301 us without. Partial sums and counts
+// cross XCDs: they go through agent-scope atomics, which write through
 // the XCD's L2, and a workgroup counts when its partial sum has arrived (a
 // release per workgroup, which writes the whole L2 back, cost 70 us more). The
 // last workgroup sets the counts back to 0.
@@ -605,12 +616,16 @@ __global__ __launch_bounds__(kNormThreads) void k_grad_norm(AwNormTable t, doubl
   Chunk at = norm_chunk(t, chunk);
   while (chunk < t.chunks) {
     const Chunk now = at;
+    const bool keep = chunk >= t.keep_from;
     chunk += gridDim.x;
     auto next = [&] { at = norm_chunk(t, chunk); };
     const bool f32 = now.gtype == PS_TYPE_F32, half = now.gtype == PS_TYPE_F16;
     const gptr p = now.p;
     if (now.left == kNormChunk) {
-      chunk_squares(p, f32, half, s, next);
+      if (keep)
+        chunk_squares<true>(p, f32, half, s, next);
+      else
+        chunk_squares<false>(p, f32, half, s, next);
       continue;
     }
     next();

@@ -13,6 +13,7 @@ constexpr int kAwItemElems = 512;     // step work item: one 64-lane wave, 8 ele
 constexpr uint32_t kAwMaxItems = 0xFFFFFFFFu / 64;   // a launch has fewer than 2^32 lanes
 constexpr int kNormChunk = 8192;      // norm work item: one 256-thread workgroup, 32 elements per thread
 constexpr uint32_t kNormMaxWg = 1024;      // norm workgroups (and partial sums) at most
+constexpr int64_t kNormKeepBytes = 256 << 20;   // the last-level cache's size
 constexpr uint32_t kNormCounts = 32;      // first-level counts of finished norm workgroups
 constexpr uint32_t kNormCountStride = 64; // words from one to the next: each on a cache line of its own
 constexpr int kAwGrads = 384;         // gradient pointers in one k_set_grads launch
@@ -52,6 +53,8 @@ struct AwNormTable {
   const uint32_t* chunk_end;
   int32_t n;
   uint32_t chunks;
+  uint32_t keep_from;  // chunks from here on are read so that they stay in the last-level cache
+  uint32_t pad;
 };
 
 // Scalars of one group, by value in the kernel arguments or, when the step is
