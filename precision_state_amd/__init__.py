@@ -493,21 +493,22 @@ def _adamw_record(i, t):
         raise wrong("param and grad are both None")
     n = ref.numel()
     types = {torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16, torch.float16: TYPE_F16}
-    nb, device, ptr = (n + BLOCK - 1) // BLOCK, ref.device, {}
-    for name, x, size in (("param", t.param, n), ("grad", t.grad, n), ("m", t.m, n), ("v", t.v, n),
-                          ("residual", t.residual, n), ("copy", t.copy, n), ("m_scale", t.m_scale, nb),
-                          ("v_scale", t.v_scale, nb)):
+    nb, device = (n + BLOCK - 1) // BLOCK, ref.get_device()
+
+    def ptr(name, x, size):
         if x is None:
-            continue
+            return None
         if x.numel() != size:
             raise wrong(f"{name} has {x.numel()} elements, not {size}")
         if not x.is_contiguous():
             raise wrong(f"{name} is not contiguous")
-        if x.device != device:
-            raise wrong(f"{name} is on {x.device}, not on {device}")
-        if size:
-            ptr[name] = x.data_ptr()
-    rec = CAdamWTensor(numel=n, group=t.group, **ptr)
+        if x.get_device() != device:
+            raise wrong(f"{name} is on {x.device}, not on {ref.device}")
+        return x.data_ptr() if size else None
+    rec = CAdamWTensor(ptr("param", t.param, n), ptr("residual", t.residual, n), ptr("copy", t.copy, n),
+                       ptr("grad", t.grad, n), ptr("m", t.m, n), ptr("m_scale", t.m_scale, nb), ptr("v", t.v, n),
+                       ptr("v_scale", t.v_scale, nb), n)
+    rec.group = t.group
     if t.grad is not None:
         if t.grad.dtype not in types:
             raise wrong(f"grad has dtype {t.grad.dtype}")
