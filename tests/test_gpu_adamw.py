@@ -347,6 +347,23 @@ def test_norm_of_extreme_values_and_repeatability():
         assert abs(float(plan.grad_mul) - min(1.0, 1.0 / (want + 1e-6))) <= max(HALF * float(plan.grad_mul) * 1.001, 2.0 ** -149)
 
 
+@pytest.mark.parametrize("sizes", [[700], [8192 * 40 + 5], [3_000_001, 5, 6_000_000], [4_000_000] * 5])
+def test_norms_in_a_row_see_their_own_gradients(sizes):
+    """Many calls with nothing between them but an exact doubling or halving of the gradients: every norm is the first one
+    or its double, so no call reads a partial sum of the one before."""
+    rng = np.random.default_rng(55)
+    gs = [torch.from_numpy(rng.normal(0, 1e-3, n).astype(np.float32)).cuda() for n in sizes]
+    plan = ps.AdamWPlan([ps.AdamWTensor(None, g) for g in gs])
+    seen = torch.zeros(400, device="cuda")
+    for i in range(400):
+        plan.grad_norm(1.0)
+        seen[i].copy_(plan.norm)
+        for g in gs:
+            g.mul_(0.5 if i % 2 else 2.0)
+    seen = seen.cpu().numpy()
+    assert np.all(seen[0::2] == seen[0]) and np.all(seen[1::2] == 2 * seen[0])
+
+
 def test_norm_of_nothing():
     plan = ps.AdamWPlan([])
     plan.grad_norm(1.0)
