@@ -600,7 +600,8 @@ __device__ __forceinline__ Chunk norm_chunk(const AwNormTable& t, uint32_t chunk
 // stay in the last-level cache; the step, whose own streams carry the hint,
 // finds them there (norm and step of a 202M layer with e4m3 moments: 576, 560, 553
 // and 549 us for 0, 128, 192 and 256 MiB). The others carry it: without any the norm
-// of 514M fp32 gradients takes 335 us, with all 296, with these 299.
+// of 514M fp32 gradients takes 335 us, with all 296, with these 299; 42M bf16
+// gradients, which are all kept, take 18 us for the 16.9 below.
 //
 // The last one is found by counting: each workgroup counts on one of kNormCounts
 // addresses, the last of those on a common one. (An address takes about 10 ns
