@@ -555,8 +555,10 @@ def _adamw_record(i, t):
 class AdamWPlan:
     """AdamW over a fixed list of tensors, and the norm of their gradients
     (ps_adamw_*). Made once; every call then runs on the plan's device, on
-    `stream` or the device's current stream, with no allocation. The plan keeps
-    its tensors alive; a graph that captured its calls needs the plan.
+    `stream` or the device's current stream, with no allocation. Until it is
+    closed the plan keeps the memory of its tensors alive, by references of its
+    own: it neither changes the records nor reads them again (set_grads gives it
+    other gradients). A graph that captured its calls needs the plan.
 
     The control block's fields are 0-dim tensors in device memory, read and
     written in stream order: norm, grad_mul, skip, skipped, step, lr_mul."""
@@ -585,7 +587,12 @@ class AdamWPlan:
             _check(_lib.ps_adamw_plan_create(arr, len(recs), self.workspace.data_ptr(), size.value, self._stream0,
                                              ctypes.byref(h)))
         self._h = h
-        self._tensors = tensors          # the arrays live as long as the plan
+        # The plan's own references to the memory that its device tables address: what becomes of the caller's records
+        # and tensors (another gradient, another storage) does not free it.
+        self._arrays = [x.detach() for t in tensors
+                        for x in (t.param, t.residual, t.copy, t.m, t.m_scale, t.v, t.v_scale) if x is not None]
+        self._grads = [None if t.grad is None else t.grad.detach() for t in tensors]
+        self._captured = []              # gradients of captured set_grads calls
         ctl = self.workspace[:ctypes.sizeof(CAdamWControl)]
 
         def field(name, dtype):
@@ -613,8 +620,17 @@ class AdamWPlan:
                 status = f(self._h, *args)
         _check(status)
 
+    def _is_capturing(self, stream, raw):
+        with _on(self.device):
+            if stream is None or raw == _current_raw_stream(self._index):
+                return torch.cuda.is_current_stream_capturing()
+            with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else
+                                   torch.cuda.ExternalStream(raw, device=self.device)):
+                return torch.cuda.is_current_stream_capturing()
+
     def set_grads(self, grads, stream=None):
-        """New gradients for all tensors, in list order; None: the tensor is passed by."""
+        """New gradients for all tensors, in list order; None: the tensor is passed by. The plan keeps them alive
+        in place of the ones before; gradients of a captured call, which replays set again, as long as it lives."""
         if len(grads) != len(self._sizes):
             raise ValueError(f"{len(grads)} gradients for {len(self._sizes)} tensors")
         types = (torch.float32, torch.bfloat16, torch.float16)
@@ -627,8 +643,14 @@ class AdamWPlan:
             arr[i] = g.data_ptr()
         raw = self._on_stream(stream)
         self._run(_lib.ps_adamw_set_grads, arr, len(grads), raw)
-        for t, g in zip(self._tensors, grads):
-            t.grad = g
+        if self._is_capturing(stream, raw):          # the tables change when the graph runs
+            self._captured += [g.detach() for g in grads if g is not None]
+            return
+        for i, (old, g) in enumerate(zip(self._grads, grads)):
+            if g is None:
+                self._grads[i] = None
+            elif old is None or old.data_ptr() != arr[i]:
+                self._grads[i] = g.detach()
 
     def grad_norm(self, max_norm=float("inf"), grad_scale=1.0, stream=None):
         """The gradients' global 2-norm and clip factor into the control block (ps_adamw_grad_norm)."""
@@ -646,6 +668,7 @@ class AdamWPlan:
     def close(self):
         if self._h:
             h, self._h = self._h, None
+            self._arrays, self._grads, self._captured = [], [], []
             _check(_lib.ps_adamw_plan_destroy(h))
 
     def __del__(self):
