@@ -558,7 +558,9 @@ class AdamWPlan:
     `stream` or the device's current stream, with no allocation. Until it is
     closed the plan keeps the memory of its tensors alive, by references of its
     own: it neither changes the records nor reads them again (set_grads gives it
-    other gradients). A graph that captured its calls needs the plan.
+    other gradients). A graph that captured its calls needs the plan. What is
+    released after calls on another stream is recorded on it, so a stream given
+    as an integer has to exist as long as the plan.
 
     The control block's fields are 0-dim tensors in device memory, read and
     written in stream order: norm, grad_mul, skip, skipped, step, lr_mul."""
@@ -593,6 +595,7 @@ class AdamWPlan:
                         for x in (t.param, t.residual, t.copy, t.m, t.m_scale, t.v, t.v_scale) if x is not None]
         self._grads = [None if t.grad is None else t.grad.detach() for t in tensors]
         self._captured = []              # gradients of captured set_grads calls
+        self._streams = {}               # those that the plan ran on, by their integers
         ctl = self.workspace[:ctypes.sizeof(CAdamWControl)]
 
         def field(name, dtype):
@@ -607,11 +610,23 @@ class AdamWPlan:
         if not self._h:
             raise ValueError("the plan is closed")
         raw = _current_raw_stream(self._index) if stream is None else _raw_stream(self.device, stream)
-        if raw != self._stream0 and not torch.cuda.is_current_stream_capturing():
-            # the allocator must not hand the workspace out before this stream is done with it
-            self.workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
-                                         torch.cuda.ExternalStream(raw, device=self.device))
+        if raw not in self._streams:
+            self._streams[raw] = self._stream_object(stream, raw)
         return raw
+
+    def _stream_object(self, stream, raw):
+        if isinstance(stream, torch.cuda.Stream):
+            return stream
+        if raw == 0:    # ExternalStream(0) would be a new stream
+            return torch.cuda.default_stream(self.device)
+        return torch.cuda.ExternalStream(raw, device=self.device)
+
+    def _release(self, arrays):
+        """Before the plan lets arrays go: the allocator must not hand their memory out before the streams that the
+        plan ran on are done with it."""
+        for stream in self._streams.values():
+            for x in arrays:
+                x.record_stream(stream)
 
     def _run(self, f, *args):
         status = f(self._h, *args)
@@ -624,8 +639,7 @@ class AdamWPlan:
         with _on(self.device):
             if stream is None or raw == _current_raw_stream(self._index):
                 return torch.cuda.is_current_stream_capturing()
-            with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else
-                                   torch.cuda.ExternalStream(raw, device=self.device)):
+            with torch.cuda.stream(self._stream_object(stream, raw)):
                 return torch.cuda.is_current_stream_capturing()
 
     def set_grads(self, grads, stream=None):
@@ -646,11 +660,14 @@ class AdamWPlan:
         if self._is_capturing(stream, raw):          # the tables change when the graph runs
             self._captured += [g.detach() for g in grads if g is not None]
             return
+        released = []
         for i, (old, g) in enumerate(zip(self._grads, grads)):
-            if g is None:
-                self._grads[i] = None
-            elif old is None or old.data_ptr() != arr[i]:
-                self._grads[i] = g.detach()
+            if g is not None and old is not None and old.data_ptr() == arr[i]:
+                continue
+            if old is not None:
+                released.append(old)
+            self._grads[i] = None if g is None else g.detach()
+        self._release(released)
 
     def grad_norm(self, max_norm=float("inf"), grad_scale=1.0, stream=None):
         """The gradients' global 2-norm and clip factor into the control block (ps_adamw_grad_norm)."""
@@ -668,6 +685,7 @@ class AdamWPlan:
     def close(self):
         if self._h:
             h, self._h = self._h, None
+            self._release(self._arrays + [g for g in self._grads if g is not None] + self._captured + [self.workspace])
             self._arrays, self._grads, self._captured = [], [], []
             _check(_lib.ps_adamw_plan_destroy(h))
 

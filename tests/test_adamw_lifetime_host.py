@@ -65,7 +65,7 @@ class Entries:
 
 
 class FakeStream:
-    def __init__(self, raw, device=None):
+    def __init__(self, raw):
         self.cuda_stream = raw
 
 
@@ -82,7 +82,12 @@ def entries(monkeypatch):
 
         def __exit__(self, *exc):
             e.current = self.old
-    cuda = types.SimpleNamespace(current_device=lambda: 0, Stream=FakeStream, ExternalStream=FakeStream, stream=on_stream,
+
+    def external(raw, device):
+        assert raw != 0                                     # torch makes a new stream of a 0
+        return FakeStream(raw)
+    cuda = types.SimpleNamespace(current_device=lambda: 0, Stream=FakeStream, ExternalStream=external,
+                                 default_stream=lambda device: FakeStream(0), stream=on_stream,
                                  is_current_stream_capturing=lambda: e.current in e.capturing)
 
     class FakeTorch:
@@ -175,3 +180,42 @@ def test_gradients_of_a_captured_call_live_as_long_as_the_plan(entries):
     entries.capturing.clear()
     del plan
     assert gone(captured_ref, captured_ref2, later_ref) == [True] * 3
+
+
+def test_released_arrays_are_recorded_on_the_plans_streams(entries):
+    """The allocator must not hand out what the plan lets go before the streams that the plan ran on are done with it."""
+    rec, _ = record()
+    plan = ps.AdamWPlan([rec])
+    first, kept = rec.grad.data_ptr(), [x.data_ptr() for x in (rec.param, rec.m, rec.v)]
+    hp = [ps.HParams(algo=ps.ALGO_ADAM)]
+    plan.grad_norm(stream=FakeStream(5))
+    plan.step(hp, 1, stream=6)
+    assert OnGpu.recorded == []                             # nothing has been released
+    second, _ = array(300)
+    plan.set_grads([second])                                # on stream 0
+    assert sorted(OnGpu.recorded) == [(first, 0), (first, 5), (first, 6)]
+    OnGpu.recorded.clear()
+    plan.set_grads([second])                                # the same array: kept
+    assert OnGpu.recorded == []
+    workspace = plan.workspace.data_ptr()
+    plan.close()
+    assert sorted(OnGpu.recorded) == sorted((p, s) for p in kept + [second.data_ptr(), workspace] for s in (0, 5, 6))
+    OnGpu.recorded.clear()
+    plan.close()
+    assert OnGpu.recorded == []
+
+
+def test_a_plan_that_is_let_go_records_its_arrays(entries):
+    rec, _ = record()
+    plan = ps.AdamWPlan([rec])
+    entries.current = 9
+    plan.step([ps.HParams(algo=ps.ALGO_ADAM)], 1)
+    captured, _ = array(300)
+    entries.capturing.add(9)
+    plan.set_grads([captured])
+    entries.capturing.clear()
+    workspace = plan.workspace.data_ptr()
+    del plan
+    gc.collect()
+    arrays = [x.data_ptr() for x in (rec.param, rec.grad, rec.m, rec.v, captured)]
+    assert sorted(OnGpu.recorded) == sorted((p, 9) for p in arrays + [workspace])

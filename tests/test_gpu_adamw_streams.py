@@ -1,0 +1,68 @@
+"""GPU test of what an AdamW plan releases while another stream still works on
+it: the caching allocator must not hand it out yet."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+
+import precision_state_amd as ps  # noqa: E402
+
+N = 5_000_000   # a size of its own in the allocator's cache
+
+
+def fresh(*sizes):
+    return [torch.zeros(n, device="cuda") for n in sizes]
+
+
+def pointers_handed_out(n, count):
+    """The next allocations of n floats on the current stream (after a first call they come from the cache)."""
+    taken = [torch.empty(n, device="cuda") for _ in range(count)]
+    return {x.data_ptr() for x in taken}
+
+
+@pytest.mark.parametrize("how", ["stream", "integer", "current"])
+def test_released_arrays_wait_for_the_stream_that_uses_them(how):
+    hp = [ps.HParams(algo=ps.ALGO_ADAM, lr=1e-3)]
+    side = torch.cuda.Stream()
+    w, g, m, v = fresh(N, N, N, N)
+    g.fill_(1e-3)
+    plan = ps.AdamWPlan([ps.AdamWTensor(w, g, m, v)])
+    torch.cuda.synchronize()
+    pointers_handed_out(N, 8)
+    old, state = g.data_ptr(), {x.data_ptr() for x in (w, m, v)}
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)                      # about 0.1 s before the step on this stream
+    new = torch.full((N,), 1e-3, device="cuda")
+    torch.cuda.current_stream().synchronize()
+    kw = {"stream": dict(stream=side), "integer": dict(stream=side.cuda_stream), "current": {}}[how]
+    with torch.cuda.stream(side if how == "current" else torch.cuda.current_stream()):
+        plan.step(hp, 1, **kw)
+        plan.set_grads([new], **kw)
+        plan.step(hp, 2, **kw)
+    del g
+    assert old not in pointers_handed_out(N, 3)
+    assert not side.query()                                 # its work was still to come
+    del w, m, v, plan
+    assert not state & pointers_handed_out(N, 4)
+    assert not side.query()
+    side.synchronize()
+
+
+def test_a_plan_made_on_a_side_stream_and_run_on_the_default_one():
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        w, g, m, v = fresh(N, N, N, N)
+        plan = ps.AdamWPlan([ps.AdamWTensor(w, g, m, v)])
+        pointers_handed_out(N, 8)
+    side.synchronize()
+    state = {x.data_ptr() for x in (w, g, m, v)} | {plan.workspace.data_ptr()}
+    torch.cuda._sleep(200_000_000)
+    plan.step([ps.HParams(algo=ps.ALGO_ADAM, lr=1e-3)], 1)
+    del w, g, m, v, plan
+    with torch.cuda.stream(side):
+        assert not state & pointers_handed_out(N, 5)
+    assert not torch.cuda.current_stream().query()
+    torch.cuda.synchronize()
