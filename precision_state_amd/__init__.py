@@ -414,10 +414,16 @@ def _raw_stream(device, stream):
     return _current_raw_stream(device.index)
 
 
+# What holds e4m3 codes: the type itself, or plain bytes. Other 8-bit floats are other values.
+_E4M3_DTYPES = () if torch is None else (torch.float8_e4m3fn, torch.uint8, torch.int8)
+
+
 def _fp8_check(x, code, scale):
     n = x.numel()
-    if x.dtype != torch.float32 or scale.dtype != torch.float32 or code.element_size() != 1:
-        raise ValueError("x and scale are float32, code has 1-byte elements")
+    if x.dtype != torch.float32 or scale.dtype != torch.float32:
+        raise ValueError("x and scale are float32")
+    if code.dtype not in _E4M3_DTYPES:
+        raise ValueError(f"code has dtype {code.dtype}, not float8_e4m3fn, uint8 or int8")
     if code.numel() != n or scale.numel() != (n + BLOCK - 1) // BLOCK:
         raise ValueError("code needs x's size and scale one value for each 256 of them")
     if not (x.is_contiguous() and code.is_contiguous() and scale.is_contiguous()):
@@ -432,7 +438,7 @@ def _fp8_check(x, code, scale):
 
 def encode_fp8(x, code, scale, kind, stream=None):
     """float32 moments -> e4m3 codes and a power-of-two scale for each 256 (ps_encode_fp8); kind MOMENT_UNSIGNED
-    codes the square root. code: any 1-byte dtype, torch.float8_e4m3fn among them."""
+    codes the square root. code: torch.float8_e4m3fn, or its bytes as uint8 or int8."""
     n, device = _fp8_check(x, code, scale)
     with _on(device):
         _check(_lib.ps_encode_fp8(x.data_ptr(), code.data_ptr(), scale.data_ptr(), n, kind, _raw_stream(device, stream)))
@@ -470,8 +476,8 @@ class AdamWTensor:
     param: float32, or bfloat16 (any other 2-byte dtype is read as bf16 bits);
     None if only the gradient's norm is wanted. grad: float32, bfloat16 or
     float16, or None; grad_dtype says what a later one will be (param's dtype if
-    not given). m, v: float32, or a 1-byte dtype (e4m3 codes) with m_scale
-    and v_scale. residual: a bf16 parameter's low halves. copy: bfloat16 or
+    not given). m, v: float32, or e4m3 codes (float8_e4m3fn, or their bytes as
+    uint8 or int8) with m_scale and v_scale. residual: a bf16 parameter's low halves. copy: bfloat16 or
     float16, written with a float32 parameter's new values."""
     param: object
     grad: object
@@ -541,7 +547,7 @@ def _adamw_record(i, t):
         rec.state_type = STATE_F32
         if t.m_scale is not None or t.v_scale is not None:
             raise wrong("float32 moments have no scales")
-    elif t.m.element_size() == 1 and t.v.element_size() == 1:
+    elif t.m.dtype in _E4M3_DTYPES and t.v.dtype in _E4M3_DTYPES:
         rec.state_type = STATE_E4M3
         if t.m_scale is None or t.v_scale is None:
             raise wrong("e4m3 moments need m_scale and v_scale")

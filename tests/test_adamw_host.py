@@ -181,6 +181,31 @@ def test_binding_refuses_wrong_tensors(ps):
             ps.decode_fp8(c, s, x, 0)
 
 
+@pytest.mark.parametrize("dtype", ["float8_e4m3fnuz", "float8_e5m2", "float8_e5m2fnuz", "float8_e8m0fnu", "bool"])
+def test_binding_refuses_bytes_that_are_no_e4m3_codes(ps, dtype):
+    """Other 8-bit floats have another bias or other places; their bytes would be moments of other values."""
+    torch = pytest.importorskip("torch")
+    f = lambda n, dt=torch.float32: torch.zeros(n, dtype=dt)  # noqa: E731
+    other, code = f(8, torch.uint8).view(getattr(torch, dtype)), f(8, torch.uint8)
+    for m, v in ((other, code), (code, other), (other, other)):
+        with pytest.raises(ValueError, match="dtype"):
+            ps.AdamWPlan([ps.AdamWTensor(f(8), f(8), m, v, f(1), f(1))])
+    for call in (lambda: ps.encode_fp8(f(8), other, f(1), 0), lambda: ps.decode_fp8(other, f(1), f(8), 0)):
+        with pytest.raises(ValueError, match="dtype"):
+            call()
+
+
+@pytest.mark.parametrize("dtype", ["float8_e4m3fn", "uint8", "int8"])
+def test_binding_takes_e4m3_codes_and_plain_bytes(ps, dtype):
+    torch = pytest.importorskip("torch")
+    f = lambda n, dt=torch.float32: torch.zeros(n, dtype=dt)  # noqa: E731
+    code = f(8, torch.uint8).view(getattr(torch, dtype))
+    with pytest.raises(ValueError, match="not on a GPU"):
+        ps.AdamWPlan([ps.AdamWTensor(f(8), f(8), code, code.clone(), f(1), f(1))])
+    with pytest.raises(ValueError, match="not on a GPU"):
+        ps.decode_fp8(code, f(1), f(8), 0)
+
+
 # ---- the numpy reference itself ----
 
 def test_reference_codes_equal_torch():
