@@ -388,8 +388,8 @@ ps_status ps_adamw_workspace_size(const ps_adamw_tensor* tensors, int32_t n_tens
  * the plan is destroyed and its last run has ended). Ordered on `stream`,
  * which it synchronizes; PS_ERR_UNSUPPORTED while `stream` is being captured.
  * The list itself is not kept. Arrays that are written (param, residual, copy,
- * moments, scales) must not overlap each other or a gradient
- * (PS_ERR_INVALID_ARG); gradients may. */
+ * moments, scales) must not overlap each other, a gradient or the workspace,
+ * nor a gradient the workspace (PS_ERR_INVALID_ARG); gradients may overlap. */
 ps_status ps_adamw_plan_create(const ps_adamw_tensor* tensors, int32_t n_tensors, void* workspace,
                                size_t workspace_bytes, ps_stream_t stream, ps_adamw_plan** plan);
 

@@ -39,7 +39,8 @@ struct ps_adamw_plan {
   AwTable table[kAwKinds] = {};
   uint32_t items[kAwKinds] = {};
   AwNormTable norm = {};
-  std::vector<Range> written;   // sorted
+  uintptr_t ws_lo = 0, ws_hi = 0;   // the workspace's bytes
+  std::vector<Range> written;       // sorted
   std::vector<Grad> grads;
   int32_t max_group = -1;
   bool any_bf16 = false, lacks_residual = false;
@@ -172,6 +173,7 @@ ps_status check_grad(const ps_adamw_plan& p, const void* g, int32_t i) {
   if (!g || p.grads[i].n == 0) return PS_OK;
   if (ps_status s = check(g, "grad", i, 16)) return s;
   const uintptr_t lo = (uintptr_t)g, hi = lo + (uintptr_t)(p.grads[i].n * elem_size(p.grads[i].type));
+  if (lo < p.ws_hi && p.ws_lo < hi) return fail(PS_ERR_INVALID_ARG, "tensor %d: grad overlaps the workspace", i);
   // the first written range that ends behind lo
   auto it = std::upper_bound(p.written.begin(), p.written.end(), lo, [](uintptr_t a, const auto& r) { return a < r.hi; });
   if (it != p.written.end() && it->lo < hi)
@@ -203,14 +205,15 @@ ps_status create(const ps_adamw_tensor* t, int32_t n, void* workspace, size_t wo
   ps_adamw_plan tmp;
   if (ps_status s = written_ranges(t, n, tmp.written)) return s;
   for (int32_t i = 0; i < n; ++i) tmp.grads.push_back({t[i].numel, t[i].grad_type});
+  tmp.ws_lo = (uintptr_t)workspace;
+  tmp.ws_hi = tmp.ws_lo + l.bytes;
   for (int32_t i = 0; i < n; ++i)
     if (ps_status s = check_grad(tmp, t[i].grad, i)) return s;
   if (!workspace || workspace_bytes < l.bytes)
     return fail(PS_ERR_WORKSPACE, "workspace is %zu bytes, %zu are needed", workspace ? workspace_bytes : (size_t)0, l.bytes);
   if (!is_aligned(workspace, 256)) return fail(PS_ERR_ALIGNMENT, "workspace is not 256-byte aligned");
-  const uintptr_t wlo = (uintptr_t)workspace, whi = wlo + l.bytes;
   for (const auto& r : tmp.written)
-    if (r.lo < whi && wlo < r.hi)
+    if (r.lo < tmp.ws_hi && tmp.ws_lo < r.hi)
       return fail(PS_ERR_INVALID_ARG, "the workspace overlaps an array of tensor %d", r.tensor);
 
   std::vector<unsigned char> image(l.bytes, 0);

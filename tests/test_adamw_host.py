@@ -127,6 +127,16 @@ def test_workspace_inside_an_array_is_refused(ps):
     assert "workspace" in ps.last_error()
 
 
+@pytest.mark.parametrize("grad,refused", [((1 << 30) + 256, True), ((1 << 30) - 1008, True), ((1 << 30) - 2000, False)])
+def test_gradients_inside_the_workspace_are_refused(ps, grad, refused):
+    """1000 bf16 gradients behind, across and before the workspace's start; also where only the gradient counts. The
+    second tensor has a fault of its own, found later, so that no list gets to a device call."""
+    later = _rec(ps, param=(1 << 30) + 4096, m=9 << 20, v=10 << 20)
+    for first in (_rec(ps, grad=grad), _rec(ps, grad=grad, param=0)):
+        assert _create(ps, [first, later])[0] == 1
+        assert ("grad overlaps the workspace" if refused else "the workspace overlaps an array of tensor 1") in ps.last_error()
+
+
 def test_calls_without_a_plan_are_refused(ps):
     L = ps.lib()
     h = ps.HParams().c()

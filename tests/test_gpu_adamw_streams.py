@@ -1,5 +1,5 @@
-"""GPU test of what an AdamW plan releases while another stream still works on
-it: the caching allocator must not hand it out yet."""
+"""GPU tests of the memory around an AdamW plan: what it releases while another
+stream still works on it, and gradients inside its workspace."""
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -66,3 +66,14 @@ def test_a_plan_made_on_a_side_stream_and_run_on_the_default_one():
         assert not state & pointers_handed_out(N, 5)
     assert not torch.cuda.current_stream().query()
     torch.cuda.synchronize()
+
+
+def test_gradients_inside_the_workspace_are_refused():
+    w, g, m, v = fresh(64, 64, 64, 64)
+    plan = ps.AdamWPlan([ps.AdamWTensor(w, g, m, v)])
+    inside = plan.workspace[256:512].view(torch.float32)
+    with pytest.raises(ps.PSError, match="grad overlaps the workspace"):
+        plan.set_grads([inside])
+    g.fill_(2.0)
+    plan.grad_norm()                                        # the gradients from before still count
+    assert float(plan.norm) == 16.0
