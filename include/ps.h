@@ -331,9 +331,9 @@ enum { PS_ROUND_NEAREST = 0, PS_ROUND_STOCHASTIC = 1 };
  *   grad      array of grad_type, read only; NULL: the tensor is passed by
  *             (a later ps_adamw_set_grads may give it one)
  *   m, v      moments (state_type); m_scale, v_scale: PS_STATE_E4M3 only,
- *             ceil(numel / 256) floats, powers of two as ps_encode_fp8 makes
- *             them (the step reads their exponents only). All bytes zero is a
- *             fresh state
+ *             ceil(numel / 256) floats. A moment is what ps_decode_fp8 makes of
+ *             its code and scale; a step writes scales as ps_encode_fp8 does.
+ *             All bytes zero is a fresh state
  *   group     index of the tensor's hyperparameters in ps_adamw_step's groups
  * A tensor with numel == 0 is passed by and its pointers are not read. */
 typedef struct ps_adamw_tensor {

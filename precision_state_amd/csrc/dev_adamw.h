@@ -32,14 +32,7 @@ __device__ __forceinline__ uint32_t e4m3_pack4(const float* y) {
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], lo, true);
 }
 
-// The same with a power-of-two scale in the conversion: codes times s, and
-// codes of x / s.
-__device__ __forceinline__ void e4m3_unpack4(uint32_t c, float s, float* d) {
-  const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c, s, false),
-              b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c, s, true);
-  d[0] = a.x; d[1] = a.y; d[2] = b.x; d[3] = b.y;
-}
-
+// Codes of x / s, the power-of-two scale s in the conversion.
 __device__ __forceinline__ uint32_t e4m3_pack4(const float* x, float s) {
   i16x2 c = {0, 0};
   c = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(c, x[0], x[1], s, false);

@@ -294,13 +294,21 @@ __device__ __forceinline__ void adamw_item(const AwRec& T, int64_t elem0, uint32
 
   if (!G32) unpack<8>(gw, T.gtype == PS_TYPE_F16, g);
   if (E8) {
+    // The whole scale counts, as in ps_decode_fp8: the conversion that takes a
+    // scale reads only its exponent. (It saves 0.3 of 75.1 us for 42M weights and
+    // second moments rounded stochastically, and nothing for the other kinds.)
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      e4m3_unpack4(mc[q], ms[L::block_of(4 * q)], m + 4 * q);
-      e4m3_unpack4(vc[q], vs[L::block_of(4 * q)], v + 4 * q);
+      e4m3_unpack4(mc[q], m + 4 * q);
+      e4m3_unpack4(vc[q], v + 4 * q);
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = v[j] * v[j];
+    for (int j = 0; j < 8; ++j) {
+      const int b = L::block_of(j);
+      m[j] = m[j] * ms[b];
+      const float r = v[j] * vs[b];
+      v[j] = r * r;
+    }
   }
 
   // Moments, and what decides whether the fast square root and quotient hold

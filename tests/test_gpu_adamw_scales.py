@@ -1,5 +1,6 @@
 """GPU tests of the AdamW step on 8-bit moments at the ends of their scales'
-range, bit for bit against the formulas in float32."""
+range and with scales that ps_encode_fp8 would not make, bit for bit against the
+formulas in float32."""
 import numpy as np
 import pytest
 
@@ -82,3 +83,29 @@ def test_stored_codes_at_the_scales_floor(gradient, split):
         put(p, m=code | (rng.integers(0, 2, p.n) << 7).astype(np.uint8), v=rng.permutation(code),
             ms=np.full(nb, 2.0 ** -126, np.float32), vs=(2.0 ** rng.integers(-90, -60, nb)).astype(np.float32))
     steps(params, lambda n: (rng.normal(0, 1, n) * gradient).astype(np.float32), 0, 1, split)
+
+
+@pytest.mark.parametrize("algo,rounding,split", [(0, 0, 0), (1, 1, 0), (0, 1, 2), (1, 0, 2)])
+def test_scales_that_are_no_powers_of_two(algo, rounding, split):
+    """A moment is its code times its scale, the one that ps_decode_fp8 gives, whoever made the scale."""
+    rng = np.random.default_rng(62)
+    params = build(rng)
+    for p in params:
+        nb = ref.blocks_of(p.n)
+        put(p, ms=(p.ms * rng.uniform(1, 2, nb)).astype(np.float32), vs=(p.vs * rng.uniform(1, 2, nb)).astype(np.float32))
+        for code, scale, kind, want in ((p.m, "ms", ps.MOMENT_SIGNED, p.moments()[0]), (p.v, "vs", ps.MOMENT_UNSIGNED, p.moments()[1])):
+            x = torch.empty(p.n, device="cuda")
+            ps.decode_fp8(torch.from_numpy(code).cuda(), p.d[scale].t, x, kind)
+            assert np.array_equal(x.cpu().numpy(), want)
+    steps(params, lambda n: rng.normal(0, 1e-3, n).astype(np.float32), algo, rounding, split)
+
+
+def test_scales_of_zero_and_extreme_size():
+    """Zero scales (a fresh state's, with codes left in place), subnormal and the largest ones."""
+    rng = np.random.default_rng(63)
+    params = build(rng)
+    for p in params:
+        nb = ref.blocks_of(p.n)
+        level = np.array([0.0, 1e-45, 1e-40, 2.0 ** -127, 3e-38, 1.0, 3e16, 2.0 ** 56], np.float32)
+        put(p, ms=level[rng.integers(0, 8, nb)], vs=np.minimum(level, 3e4)[rng.integers(0, 8, nb)].astype(np.float32))
+    steps(params, lambda n: rng.normal(0, 1e-3, n).astype(np.float32), 0, 0)
