@@ -406,16 +406,16 @@ __device__ __forceinline__ void adamw_item(const AwRec& T, int64_t elem0, uint32
   const uint32_t om[2] = {e4m3_pack4(m, sm[0]), e4m3_pack4(m + 4, sm[L::block_of(4)])};
   at.store_u8(mp, om);
 
-  // Roots below 2^-6 of their scale, rare, take the general form, as blocks do
-  // whose roots may be subnormal. The others are cut as they are: the scale
-  // moves only their exponent.
+  // Roots below 2^-6 of their scale, rare, take the general form; so do blocks
+  // of zeros. The others are cut as they are: no root above zero is subnormal
+  // (the least is 2^-74.5), so the scale moves only their exponent.
   bool small = false;
 #pragma unroll
   for (int b = 0; b < L::kBlocks; ++b) {
     float least = v[4 * b];
 #pragma unroll
     for (int j = 1; j < 8 / L::kBlocks; ++j) least = __builtin_fminf(least, v[4 * b + j]);
-    small |= least < 0x1p-6f * sv[b] || sv[b] < 0x1p-100f;
+    small |= least < 0x1p-6f * sv[b];
   }
   small = __builtin_amdgcn_ballot_w64(small) != 0;
   uint64_t z[2] = {0u, 0u};

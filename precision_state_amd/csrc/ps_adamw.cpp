@@ -43,7 +43,7 @@ struct ps_adamw_plan {
   std::vector<Range> written;       // sorted
   std::vector<Grad> grads;
   int32_t max_group = -1;
-  bool any_bf16 = false, lacks_residual = false;
+  bool lacks_residual = false;
   // the last step's scalars
   std::vector<ps_hparams> last_groups;
   int64_t last_step = 0;
@@ -241,7 +241,6 @@ ps_status create(const ps_adamw_tensor* t, int32_t n, void* workspace, size_t wo
       slot[2 * i] = (uint32_t)(k + 1);   // 0: not a step tensor
       ++k;
       tmp.max_group = std::max(tmp.max_group, x.group);
-      tmp.any_bf16 |= x.param_type == PS_TYPE_BF16;
       tmp.lacks_residual |= x.param_type == PS_TYPE_BF16 && !x.residual;
     }
     tmp.table[kind] = AwTable{(const AwRec*)(w + l.recs) + k0, (const uint32_t*)(w + l.ends) + k0, (int32_t)(k - k0)};
