@@ -604,12 +604,13 @@ __device__ __forceinline__ Chunk norm_chunk(const AwNormTable& t, uint32_t chunk
 // the partial sums, in index order whichever it is, and writes the control
 // block, so that there is one launch.
 //
-// The gradients' last kNormKeepBytes are read without the non-temporal hint and
-// stay in the last-level cache; the step, whose own streams carry the hint,
-// finds them there (norm and step of a 202M layer with e4m3 moments: 576, 560, 553
-// and 549 us for 0, 128, 192 and 256 MiB). The others carry it: without any the norm
-// of 514M fp32 gradients takes 335 us, with all 296, with these 299; 42M bf16
-// gradients, which are all kept, take 18 us for the 16.9 below.
+// The gradients' last kNormKeepBytes, of whole chunks, are read without the
+// non-temporal hint and stay in the last-level cache (norm_keep.h); the step,
+// whose own streams carry the hint, finds them there (norm and step of a 202M
+// layer with e4m3 moments: 576, 560, 553 and 549 us for 0, 128, 192 and 256 MiB).
+// The others carry it: without any the norm of 514M fp32 gradients takes 335 us,
+// with all 296, with these 299; 42M bf16 gradients, which are all kept, take
+// 18 us for the 16.9 below.
 //
 // The last one is found by counting: each workgroup counts on one of kNormCounts
 // addresses, the last of those on a common one. (An address takes about 10 ns

@@ -12,6 +12,7 @@
 #include <new>
 #include <vector>
 
+#include "norm_keep.h"
 #include "ps_adamw.h"
 
 using namespace ps;
@@ -255,15 +256,8 @@ ps_status create(const ps_adamw_tensor* t, int32_t n, void* workspace, size_t wo
     nends[q] = (uint32_t)chunks;
     slot[2 * i + 1] = (uint32_t)++q;
   }
-  uint64_t keep_from = chunks;
-  int64_t keep = kNormKeepBytes;
-  for (size_t k = q; k-- > 0 && keep > 0;) {
-    const int64_t chunk_bytes = (int64_t)kNormChunk * elem_size(nrecs[k].gtype);
-    const int64_t of_k = nends[k] - (k ? nends[k - 1] : 0);
-    const int64_t kept = std::min<int64_t>(of_k, keep / chunk_bytes);
-    keep_from -= (uint64_t)kept;
-    keep = kept < of_k ? 0 : keep - of_k * chunk_bytes;
-  }
+  const uint64_t keep_from = norm_keep_from(
+      tmp.grads, [](const auto& g) { return std::pair<int64_t, int64_t>(g.n, elem_size(g.type)); }, kNormChunk, kNormKeepBytes);
   tmp.norm = AwNormTable{(const AwNormRec*)(w + l.nrecs), (const uint32_t*)(w + l.nends), (int32_t)q, (uint32_t)chunks,
                          (uint32_t)keep_from, 0};
   tmp.ctl = (ps_adamw_control*)w;
