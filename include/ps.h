@@ -438,6 +438,8 @@ ps_status ps_adamw_grad_norm(ps_adamw_plan* plan, double max_norm, double grad_s
  * calls with step = 0.
  * Calls on one plan must be ordered by the caller, as two calls on one stream
  * are; the current device must be the plan's (PS_ERR_INVALID_ARG).
+ * What infinite or NaN gradients or state become is not specified, but a clipped
+ * step after a norm that found such a gradient changes nothing.
  * Errors: PS_ERR_INVALID_ARG, PS_ERR_UNSUPPORTED, PS_ERR_HIP. */
 ps_status ps_adamw_step(ps_adamw_plan* plan, const ps_hparams* groups, int32_t n_groups, int64_t step,
                         int32_t clipped, int32_t rounding, ps_stream_t stream);
@@ -456,7 +458,8 @@ ps_status ps_adamw_plan_destroy(ps_adamw_plan* plan);
  * no second moment above zero becomes zero.
  * Decode: SIGNED x = code * s; UNSIGNED x = (code * s)^2. Since s is a power of
  * two, SIGNED decode is exact and a block that is decoded and encoded again
- * keeps its values. Arrays 16-byte aligned, scale 4-byte. */
+ * keeps its values. A block with an infinite or NaN x has unspecified codes.
+ * Arrays 16-byte aligned, scale 4-byte. */
 ps_status ps_encode_fp8(const float* x, uint8_t* code, float* scale, int64_t n, int32_t kind, ps_stream_t stream);
 ps_status ps_decode_fp8(const uint8_t* code, const float* scale, float* x, int64_t n, int32_t kind,
                         ps_stream_t stream);

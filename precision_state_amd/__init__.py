@@ -477,8 +477,10 @@ class AdamWTensor:
     None if only the gradient's norm is wanted. grad: float32, bfloat16 or
     float16, or None; grad_dtype says what a later one will be (param's dtype if
     not given). m, v: float32, or e4m3 codes (float8_e4m3fn, or their bytes as
-    uint8 or int8) with m_scale and v_scale. residual: a bf16 parameter's low halves. copy: bfloat16 or
-    float16, written with a float32 parameter's new values."""
+    uint8 or int8) with m_scale and v_scale (float32, read whole, written as
+    powers of two). residual: a bf16 parameter's low halves. copy: bfloat16 or
+    float16, written with a float32 parameter's new values. All contiguous and
+    16-byte aligned, scales 4-byte."""
     param: object
     grad: object
     m: object = None
@@ -569,7 +571,7 @@ class AdamWPlan:
     as an integer has to exist as long as the plan.
 
     The control block's fields are 0-dim tensors in device memory, read and
-    written in stream order: norm, grad_mul, skip, skipped, step, lr_mul."""
+    written in stream order: norm, grad_mul, skip, skipped, step_count, lr_mul."""
 
     _h = None
 

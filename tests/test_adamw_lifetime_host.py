@@ -219,3 +219,12 @@ def test_a_plan_that_is_let_go_records_its_arrays(entries):
     gc.collect()
     arrays = [x.data_ptr() for x in (rec.param, rec.grad, rec.m, rec.v, captured)]
     assert sorted(OnGpu.recorded) == sorted((p, 9) for p in arrays + [workspace])
+
+
+def test_control_block_fields_have_the_names_of_the_docstring(entries):
+    plan = ps.AdamWPlan([record()[0]])
+    names = ps.AdamWPlan.__doc__.split("in stream order:")[1].split(".")[0].replace("\n", " ").split(",")
+    assert len(names) == 6
+    for name in names:
+        field = getattr(plan, name.strip())
+        assert isinstance(field, torch.Tensor) and field.dim() == 0, name
