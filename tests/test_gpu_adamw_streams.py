@@ -1,5 +1,7 @@
 """GPU tests of the memory around an AdamW plan: what it releases while another
-stream still works on it, and gradients inside its workspace."""
+stream still works on it, gradients of captured calls, and gradients inside its
+workspace."""
+import numpy as np
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -77,3 +79,34 @@ def test_gradients_inside_the_workspace_are_refused():
     g.fill_(2.0)
     plan.grad_norm()                                        # the gradients from before still count
     assert float(plan.norm) == 16.0
+
+
+def test_captured_set_grads_replays_with_gradients_that_nobody_else_holds():
+    """The graph sets its own gradients, eager calls others, in turn; the plan alone holds all of them."""
+    n = 100_000
+    w, first, m, v = fresh(n, n, n, n)
+    first.fill_(2.0 ** -6)
+    plan = ps.AdamWPlan([ps.AdamWTensor(w, first, m, v)])
+    del first
+    captured = torch.full((n,), 2.0 ** -7, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        plan.set_grads([captured])
+        plan.grad_norm()
+    del captured
+    root = np.sqrt(np.float64(n))
+
+    def norm_is(level):
+        noise = [torch.full((n,), 1e3, device="cuda") for _ in range(6)]    # into whatever memory is free
+        torch.cuda.synchronize()
+        del noise
+        assert float(plan.norm) == float(np.float32(root * level))          # sums and scale are exact
+    plan.grad_norm()
+    norm_is(2.0 ** -6)                                      # the ones before the first replay
+    for level in (2.0 ** -3, 2.0 ** -4, 2.0 ** -5):
+        graph.replay()
+        norm_is(2.0 ** -7)
+        plan.set_grads([torch.full((n,), level, device="cuda")])
+        plan.grad_norm()
+        norm_is(level)
