@@ -12,7 +12,8 @@ if not torch.cuda.is_available():
 
 import precision_state_amd as ps  # noqa: E402
 
-N = 5_000_000   # a size of its own in the allocator's cache
+N = 5_000_000         # a size of its own in the allocator's cache
+SLEEP = 800_000_000   # clock cycles, a third of a second, before the work on the stream that arrays are used on
 
 
 def fresh(*sizes):
@@ -31,14 +32,14 @@ def test_released_arrays_wait_for_the_stream_that_uses_them(how):
     side = torch.cuda.Stream()
     w, g, m, v = fresh(N, N, N, N)
     g.fill_(1e-3)
+    new = torch.full((N,), 1e-3, device="cuda")
     plan = ps.AdamWPlan([ps.AdamWTensor(w, g, m, v)])
     torch.cuda.synchronize()
     pointers_handed_out(N, 8)
     old, state = g.data_ptr(), {x.data_ptr() for x in (w, m, v)}
     with torch.cuda.stream(side):
-        torch.cuda._sleep(200_000_000)                      # about 0.1 s before the step on this stream
-    new = torch.full((N,), 1e-3, device="cuda")
-    torch.cuda.current_stream().synchronize()
+        torch.cuda._sleep(SLEEP)
+    # No work for the default stream from here on: it may share a hardware queue with this one and wait for it.
     kw = {"stream": dict(stream=side), "integer": dict(stream=side.cuda_stream), "current": {}}[how]
     with torch.cuda.stream(side if how == "current" else torch.cuda.current_stream()):
         plan.step(hp, 1, **kw)
@@ -61,7 +62,7 @@ def test_a_plan_made_on_a_side_stream_and_run_on_the_default_one():
         pointers_handed_out(N, 8)
     side.synchronize()
     state = {x.data_ptr() for x in (w, g, m, v)} | {plan.workspace.data_ptr()}
-    torch.cuda._sleep(200_000_000)
+    torch.cuda._sleep(SLEEP)
     plan.step([ps.HParams(algo=ps.ALGO_ADAM, lr=1e-3)], 1)
     del w, g, m, v, plan
     with torch.cuda.stream(side):
