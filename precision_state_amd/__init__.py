@@ -567,8 +567,9 @@ class AdamWPlan:
     closed the plan keeps the memory of its tensors alive, by references of its
     own: it neither changes the records nor reads them again (set_grads gives it
     other gradients). A graph that captured its calls needs the plan. What is
-    released after calls on another stream is recorded on it, so a stream given
-    as an integer has to exist as long as the plan.
+    released after calls on another stream than the one that was current when it
+    was given is recorded on it, so a stream given as an integer has to exist as
+    long as the plan.
 
     The control block's fields are 0-dim tensors in device memory, read and
     written in stream order: norm, grad_mul, skip, skipped, step_count, lr_mul."""
@@ -601,9 +602,11 @@ class AdamWPlan:
         # and tensors (another gradient, another storage) does not free it.
         self._arrays = [x.detach() for t in tensors
                         for x in (t.param, t.residual, t.copy, t.m, t.m_scale, t.v, t.v_scale) if x is not None]
-        self._grads = [None if t.grad is None else t.grad.detach() for t in tensors]
+        # gradients by their storages, which take a sixth of the time of another tensor
+        self._grads = [None if t.grad is None else t.grad.untyped_storage() for t in tensors]
         self._captured = []              # gradients of captured set_grads calls
-        self._streams = {}               # those that the plan ran on, by their integers
+        self._streams, self._last = {}, None   # those that the plan ran on, by their integers, and the last one
+        self._seen = {self._stream0}     # and those that were current when it was given arrays
         ctl = self.workspace[:ctypes.sizeof(CAdamWControl)]
 
         def field(name, dtype):
@@ -618,8 +621,11 @@ class AdamWPlan:
         if not self._h:
             raise ValueError("the plan is closed")
         raw = _current_raw_stream(self._index) if stream is None else _raw_stream(self.device, stream)
-        if raw not in self._streams:
-            self._streams[raw] = self._stream_object(stream, raw)
+        if raw != self._last:
+            self._last = raw
+            if raw not in self._streams:
+                self._streams[raw] = self._stream_object(stream, raw)
+                self._seen.add(raw)
         return raw
 
     def _stream_object(self, stream, raw):
@@ -629,11 +635,13 @@ class AdamWPlan:
             return torch.cuda.default_stream(self.device)
         return torch.cuda.ExternalStream(raw, device=self.device)
 
-    def _release(self, arrays):
-        """Before the plan lets arrays go: the allocator must not hand their memory out before the streams that the
-        plan ran on are done with it."""
-        for stream in self._streams.values():
-            for x in arrays:
+    def _release(self, arrays, storages):
+        """Before the plan lets memory go: the allocator must not hand it out before the streams that the plan ran on
+        are done with it. It does not where all was given and run on one stream."""
+        if len(self._seen) == 1:
+            return
+        for x in arrays + [torch.empty(0, dtype=torch.uint8, device=self.device).set_(s) for s in storages]:
+            for stream in self._streams.values():
                 x.record_stream(stream)
 
     def _run(self, f, *args):
@@ -655,27 +663,24 @@ class AdamWPlan:
         in place of the ones before; gradients of a captured call, which replays set again, as long as it lives."""
         if len(grads) != len(self._sizes):
             raise ValueError(f"{len(grads)} gradients for {len(self._sizes)} tensors")
-        types = (torch.float32, torch.bfloat16, torch.float16)
+        types, device = (torch.float32, torch.bfloat16, torch.float16), self.device
         arr = (ctypes.c_void_p * max(1, len(grads)))()
         for i, (g, (n, ty)) in enumerate(zip(grads, self._sizes)):
             if g is None:
                 continue
-            if g.dtype != types[ty] or g.numel() != n or not g.is_contiguous() or g.device != self.device:
-                raise ValueError(f"tensor {i}: the gradient must be contiguous {types[ty]} on {self.device} with {n} elements")
+            if g.dtype != types[ty] or g.numel() != n or not g.is_contiguous() or g.device != device:
+                raise ValueError(f"tensor {i}: the gradient must be contiguous {types[ty]} on {device} with {n} elements")
             arr[i] = g.data_ptr()
         raw = self._on_stream(stream)
         self._run(_lib.ps_adamw_set_grads, arr, len(grads), raw)
         if self._is_capturing(stream, raw):          # the tables change when the graph runs
-            self._captured += [g.detach() for g in grads if g is not None]
+            self._captured += [g.untyped_storage() for g in grads if g is not None]
             return
-        released = []
-        for i, (old, g) in enumerate(zip(self._grads, grads)):
-            if g is not None and old is not None and old.data_ptr() == arr[i]:
-                continue
-            if old is not None:
-                released.append(old)
-            self._grads[i] = None if g is None else g.detach()
-        self._release(released)
+        self._seen.add(_current_raw_stream(self._index))
+        old, self._grads = self._grads, [None if g is None else g.untyped_storage() for g in grads]
+        if len(self._seen) > 1:
+            self._release([], [x for x, y in zip(old, self._grads)
+                               if x is not None and (y is None or x.data_ptr() != y.data_ptr())])
 
     def grad_norm(self, max_norm=float("inf"), grad_scale=1.0, stream=None):
         """The gradients' global 2-norm and clip factor into the control block (ps_adamw_grad_norm)."""
@@ -693,7 +698,7 @@ class AdamWPlan:
     def close(self):
         if self._h:
             h, self._h = self._h, None
-            self._release(self._arrays + [g for g in self._grads if g is not None] + self._captured + [self.workspace])
+            self._release(self._arrays + [self.workspace], [g for g in self._grads if g is not None] + self._captured)
             self._arrays, self._grads, self._captured = [], [], []
             _check(_lib.ps_adamw_plan_destroy(h))
 

@@ -205,6 +205,32 @@ def test_released_arrays_are_recorded_on_the_plans_streams(entries):
     assert OnGpu.recorded == []
 
 
+def test_nothing_is_recorded_where_all_is_on_one_stream(entries):
+    """Memory that is given and used on one stream is handed out in its order."""
+    rec, _ = record()
+    entries.current = 4
+    plan = ps.AdamWPlan([rec])
+    for _ in range(3):
+        plan.set_grads([array(300)[0]])
+        plan.grad_norm()
+        plan.step([ps.HParams(algo=ps.ALGO_ADAM)], 1, stream=4)
+    plan.close()
+    assert OnGpu.recorded == []
+
+
+def test_gradients_given_on_another_stream_are_recorded(entries):
+    rec, _ = record()
+    plan = ps.AdamWPlan([rec])
+    plan.grad_norm()
+    entries.current = 8                                     # the gradient is this stream's, the calls are on stream 0
+    g, _ = array(300)
+    plan.set_grads([g], stream=0)
+    assert OnGpu.recorded == [(rec.grad.data_ptr(), 0)]
+    OnGpu.recorded.clear()
+    plan.set_grads([None], stream=0)
+    assert OnGpu.recorded == [(g.data_ptr(), 0)]
+
+
 def test_a_plan_that_is_let_go_records_its_arrays(entries):
     rec, _ = record()
     plan = ps.AdamWPlan([rec])
