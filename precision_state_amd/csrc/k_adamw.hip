@@ -195,12 +195,14 @@ constexpr bool quad_lanes(int kind) { return !(kind & kAwE4m3) || !(kind & kAwBf
 // the streams' reads and writes meet less in HBM, and as long as the
 // arithmetic stays hidden that is worth more than latency. The 202M layer with
 // fp32 moments took 1020, 890, 920, 946, 953 and 995 us at 1, 2, 3, 4, 5 and 8
-// waves; 514M bf16 weights with e4m3 moments 1459, 1188, 1138, 1150 and 1180 us at
-// 2, 3, 4, 5 and 8: about 15 KB of loads in flight a SIMD for both. Where weights
-// are rounded stochastically beside e4m3 moments, integer work for the random
-// bits fills the vector units and wants as many waves as have registers (42M
+// waves; 298M bf16 weights rounded stochastically, fp32 moments 1020, 1039 and 1061
+// us at 2, 3 and 4; 514M bf16 weights with e4m3 moments 1459, 1188, 1138, 1150 and
+// 1180 us at 2, 3, 4, 5 and 8: about 15 KB of loads in flight a SIMD for all. Where
+// weights are rounded stochastically beside e4m3 moments, integer work for the
+// random bits fills the vector units and wants as many waves as have registers (42M
 // parameters, both rounded so: 87, 83, 79 and 77 us at 4, 5, 6 and 7 waves; 8 spill,
-// 83 us).
+// 83 us). Each row was measured in turn on one card with the arithmetic of its
+// time; cards differ by up to 3%.
 constexpr int waves_of(int kind, int split) {
   return !(kind & kAwE4m3) ? 2 : (kind & kAwBf16) && split == PS_SPLIT_STOCHASTIC ? 7 : 4;
 }
@@ -295,7 +297,7 @@ __device__ __forceinline__ void adamw_item(const AwRec& T, int64_t elem0, uint32
   if (!G32) unpack<8>(gw, T.gtype == PS_TYPE_F16, g);
   if (E8) {
     // The whole scale counts, as in ps_decode_fp8: the conversion that takes a
-    // scale reads only its exponent. (It saves 0.3 of 75.1 us for 42M weights and
+    // scale reads only its exponent. (It saves 0.5 of 75.2 us for 42M weights and
     // second moments rounded stochastically, and nothing for the other kinds.)
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
@@ -463,7 +465,7 @@ __device__ __forceinline__ int find(const uint32_t* ends, int n, uint32_t item) 
 }
 
 // One step of one kind of tensors. 202M fp32 weights with bf16 gradients and
-// copy and fp32 moments take 892 us (6.3 TB/s), 514M bf16 weights with residuals and
+// copy and fp32 moments take 898 us (6.3 TB/s), 514M bf16 weights with residuals and
 // e4m3 moments 1150 us (6.3 TB/s), both bound by HBM; 42M bf16 weights with e4m3
 // moments, both rounded stochastically, 75 us (5.6 TB/s), bound by the vector units.
 template <int KIND, int SPLIT, bool NADAM>
