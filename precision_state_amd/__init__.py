@@ -598,11 +598,10 @@ class AdamWPlan:
             _check(_lib.ps_adamw_plan_create(arr, len(recs), self.workspace.data_ptr(), size.value, self._stream0,
                                              ctypes.byref(h)))
         self._h = h
-        # The plan's own references to the memory that its device tables address: what becomes of the caller's records
-        # and tensors (another gradient, another storage) does not free it.
-        self._arrays = [x.detach() for t in tensors
+        # The plan's own references to the memory that its device tables address, the storages: what becomes of the
+        # caller's records and tensors (another gradient, another storage) does not free it.
+        self._arrays = [x.untyped_storage() for t in tensors
                         for x in (t.param, t.residual, t.copy, t.m, t.m_scale, t.v, t.v_scale) if x is not None]
-        # gradients by their storages, which take a sixth of the time of another tensor
         self._grads = [None if t.grad is None else t.grad.untyped_storage() for t in tensors]
         self._captured = []              # gradients of captured set_grads calls
         self._streams, self._last = {}, None   # those that the plan ran on, by their integers, and the last one
@@ -635,12 +634,13 @@ class AdamWPlan:
             return torch.cuda.default_stream(self.device)
         return torch.cuda.ExternalStream(raw, device=self.device)
 
-    def _release(self, arrays, storages):
+    def _release(self, storages):
         """Before the plan lets memory go: the allocator must not hand it out before the streams that the plan ran on
         are done with it. It does not where all was given and run on one stream."""
         if len(self._seen) == 1:
             return
-        for x in arrays + [torch.empty(0, dtype=torch.uint8, device=self.device).set_(s) for s in storages]:
+        for s in storages:
+            x = torch.empty(0, dtype=torch.uint8, device=self.device).set_(s)
             for stream in self._streams.values():
                 x.record_stream(stream)
 
@@ -679,8 +679,8 @@ class AdamWPlan:
         self._seen.add(_current_raw_stream(self._index))
         old, self._grads = self._grads, [None if g is None else g.untyped_storage() for g in grads]
         if len(self._seen) > 1:
-            self._release([], [x for x, y in zip(old, self._grads)
-                               if x is not None and (y is None or x.data_ptr() != y.data_ptr())])
+            self._release([x for x, y in zip(old, self._grads)
+                           if x is not None and (y is None or x.data_ptr() != y.data_ptr())])
 
     def grad_norm(self, max_norm=float("inf"), grad_scale=1.0, stream=None):
         """The gradients' global 2-norm and clip factor into the control block (ps_adamw_grad_norm)."""
@@ -698,9 +698,11 @@ class AdamWPlan:
     def close(self):
         if self._h:
             h, self._h = self._h, None
-            self._release(self._arrays + [self.workspace], [g for g in self._grads if g is not None] + self._captured)
+            status = _lib.ps_adamw_plan_destroy(h)
+            arrays = self._arrays + [g for g in self._grads if g is not None] + self._captured
             self._arrays, self._grads, self._captured = [], [], []
-            _check(_lib.ps_adamw_plan_destroy(h))
+            self._release(arrays + [self.workspace.untyped_storage()])
+            _check(status)
 
     def __del__(self):
         try:
