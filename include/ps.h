@@ -464,6 +464,205 @@ ps_status ps_encode_fp8(const float* x, uint8_t* code, float* scale, int64_t n, 
 ps_status ps_decode_fp8(const uint8_t* code, const float* scale, float* x, int64_t n, int32_t kind,
                         ps_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Activation checkpoints in 8 bits, and their use in the backward pass.
+ *
+ * What a forward pass saves for the backward one is held as e4m3 codes: the
+ * inputs of linear layers and of feed-forward activations with a power-of-two
+ * scale for each 128 columns of a row, normalised values with none. The
+ * backward entries read the codes; no wider copy is made.
+ *
+ * Matrices are row-major; `ld` is the distance between rows in elements
+ * (ld >= cols), codes are contiguous [rows, cols], scales contiguous
+ * [rows, ceil(cols / 128)] floats. Arrays need the alignment of their element
+ * only. `type` is the PS_TYPE_* of activations and their gradients; arithmetic
+ * is fp32, each result rounded to `type` once, to nearest even. rows or cols of
+ * 0: nothing is read, and only sums over no rows are written. rows < 2^31,
+ * cols <= 2^24, rows * ceil(cols / 128) < 2^31.
+ * What is written must not overlap anything else of the call unless it says so
+ * (PS_ERR_INVALID_ARG). Calls allocate nothing and can be captured. An infinite
+ * or NaN value is an ordinary input: where it goes through a code it becomes
+ * NaN, so that it reaches the gradients that ps_adamw_grad_norm looks at.
+ * ------------------------------------------------------------------------- */
+
+/* Columns of a row that share a scale. */
+#define PS_ACT_BLOCK 128
+
+/* ps_encode_act / ps_decode_act - codes of a matrix and back. Per block:
+ * s = the smallest power of two >= 2^-126 with max|x| <= 448 s over the finite
+ * x; code = x / s rounded to the nearest e4m3 value, ties to even, NaN for an
+ * infinite or NaN x. Decode: x = code * s (exact in fp32 and bf16, rounded to
+ * fp16), whatever the scale. */
+ps_status ps_encode_act(const void* x, int32_t type, int64_t rows, int64_t cols, int64_t ld, uint8_t* code,
+                        float* scale, ps_stream_t stream);
+ps_status ps_decode_act(const uint8_t* code, const float* scale, void* x, int32_t type, int64_t rows, int64_t cols,
+                        int64_t ld, ps_stream_t stream);
+
+/* ps_glu_forward / ps_glu_backward - the activation of a feed-forward layer,
+ * gated: out = f(a) * b, or not (b NULL): out = f(a).
+ *   SILU       f(a) = a / (1 + exp(-a))
+ *   GELU       f(a) = a * Phi(a), Phi the normal distribution function
+ *   GELU_TANH  f(a) = a / 2 * (1 + tanh(sqrt(2 / pi) * (a + 0.044715 a^3)))
+ * Forward: a_code, a_scale and, if gated, b_code, b_scale are what
+ * ps_encode_act makes of a and b; all NULL: nothing is saved.
+ * Backward, with a and b decoded: da = dout * b * f'(a), db = dout * f(a), and
+ * out once more (NULL: not wanted). da or db may be dout itself (the same
+ * pointer and ld), a and b may be halves of one matrix. b_code and b_scale NULL:
+ * not gated, and db is NULL too. */
+enum { PS_ACT_SILU = 0, PS_ACT_GELU = 1, PS_ACT_GELU_TANH = 2 };
+ps_status ps_glu_forward(int64_t rows, int64_t cols, int32_t type, int32_t act, const void* a, int64_t lda,
+                         const void* b, int64_t ldb, void* out, int64_t ldo, uint8_t* a_code, float* a_scale,
+                         uint8_t* b_code, float* b_scale, ps_stream_t stream);
+ps_status ps_glu_backward(int64_t rows, int64_t cols, int32_t type, int32_t act, const void* dout, int64_t ldd,
+                          const uint8_t* a_code, const float* a_scale, const uint8_t* b_code, const float* b_scale,
+                          void* da, int64_t lda, void* db, int64_t ldb, void* out, int64_t ldo, ps_stream_t stream);
+
+/* The norms around a block's place in the residual stream: after the block
+ * (post) and before the next one (pre), with the gate and scale between them.
+ *   v = N1(y) * post_weight       N1: post_norm, NONE is v = y
+ *   h = residual_scale * x + branch_scale * (gate * v)
+ *   n = N2(h) * m + add           N2: pre_norm; m = mul, or 1 + mul (MUL_PLUS_ONE)
+ * N(z) = z * r, r = 1 / sqrt(mean(z^2) + eps) (RMS) or (z - mean z) * r, with
+ * the variance in place of the mean square (LAYER); means over a row's cols.
+ * With no branch (y NULL) h is x. NULL vectors are left out (1, 0 for add).
+ *   post_weight  [cols]; only with a post_norm
+ *   gate         [cols], or [n_segs, cols] with GATE_BY_SEG
+ *   mul, add     [cols], or [n_segs, cols] with MOD_BY_SEG
+ *   seg_start    int32[n_segs + 1] in device memory, ascending: segment b is
+ *                rows seg_start[b] .. seg_start[b + 1] - 1 (it may be empty).
+ *                Rows of no segment are left as they are in every output and
+ *                in no sum. NULL (n_segs 0): all rows are one segment
+ * eps >= 0, scales finite; cols <= PS_NORM_MAX_COLS. vec_type: PS_TYPE_* of the
+ * four vectors. */
+enum { PS_NORM_NONE = 0, PS_NORM_RMS = 1, PS_NORM_LAYER = 2 };
+enum { PS_NORM_GATE_BY_SEG = 1u << 0, PS_NORM_MOD_BY_SEG = 1u << 1, PS_NORM_MUL_PLUS_ONE = 1u << 2 };
+#define PS_NORM_MAX_COLS 16384
+typedef struct ps_block_norm {
+  int64_t rows;
+  int64_t cols;
+  const int32_t* seg_start;
+  const void* post_weight;
+  const void* gate;
+  const void* mul;
+  const void* add;
+  double post_eps;
+  double pre_eps;
+  double residual_scale;
+  double branch_scale;
+  int32_t type;
+  int32_t vec_type;
+  int32_t post_norm;
+  int32_t pre_norm;
+  int32_t n_segs;
+  uint32_t flags; /* PS_NORM_* bits */
+} ps_block_norm;
+
+/* Forward arrays. x, and y unless there is no branch, are read; n is written,
+ * and h if there is a branch (h may be x itself, the same pointer and ld; NULL
+ * without one). Saved for the backward pass, each NULL if not wanted (the
+ * backward needs all that the call has):
+ *   h_code, h_rstd  N2(h) as e4m3 (|N2(h)| <= sqrt(cols), no scale), r of N2
+ *   y_code, y_rstd  with a post_norm: N1(y) as e4m3, r of N1
+ *   y_code, y_scale with a gate and no post_norm: y as ps_encode_act codes it
+ * rstd arrays are float[rows]. */
+typedef struct ps_block_norm_fwd {
+  const void* x;
+  int64_t ldx;
+  const void* y;
+  int64_t ldy;
+  void* h;
+  int64_t ldh;
+  void* n;
+  int64_t ldn;
+  uint8_t* h_code;
+  float* h_rstd;
+  uint8_t* y_code;
+  float* y_scale;
+  float* y_rstd;
+} ps_block_norm_fwd;
+
+/* Backward arrays: the gradients dn of n and dh of h from elsewhere (NULL: 0)
+ * are read with what the forward pass saved; dx and, with a branch, dy are
+ * written (dy NULL: there is none, and the branch's gradients are not made). dx or dy may be dh or dn
+ * itself. With xh, yh the decoded values and G the whole gradient of h:
+ *   G  = dh + back(dn * m, xh, h_rstd);  dx = residual_scale * G
+ *   p  = branch_scale * G;  dy = back(p * gate * post_weight, yh, y_rstd), or
+ *   p * gate with no post_norm
+ *   back(g, z, r) = r * (g - z * mean(g z))          RMS
+ *                   r * (g - mean g - z * mean(g z)) LAYER
+ * Gradients of the vectors, float, shaped as they are, each NULL if not wanted:
+ *   d_mul = sum dn * xh; d_add = sum dn; d_gate = sum p * yh * post_weight;
+ *   d_post_weight = sum p * gate * yh
+ * summed over the segment's rows, or over all segments', in an order that
+ * depends on sizes and segments only. accumulate 1: they are added to what the
+ * arrays hold. workspace: 16-byte aligned, ps_block_norm_workspace_size bytes;
+ * its contents on entry are ignored and it belongs to one call at a time. */
+typedef struct ps_block_norm_bwd {
+  const void* dn;
+  int64_t lddn;
+  const void* dh;
+  int64_t lddh;
+  const uint8_t* h_code;
+  const float* h_rstd;
+  const uint8_t* y_code;
+  const float* y_scale;
+  const float* y_rstd;
+  void* dx;
+  int64_t lddx;
+  void* dy;
+  int64_t lddy;
+  float* d_post_weight;
+  float* d_gate;
+  float* d_mul;
+  float* d_add;
+  void* workspace;
+  size_t workspace_bytes;
+  int32_t accumulate;
+  int32_t reserved; /* must be 0 */
+} ps_block_norm_bwd;
+
+ps_status ps_block_norm_forward(const ps_block_norm* norm, const ps_block_norm_fwd* io, ps_stream_t stream);
+/* Workspace bytes of a backward call with this rows, cols and n_segs. Host only. */
+ps_status ps_block_norm_workspace_size(const ps_block_norm* norm, size_t* bytes);
+ps_status ps_block_norm_backward(const ps_block_norm* norm, const ps_block_norm_bwd* io, ps_stream_t stream);
+
+/* ps_linear_wgrad - the weight gradient of y = x W^T, W [out, in], from dy
+ * [tokens, out] and the codes of x [tokens, in]:
+ *   db[n]    = sum_t dy[t, n]
+ *   dw[n, k] = mul[k] * (sum_t dy[t, n] * z[t, k]) + add[k] * db[n]
+ * z is code * scale, or the code's value itself (scale NULL): with the h_code
+ * of a block norm and its vectors as mul and add (NULL: 1 and 0; a mul that
+ * means 1 + mul has to be given so), x is the norm's output n.
+ * dy_type is PS_TYPE_BF16 or PS_TYPE_F16; z is multiplied in that type: bf16
+ * holds it whole if scales are powers of two, fp16 within its range. Products
+ * and sums are fp32, in an order that depends on the sizes only. dw of dw_type
+ * (PS_TYPE_*) with distance lddw between rows; db float[out], NULL: not wanted;
+ * mul, add float[in]. accumulate 1: dw and db are added to what the arrays
+ * hold, in fp32, and rounded once. workspace as for a block norm's backward
+ * call, ps_linear_wgrad_workspace_size bytes. */
+typedef struct ps_linear_wgrad_args {
+  int64_t tokens;
+  int64_t out_features;
+  int64_t in_features;
+  const void* dy;
+  int64_t lddy;
+  const uint8_t* code;
+  const float* scale;
+  const float* mul;
+  const float* add;
+  void* dw;
+  int64_t lddw;
+  float* db;
+  void* workspace;
+  size_t workspace_bytes;
+  int32_t dy_type;
+  int32_t dw_type;
+  int32_t accumulate;
+  int32_t reserved; /* must be 0 */
+} ps_linear_wgrad_args;
+ps_status ps_linear_wgrad_workspace_size(int64_t tokens, int64_t out_features, int64_t in_features, size_t* bytes);
+ps_status ps_linear_wgrad(const ps_linear_wgrad_args* args, ps_stream_t stream);
+
 /* Host-offload pipeline [NADAM, opening post: moments (and here the
  * residuals) live in host memory and cross PCIe every step].
  * A group is one set of tensors stepped together (e.g. one transformer

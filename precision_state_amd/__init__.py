@@ -43,6 +43,11 @@ TYPE_F32, TYPE_BF16, TYPE_F16 = 0, 1, 2
 STATE_F32, STATE_E4M3 = 0, 1
 ROUND_NEAREST, ROUND_STOCHASTIC = 0, 1
 ADAMW_MAX_GROUPS = 16
+ACT_BLOCK = 128
+ACT_SILU, ACT_GELU, ACT_GELU_TANH = 0, 1, 2
+NORM_NONE, NORM_RMS, NORM_LAYER = 0, 1, 2
+NORM_GATE_BY_SEG, NORM_MOD_BY_SEG, NORM_MUL_PLUS_ONE = 1, 2, 4
+NORM_MAX_COLS = 16384
 
 STATUS = {0: "PS_OK", 1: "PS_ERR_INVALID_ARG", 2: "PS_ERR_ALIGNMENT", 3: "PS_ERR_SHAPE",
           4: "PS_ERR_UNSUPPORTED", 5: "PS_ERR_HIP", 6: "PS_ERR_NO_MEMORY", 7: "PS_ERR_WORKSPACE"}
@@ -51,7 +56,9 @@ EXPORTED = ["ps_opt_step_multi", "ps_step_scalars", "ps_split", "ps_join", "ps_e
             "ps_decode_moments", "ps_factored_workspace_size", "ps_factored_step", "ps_factored_step_noalloc",
             "ps_adamw_workspace_size", "ps_adamw_plan_create", "ps_adamw_set_grads", "ps_adamw_grad_norm",
             "ps_adamw_step", "ps_adamw_plan_destroy", "ps_encode_fp8", "ps_decode_fp8",
-            "ps_offload_plan_create", "ps_offload_plan_create_ex",
+            "ps_encode_act", "ps_decode_act", "ps_glu_forward", "ps_glu_backward", "ps_block_norm_forward",
+            "ps_block_norm_workspace_size", "ps_block_norm_backward", "ps_linear_wgrad_workspace_size",
+            "ps_linear_wgrad", "ps_offload_plan_create", "ps_offload_plan_create_ex",
             "ps_offload_run", "ps_offload_bytes", "ps_offload_plan_destroy", "ps_status_string",
             "ps_last_error", "ps_version"]
 
@@ -106,6 +113,41 @@ class COffloadOptions(ctypes.Structure):
                 ("reserved1", ctypes.c_int32)]
 
 
+class CBlockNorm(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("seg_start", ctypes.c_void_p),
+                ("post_weight", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("mul", ctypes.c_void_p),
+                ("add", ctypes.c_void_p), ("post_eps", ctypes.c_double), ("pre_eps", ctypes.c_double),
+                ("residual_scale", ctypes.c_double), ("branch_scale", ctypes.c_double), ("type", ctypes.c_int32),
+                ("vec_type", ctypes.c_int32), ("post_norm", ctypes.c_int32), ("pre_norm", ctypes.c_int32),
+                ("n_segs", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+class CBlockNormFwd(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64),
+                ("h", ctypes.c_void_p), ("ldh", ctypes.c_int64), ("n", ctypes.c_void_p), ("ldn", ctypes.c_int64),
+                ("h_code", ctypes.c_void_p), ("h_rstd", ctypes.c_void_p), ("y_code", ctypes.c_void_p),
+                ("y_scale", ctypes.c_void_p), ("y_rstd", ctypes.c_void_p)]
+
+
+class CBlockNormBwd(ctypes.Structure):
+    _fields_ = [("dn", ctypes.c_void_p), ("lddn", ctypes.c_int64), ("dh", ctypes.c_void_p), ("lddh", ctypes.c_int64),
+                ("h_code", ctypes.c_void_p), ("h_rstd", ctypes.c_void_p), ("y_code", ctypes.c_void_p),
+                ("y_scale", ctypes.c_void_p), ("y_rstd", ctypes.c_void_p), ("dx", ctypes.c_void_p),
+                ("lddx", ctypes.c_int64), ("dy", ctypes.c_void_p), ("lddy", ctypes.c_int64),
+                ("d_post_weight", ctypes.c_void_p), ("d_gate", ctypes.c_void_p), ("d_mul", ctypes.c_void_p),
+                ("d_add", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+                ("accumulate", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class CLinearWgrad(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("out_features", ctypes.c_int64), ("in_features", ctypes.c_int64),
+                ("dy", ctypes.c_void_p), ("lddy", ctypes.c_int64), ("code", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p), ("mul", ctypes.c_void_p), ("add", ctypes.c_void_p),
+                ("dw", ctypes.c_void_p), ("lddw", ctypes.c_int64), ("db", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t), ("dy_type", ctypes.c_int32),
+                ("dw_type", ctypes.c_int32), ("accumulate", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 OFFLOAD_DIRECT, OFFLOAD_STAGED = 0, 1
 OFFLOAD_DEFAULT_CUS = 8
 
@@ -130,6 +172,15 @@ _sig = {
     "ps_adamw_plan_destroy": [_vp],
     "ps_encode_fp8": [_vp, _vp, _vp, _i64, _i32, _vp],
     "ps_decode_fp8": [_vp, _vp, _vp, _i64, _i32, _vp],
+    "ps_encode_act": [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp],
+    "ps_decode_act": [_vp, _vp, _vp, _i32, _i64, _i64, _i64, _vp],
+    "ps_glu_forward": [_i64, _i64, _i32, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp],
+    "ps_glu_backward": [_i64, _i64, _i32, _i32, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp],
+    "ps_block_norm_forward": [ctypes.POINTER(CBlockNorm), ctypes.POINTER(CBlockNormFwd), _vp],
+    "ps_block_norm_workspace_size": [ctypes.POINTER(CBlockNorm), ctypes.POINTER(ctypes.c_size_t)],
+    "ps_block_norm_backward": [ctypes.POINTER(CBlockNorm), ctypes.POINTER(CBlockNormBwd), _vp],
+    "ps_linear_wgrad_workspace_size": [_i64, _i64, _i64, ctypes.POINTER(ctypes.c_size_t)],
+    "ps_linear_wgrad": [ctypes.POINTER(CLinearWgrad), _vp],
     "ps_offload_plan_create": [ctypes.POINTER(COffloadGroup), _i32, ctypes.POINTER(ctypes.c_void_p)],
     "ps_offload_plan_create_ex": [ctypes.POINTER(COffloadGroup), _i32, ctypes.POINTER(COffloadOptions),
                                   ctypes.POINTER(ctypes.c_void_p)],
@@ -709,3 +760,8 @@ class AdamWPlan:
             self.close()
         except Exception:
             pass
+
+
+from ._activations import (  # noqa: E402,F401
+    BlockNorm, block_norm_backward, block_norm_forward, block_norm_workspace_size, decode_act, encode_act, glu_backward,
+    glu_forward, linear_wgrad, linear_wgrad_workspace_size)

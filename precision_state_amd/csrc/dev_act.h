@@ -1,0 +1,175 @@
+// dev_act.h - gfx950 device helpers of the activation checkpoints: eight
+// consecutive values of a row at any alignment, vectors of any type, sums over
+// a wave.
+#pragma once
+
+#include "dev_adamw.h"
+#include "ps_act.h"
+
+namespace ps {
+
+// The hardware reads and writes global memory at any byte address; these types
+// let the compiler use the widest access for data aligned to its element only.
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ uint32_t div_by(uint32_t u, const FastDiv& f) { return (uint32_t)(((uint64_t)u * f.m) >> f.s); }
+
+// Eight values of a row as they lie in memory.
+template <int TYPE>
+struct Raw8 {
+  u32x4 w[TYPE == PS_TYPE_F32 ? 2 : 1];
+};
+template <int TYPE>
+constexpr int kBytes = TYPE == PS_TYPE_F32 ? 4 : 2;
+
+// Element `at` on, the first `left` of eight (left <= 0: none); the others are 0.
+template <int TYPE, bool STREAM = true>
+__device__ __forceinline__ Raw8<TYPE> load8(const void* base, int64_t at, int left) {
+  Raw8<TYPE> r;
+  if (left >= 8) {
+    const GLOBAL u32x4_any* p = (const GLOBAL u32x4_any*)((const char*)base + at * kBytes<TYPE>);
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(r.w) / 16; ++i) r.w[i] = STREAM ? (u32x4)__builtin_nontemporal_load(p + i) : (u32x4)p[i];
+    return r;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (TYPE == PS_TYPE_F32) {
+      r.w[j / 4][j % 4] = j < left ? ((const GLOBAL uint32_t*)base)[at + j] : 0u;
+    } else {
+      const uint32_t h = j < left ? ((const GLOBAL uint16_t*)base)[at + j] : 0u;
+      r.w[0][j / 2] = j & 1 ? r.w[0][j / 2] | h << 16 : h;
+    }
+  }
+  return r;
+}
+
+template <int TYPE>
+__device__ __forceinline__ void widen8(const Raw8<TYPE>& r, float* d) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (TYPE == PS_TYPE_F32) {
+      d[j] = __uint_as_float(r.w[j / 4][j % 4]);
+    } else if (TYPE == PS_TYPE_BF16) {
+      d[j] = j & 1 ? bf16_hi(r.w[0][j / 2]) : bf16_lo(r.w[0][j / 2]);
+    } else {
+      const uint32_t w = r.w[0][j / 2];
+      const f16x2 h = __builtin_bit_cast(f16x2, w);
+      d[j] = (float)h[j & 1];
+    }
+  }
+}
+
+template <int TYPE>
+__device__ __forceinline__ uint32_t round2(float a, float b) {
+  const f32x2 v = {a, b};
+  if (TYPE == PS_TYPE_BF16) return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
+}
+
+template <int TYPE, bool STREAM = true>
+__device__ __forceinline__ void store8(void* base, int64_t at, int left, const float* s) {
+  if (left <= 0) return;
+  Raw8<TYPE> r;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (TYPE == PS_TYPE_F32)
+      r.w[j / 4][j % 4] = __float_as_uint(s[j]);
+    else if (j % 2 == 0)
+      r.w[0][j / 2] = round2<TYPE>(s[j], s[j + 1]);
+  }
+  if (left >= 8) {
+    GLOBAL u32x4_any* p = (GLOBAL u32x4_any*)((char*)base + at * kBytes<TYPE>);
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(r.w) / 16; ++i) {
+      if (STREAM)
+        __builtin_nontemporal_store((u32x4_any)r.w[i], p + i);
+      else
+        p[i] = r.w[i];
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < left) {
+      if (TYPE == PS_TYPE_F32)
+        ((GLOBAL uint32_t*)base)[at + j] = r.w[j / 4][j % 4];
+      else
+        ((GLOBAL uint16_t*)base)[at + j] = (uint16_t)(r.w[0][j / 2] >> (16 * (j & 1)));
+    }
+}
+
+// Eight codes.
+__device__ __forceinline__ u32x2_any load_codes8(const uint8_t* base, int64_t at, int left) {
+  if (left >= 8) return __builtin_nontemporal_load((const GLOBAL u32x2_any*)(base + at));
+  u32x2_any r = {0, 0};
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < left) r[j / 4] |= (uint32_t)((const GLOBAL uint8_t*)base)[at + j] << (8 * (j % 4));
+  return r;
+}
+
+__device__ __forceinline__ void store_codes8(uint8_t* base, int64_t at, int left, u32x2_any c) {
+  if (left >= 8) {
+    __builtin_nontemporal_store(c, (GLOBAL u32x2_any*)(base + at));
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < left) ((GLOBAL uint8_t*)base)[at + j] = (uint8_t)(c[j / 4] >> (8 * (j % 4)));
+}
+
+__device__ __forceinline__ void codes_to_f32(u32x2_any c, float* d) {
+  e4m3_unpack4(c[0], d);
+  e4m3_unpack4(c[1], d + 4);
+}
+
+// Eight values of a vector of any type (uniform), kept in the caches.
+__device__ __forceinline__ void load_vec8(const void* v, int type, int64_t at, int left, float* d) {
+  if (type == PS_TYPE_F32)
+    widen8<PS_TYPE_F32>(load8<PS_TYPE_F32, false>(v, at, left), d);
+  else if (type == PS_TYPE_BF16)
+    widen8<PS_TYPE_BF16>(load8<PS_TYPE_BF16, false>(v, at, left), d);
+  else
+    widen8<PS_TYPE_F16>(load8<PS_TYPE_F16, false>(v, at, left), d);
+}
+
+// Codes and scale of a block of 128 values, eight on each of a DPP row's 16
+// lanes. The scale comes from the finite values; the conversion makes NaN of the
+// others (checked on the GPU).
+__device__ __forceinline__ u32x2_any encode_block(const float* x, float& s) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t u = __float_as_uint(x[j]) & 0x7FFFFFFFu;
+    top = __builtin_elementwise_max(top, u < 0x7F800000u ? u : 0u);
+  }
+  top = __builtin_elementwise_max(top, dpp_u32<0xB1>(top));
+  top = __builtin_elementwise_max(top, dpp_u32<0x4E>(top));
+  top = __builtin_elementwise_max(top, dpp_u32<0x141>(top));
+  top = __builtin_elementwise_max(top, dpp_u32<0x140>(top));
+  float inv;
+  e4m3_scale(top, s, inv);
+  u32x2_any c;
+  c[0] = e4m3_pack4(x, s);
+  c[1] = e4m3_pack4(x + 4, s);
+  return c;
+}
+
+// Sum over the wave, on every lane, in an order of its own kind for all sizes.
+__device__ __forceinline__ float wave_sum(float x) {
+  x += dpp<0xB1>(x);
+  x += dpp<0x4E>(x);
+  x += dpp<0x141>(x);
+  x += dpp<0x140>(x);
+  const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+  const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(q[0]) + __uint_as_float(q[1]);
+}
+
+}  // namespace ps

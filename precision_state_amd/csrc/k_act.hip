@@ -1,0 +1,260 @@
+// k_act.hip - the codec of saved activations, and the activation of a
+// feed-forward layer with its inputs saved in 8 bits: forward, and backward
+// from the codes.
+//
+// A block of 128 columns lies on 16 lanes, eight values each: its largest value
+// is a DPP maximum inside the row of lanes, and a lane's loads and stores of
+// 16-bit values are 16 bytes wide. Every call is one pass over its data.
+#include "dev_act.h"
+
+namespace ps {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTeams = kThreads / 16;   // blocks that a workgroup handles at a time
+
+// The lane's place in unit u.
+struct Place {
+  int64_t row;
+  int col, left;   // first column; how many of its eight exist
+  bool in;
+  __device__ __forceinline__ Place(const ActGrid& g, uint32_t u) {
+    in = u < g.units;
+    const uint32_t r = div_by(u, g.nb);
+    row = r;
+    col = (int)(u - r * g.nb.d) * kActBlock + (int)(threadIdx.x & 15) * 8;
+    left = in ? g.cols - col : 0;
+  }
+  __device__ __forceinline__ int64_t at(int64_t ld) const { return row * ld + col; }
+};
+
+__device__ __forceinline__ uint32_t unit_of(int k, int per) {
+  return (blockIdx.x * per + k) * (uint32_t)kTeams + threadIdx.x / 16;
+}
+
+template <int TYPE, int K>
+__global__ __launch_bounds__(kThreads) void k_encode_act(ActGrid g, const void* x, int64_t ld, uint8_t* code, float* scale) {
+  Raw8<TYPE> raw[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const Place p(g, unit_of(k, K));
+    raw[k] = load8<TYPE>(x, p.at(ld), p.left);
+  }
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const uint32_t u = unit_of(k, K);
+    const Place p(g, u);
+    float v[8], s;
+    widen8<TYPE>(raw[k], v);
+    const u32x2_any c = encode_block(v, s);
+    store_codes8(code, p.at(g.cols), p.left, c);
+    if (p.in && (threadIdx.x & 15) == 0) scale[u] = s;
+  }
+}
+
+template <int TYPE, int K>
+__global__ __launch_bounds__(kThreads) void k_decode_act(ActGrid g, const uint8_t* code, const float* scale, void* x,
+                                                         int64_t ld) {
+  u32x2_any c[K];
+  float s[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const uint32_t u = unit_of(k, K);
+    const Place p(g, u);
+    c[k] = load_codes8(code, p.at(g.cols), p.left);
+    s[k] = p.in ? scale[u] : 0.0f;
+  }
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const Place p(g, unit_of(k, K));
+    float v[8];
+    codes_to_f32(c[k], v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= s[k];
+    store8<TYPE>(x, p.at(ld), p.left, v);
+  }
+}
+
+// f(a) and f'(a). Each is a times a probability q: the logistic function for
+// SILU, Phi for GELU, and for its tanh form (1 + tanh u) / 2, which is the
+// logistic function of 2 u and loses nothing where tanh u comes near -1.
+template <int ACT>
+__device__ __forceinline__ void activation(float a, float& f, float& slope) {
+  constexpr float kLog2e = 1.44269504f;
+  if (ACT == PS_ACT_GELU) {
+    const float q = 0.5f * erfcf(a * -0.70710678f);
+    f = a * q;
+    slope = __builtin_fmaf(a * 0.39894228f, __builtin_amdgcn_exp2f(a * a * (-0.5f * kLog2e)), q);
+    return;
+  }
+  constexpr float c = 0.79788456f, c3 = 0.044715f;
+  const float z = __builtin_amdgcn_fmed3f(a, -64.0f, 64.0f);   // q is 0 or 1 there, and z^2 stays finite
+  const float u = ACT == PS_ACT_SILU ? a : 2.0f * c * z * __builtin_fmaf(c3, z * z, 1.0f);
+  const float du = ACT == PS_ACT_SILU ? 1.0f : 2.0f * c * __builtin_fmaf(3.0f * c3, z * z, 1.0f);
+  const float q = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(u * -kLog2e));
+  f = a * q;
+  slope = __builtin_fmaf(f * (1.0f - q), du, q);
+}
+
+template <int TYPE, int ACT, bool GATED, bool SAVE, int K>
+__global__ __launch_bounds__(kThreads) void k_glu_forward(ActGrid g, GluArgs t) {
+  Raw8<TYPE> ra[K], rb[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const Place p(g, unit_of(k, K));
+    ra[k] = load8<TYPE>(t.a, p.at(t.lda), p.left);
+    if (GATED) rb[k] = load8<TYPE>(t.b, p.at(t.ldb), p.left);
+  }
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const uint32_t u = unit_of(k, K);
+    const Place p(g, u);
+    float a[8], b[8], o[8], s;
+    widen8<TYPE>(ra[k], a);
+    if (GATED) widen8<TYPE>(rb[k], b);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float slope;
+      activation<ACT>(a[j], o[j], slope);
+      if (GATED) o[j] *= b[j];
+    }
+    store8<TYPE>(t.out, p.at(t.ldo), p.left, o);
+    if (SAVE) {
+      const bool writes = p.in && (threadIdx.x & 15) == 0;
+      const u32x2_any c = encode_block(a, s);
+      store_codes8(t.a_code, p.at(g.cols), p.left, c);
+      if (writes) t.a_scale[u] = s;
+      if (GATED) {
+        const u32x2_any d = encode_block(b, s);
+        store_codes8(t.b_code, p.at(g.cols), p.left, d);
+        if (writes) t.b_scale[u] = s;
+      }
+    }
+  }
+}
+
+template <int TYPE, int ACT, bool GATED, int K>
+__global__ __launch_bounds__(kThreads) void k_glu_backward(ActGrid g, GluArgs t) {
+  Raw8<TYPE> rd[K];
+  u32x2_any ca[K], cb[K];
+  float sa[K], sb[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const uint32_t u = unit_of(k, K);
+    const Place p(g, u);
+    rd[k] = load8<TYPE>(t.dout, p.at(t.ldd), p.left);
+    ca[k] = load_codes8(t.a_code, p.at(g.cols), p.left);
+    sa[k] = p.in ? t.a_scale[u] : 0.0f;
+    if (GATED) {
+      cb[k] = load_codes8(t.b_code, p.at(g.cols), p.left);
+      sb[k] = p.in ? t.b_scale[u] : 0.0f;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const Place p(g, unit_of(k, K));
+    float d[8], a[8], b[8], da[8], db[8], o[8];
+    widen8<TYPE>(rd[k], d);
+    codes_to_f32(ca[k], a);
+    if (GATED) codes_to_f32(cb[k], b);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float f, slope;
+      activation<ACT>(a[j] * sa[k], f, slope);
+      if (GATED) {
+        const float v = b[j] * sb[k];
+        db[j] = d[j] * f;
+        da[j] = d[j] * v * slope;
+        o[j] = f * v;
+      } else {
+        da[j] = d[j] * slope;
+        o[j] = f;
+      }
+    }
+    store8<TYPE>(t.da, p.at(t.lda), p.left, da);
+    if (GATED) store8<TYPE>(t.db, p.at(t.ldb), p.left, db);
+    if (t.out) store8<TYPE>(t.out, p.at(t.ldo), p.left, o);
+  }
+}
+
+dim3 grid_of(const ActGrid& g, int k) { return dim3((g.units + kTeams * k - 1) / (kTeams * k)); }
+
+template <int TYPE, int ACT>
+ps_status glu_forward(const ActGrid& g, const GluArgs& p, hipStream_t s) {
+  constexpr int K = 2;
+  const bool save = p.a_code != nullptr;
+  if (p.b && save)
+    hipLaunchKernelGGL((k_glu_forward<TYPE, ACT, true, true, K>), grid_of(g, K), dim3(kThreads), 0, s, g, p);
+  else if (p.b)
+    hipLaunchKernelGGL((k_glu_forward<TYPE, ACT, true, false, K>), grid_of(g, K), dim3(kThreads), 0, s, g, p);
+  else if (save)
+    hipLaunchKernelGGL((k_glu_forward<TYPE, ACT, false, true, K>), grid_of(g, K), dim3(kThreads), 0, s, g, p);
+  else
+    hipLaunchKernelGGL((k_glu_forward<TYPE, ACT, false, false, K>), grid_of(g, K), dim3(kThreads), 0, s, g, p);
+  return hip_check(hipGetLastError(), "k_glu_forward launch");
+}
+
+template <int TYPE, int ACT>
+ps_status glu_backward(const ActGrid& g, const GluArgs& p, hipStream_t s) {
+  constexpr int K = 2;
+  if (p.b_code)
+    hipLaunchKernelGGL((k_glu_backward<TYPE, ACT, true, K>), grid_of(g, K), dim3(kThreads), 0, s, g, p);
+  else
+    hipLaunchKernelGGL((k_glu_backward<TYPE, ACT, false, K>), grid_of(g, K), dim3(kThreads), 0, s, g, p);
+  return hip_check(hipGetLastError(), "k_glu_backward launch");
+}
+
+template <int TYPE>
+ps_status glu(bool forward, const ActGrid& g, int act, const GluArgs& p, hipStream_t s) {
+  switch (act) {
+    case PS_ACT_SILU: return forward ? glu_forward<TYPE, PS_ACT_SILU>(g, p, s) : glu_backward<TYPE, PS_ACT_SILU>(g, p, s);
+    case PS_ACT_GELU: return forward ? glu_forward<TYPE, PS_ACT_GELU>(g, p, s) : glu_backward<TYPE, PS_ACT_GELU>(g, p, s);
+    default: return forward ? glu_forward<TYPE, PS_ACT_GELU_TANH>(g, p, s) : glu_backward<TYPE, PS_ACT_GELU_TANH>(g, p, s);
+  }
+}
+
+ps_status glu(bool forward, const ActGrid& g, int type, int act, const GluArgs& p, hipStream_t s) {
+  switch (type) {
+    case PS_TYPE_F32: return glu<PS_TYPE_F32>(forward, g, act, p, s);
+    case PS_TYPE_BF16: return glu<PS_TYPE_BF16>(forward, g, act, p, s);
+    default: return glu<PS_TYPE_F16>(forward, g, act, p, s);
+  }
+}
+
+}  // namespace
+
+ps_status launch_encode_act(const ActGrid& g, int type, const void* x, int64_t ld, uint8_t* code, float* scale,
+                            hipStream_t s) {
+  constexpr int K = 2;
+  const dim3 grid = grid_of(g, K), wg(kThreads);
+  if (type == PS_TYPE_F32)
+    hipLaunchKernelGGL((k_encode_act<PS_TYPE_F32, K>), grid, wg, 0, s, g, x, ld, code, scale);
+  else if (type == PS_TYPE_BF16)
+    hipLaunchKernelGGL((k_encode_act<PS_TYPE_BF16, K>), grid, wg, 0, s, g, x, ld, code, scale);
+  else
+    hipLaunchKernelGGL((k_encode_act<PS_TYPE_F16, K>), grid, wg, 0, s, g, x, ld, code, scale);
+  return hip_check(hipGetLastError(), "k_encode_act launch");
+}
+
+ps_status launch_decode_act(const ActGrid& g, int type, const uint8_t* code, const float* scale, void* x, int64_t ld,
+                            hipStream_t s) {
+  constexpr int K = 2;
+  const dim3 grid = grid_of(g, K), wg(kThreads);
+  if (type == PS_TYPE_F32)
+    hipLaunchKernelGGL((k_decode_act<PS_TYPE_F32, K>), grid, wg, 0, s, g, code, scale, x, ld);
+  else if (type == PS_TYPE_BF16)
+    hipLaunchKernelGGL((k_decode_act<PS_TYPE_BF16, K>), grid, wg, 0, s, g, code, scale, x, ld);
+  else
+    hipLaunchKernelGGL((k_decode_act<PS_TYPE_F16, K>), grid, wg, 0, s, g, code, scale, x, ld);
+  return hip_check(hipGetLastError(), "k_decode_act launch");
+}
+
+ps_status launch_glu_forward(const ActGrid& g, int type, int act, const GluArgs& p, hipStream_t s) {
+  return glu(true, g, type, act, p, s);
+}
+
+ps_status launch_glu_backward(const ActGrid& g, int type, int act, const GluArgs& p, hipStream_t s) {
+  return glu(false, g, type, act, p, s);
+}
+
+}  // namespace ps
