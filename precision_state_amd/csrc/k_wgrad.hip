@@ -1,12 +1,12 @@
 // k_wgrad.hip - the weight gradient of a linear layer whose input was saved in
 // 8 bits: dw = dy^T z on the matrix cores, the tokens being the summed axis.
 //
-// Both operands lie in memory with the summed axis outermost. Tiles [tokens,
-// columns] go into shared memory as they lie, dy's as it is and the codes
-// converted to dy's type on the way, and ds_read_b64_tr_b16 gives each lane
-// the values of one column at four tokens, which is what a matrix instruction
-// takes; which of its 16 places a token has does not matter, as long as both
-// operands agree.
+// Both operands lie in memory with the summed axis outermost, and go into shared
+// memory as they lie, the codes as bytes. Transposing reads
+// (ds_read_b64_tr_b16, ds_read_b64_tr_b8) give each lane eight tokens of one
+// column, which is what a matrix instruction takes, and the codes become bf16
+// or fp16 between that read and the instruction, in the shadow of the matrix
+// instructions before.
 #include "dev_act.h"
 
 namespace ps {
@@ -14,46 +14,79 @@ namespace {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 #define LOCAL __attribute__((address_space(3)))
 
-constexpr int kStep = 32;      // tokens in shared memory at a time
 constexpr int kThreads = 256;  // four waves
 
-// Tiles of the result: rows (columns of dy) by columns (of z), and how the four
-// waves share it.
-template <int N_, int K_, int WN_, int WK_>
+// Tiles of the result: rows (columns of dy) by columns (of z), how the four
+// waves share it, and the tokens in shared memory at a time.
+template <int N_, int K_, int WN_, int WK_, int STEP_>
 struct Shape {
-  static constexpr int N = N_, K = K_, WN = WN_, WK = WK_;
+  static constexpr int N = N_, K = K_, WN = WN_, WK = WK_, STEP = STEP_;
   static constexpr int FN = N / WN / 32, FK = K / WK / 32;   // 32 x 32 results of a wave
   static_assert(WN * WK == 4 && FN * WN * 32 == N && FK * WK * 32 == K, "four waves");
+  // one buffer of shared memory: dy, codes, scales [STEP][blocks of 128]
+  static constexpr int KB = (K + kActBlock - 1) / kActBlock;
+  static constexpr int DY = STEP * N * 2, CODE = STEP * K, BYTES = DY + CODE + STEP * KB * 4;
 };
-using Large = Shape<256, 256, 2, 2>;
-using Middle = Shape<128, 128, 2, 2>;
-using FewRows = Shape<32, 256, 1, 4>;
-using FewCols = Shape<256, 32, 4, 1>;
+using Large = Shape<256, 256, 2, 2, 64>;
+using Middle = Shape<128, 128, 2, 2, 64>;
+using FewRows = Shape<32, 256, 1, 4, 64>;
+using FewCols = Shape<256, 32, 4, 1, 64>;
 
-// Place of a 16-byte chunk q of row t in a tile of W 16-bit columns. A transposing
-// read takes four rows at the same 64 bytes; the exchange puts them on
-// different banks.
-template <int W>
+// Where 16-byte chunk q of row t lies in a tile of rows of W bytes. A
+// transposing read takes R rows of G bytes each at the same place for half a
+// wave (64 bytes of four rows, 32 of eight); exchanging the chunks by row puts
+// them on different banks.
+template <int W, int G>
 __device__ __forceinline__ int chunk_at(int t, int q) {
-  constexpr int kRows = W >= 128 ? 1 : 128 / W;   // rows in the 256 bytes of all banks
-  return t * (W / 8) + (q ^ (4 * ((t / kRows) & (4 / kRows - 1))));
+  constexpr int kRows = W >= 256 ? 1 : 256 / W, kParts = (W >= 256 ? 256 : W) / G;
+  return t * W + 16 * (q ^ (G / 16 * ((t / kRows) & (kParts - 1))));
 }
 
-// A fragment of 16 tokens and 32 columns from column c on: tokens 0-3 and 8-11
-// on lanes 0-31, 4-7 and 12-15 on the others.
+// dy at 16 tokens and 32 columns: tokens 0-7 on lanes 0-31, 8-15 on the others.
 template <int W>
-__device__ __forceinline__ s16x8 fragment(const uint16_t* tile, int t0, int c, int lane) {
-  const int t = t0 + (lane / 32) * 4 + (lane & 15) / 4;
-  const int col = c + (lane & 16) + (lane & 3) * 4;
-  const int o0 = chunk_at<W>(t, col / 8) * 8 + (col & 4), o1 = chunk_at<W>(t + 8, col / 8) * 8 + (col & 4);
-  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LOCAL s16x4*)(tile + o0));
-  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LOCAL s16x4*)(tile + o1));
+__device__ __forceinline__ s16x8 dy_fragment(const char* tile, int t0, int c, int lane) {
+  const int t = t0 + (lane / 32) * 8 + (lane & 15) / 4, col = c + (lane & 16) + (lane & 3) * 4;
+  const int o = chunk_at<2 * W, 64>(t, col / 8) + (col & 4) * 2;
+  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LOCAL s16x4*)(tile + o));
+  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LOCAL s16x4*)(tile + o + 4 * 2 * W));
   return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// The codes at the same tokens, 32 columns.
+template <int W>
+__device__ __forceinline__ i32x2 code_fragment(const char* tile, int t0, int c, int lane) {
+  const int t = t0 + (lane / 32) * 8 + (lane & 15) / 2, col = c + (lane & 16) + (lane & 1) * 8;
+  return __builtin_amdgcn_ds_read_tr8_b64_v2i32((LOCAL i32x2*)(tile + chunk_at<W, 32>(t, col / 16) + (col & 8)));
+}
+
+// Eight codes, and their tokens' scales, as the values that are multiplied.
+// Without scales one conversion makes two values; with them the product is
+// formed in fp32 and rounded, which loses nothing if a scale is a power of two.
+template <int TYPE, bool SCALED>
+__device__ __forceinline__ s16x8 values(i32x2 c, const float* s) {
+  u32x4 w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (SCALED) {
+      const f32x2 v = i & 1 ? __builtin_amdgcn_cvt_pk_f32_fp8(c[i / 2], true) : __builtin_amdgcn_cvt_pk_f32_fp8(c[i / 2], false);
+      w[i] = round2<TYPE>(v.x * s[2 * i], v.y * s[2 * i + 1]);
+    } else if (TYPE == PS_TYPE_BF16) {
+      const bf16x2 v = i & 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[i / 2], 1.0f, true)
+                             : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[i / 2], 1.0f, false);
+      w[i] = __builtin_bit_cast(uint32_t, v);
+    } else {
+      const f16x2 v = i & 1 ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[i / 2], 1.0f, true)
+                            : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[i / 2], 1.0f, false);
+      w[i] = __builtin_bit_cast(uint32_t, v);
+    }
+  }
+  return __builtin_bit_cast(s16x8, w);
 }
 
 template <int TYPE>
@@ -63,38 +96,91 @@ __device__ __forceinline__ f32x16 mfma(s16x8 a, s16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-// How many elements there are from (t, col) to the end of a matrix of `rows`
-// rows, eight at most, none behind the last row. Columns past the row's end
-// read the next row: they only reach results that are not stored.
-__device__ __forceinline__ int left_from(int64_t t, int64_t rows, int64_t ld, int col, int cols) {
-  if (t >= rows) return 0;
-  const int64_t left = (rows - 1 - t) * ld + cols - col;
-  return left >= 8 ? 8 : (int)left;
+// The 16 bytes from (t, at) of a matrix of `rows` rows of `width` bytes, `pitch`
+// apart; those behind the matrix are 0 and not read.
+__device__ __forceinline__ u32x4 load16_guarded(const char* base, int64_t t, int64_t rows, int64_t pitch, int at, int width) {
+  const int64_t left = t < rows ? (rows - 1 - t) * pitch + width - at : 0;
+  if (left >= 16) return *(const GLOBAL u32x4_byte*)(base + t * pitch + at);
+  uint64_t lo = 0, hi = 0;
+#pragma unroll 1
+  for (int j = 0; j < left; ++j) {
+    const uint64_t byte = (uint64_t)((const GLOBAL uint8_t*)base)[t * pitch + at + j] << (8 * (j & 7));
+    if (j < 8)
+      lo |= byte;
+    else
+      hi |= byte;
+  }
+  return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
 }
 
-// One result to memory: dw = mul acc + add db [+ dw].
-__device__ __forceinline__ void store_dw(const WgradArgs& p, int n, int k, float acc) {
-  if (p.mul) acc *= p.mul[k];
-  if (p.add) acc = __builtin_fmaf(p.add[k], p.db_sum[n], acc);
+// How many rows `span` bytes can be loaded of, from byte `at` of the row on,
+// without passing the end of the matrix. Bytes past a row's end are the next
+// row's: they only reach results that are not stored.
+__device__ __forceinline__ int64_t safe_rows(int64_t rows, int64_t pitch, int64_t at, int64_t span, int64_t width) {
+  const int64_t over = at + span - width;
+  return over <= 0 ? rows : max((int64_t)0, rows - (over + pitch - 1) / pitch);
+}
+
+// Four results of a row to memory, `left` of them inside: dw = mul acc + add db [+ dw].
+__device__ __forceinline__ void store_dw(const WgradArgs& p, int n, int k, int left, f32x4 acc) {
+  if (left <= 0) return;
   const int64_t o = (int64_t)n * p.lddw + k;
-  if (p.dw_type == PS_TYPE_F32) {
-    float* d = (float*)p.dw + o;
-    *d = p.accumulate ? *d + acc : acc;
-  } else if (p.dw_type == PS_TYPE_BF16) {
-    uint16_t* d = (uint16_t*)p.dw + o;
-    if (p.accumulate) acc += bf16_lo(*d);
-    *d = (uint16_t)round2<PS_TYPE_BF16>(acc, 0.0f);
-  } else {
-    _Float16* d = (_Float16*)p.dw + o;
-    if (p.accumulate) acc += (float)*d;
-    *d = (_Float16)acc;
+  float v[8] = {acc[0], acc[1], acc[2], acc[3], 0, 0, 0, 0};
+  const float db = p.add ? p.db_sum[n] : 0.0f;
+  if (left >= 4) {
+    f32x4_any* f = (f32x4_any*)((float*)p.dw + o);
+    u32x2_any* h = (u32x2_any*)((uint16_t*)p.dw + o);
+    if (p.mul || p.add || p.accumulate) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (p.mul) v[i] *= p.mul[k + i];
+        if (p.add) v[i] = __builtin_fmaf(p.add[k + i], db, v[i]);
+      }
+      if (p.accumulate) {
+        float was[8];
+        if (p.dw_type == PS_TYPE_F32) {
+          const f32x4 w = *f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) was[i] = w[i];
+        } else if (p.dw_type == PS_TYPE_BF16) {
+          widen8<PS_TYPE_BF16>(Raw8<PS_TYPE_BF16>{{{(*h)[0], (*h)[1], 0, 0}}}, was);
+        } else {
+          widen8<PS_TYPE_F16>(Raw8<PS_TYPE_F16>{{{(*h)[0], (*h)[1], 0, 0}}}, was);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += was[i];
+      }
+    }
+    if (p.dw_type == PS_TYPE_F32)
+      *f = f32x4{v[0], v[1], v[2], v[3]};
+    else if (p.dw_type == PS_TYPE_BF16)
+      *h = u32x2_any{round2<PS_TYPE_BF16>(v[0], v[1]), round2<PS_TYPE_BF16>(v[2], v[3])};
+    else
+      *h = u32x2_any{round2<PS_TYPE_F16>(v[0], v[1]), round2<PS_TYPE_F16>(v[2], v[3])};
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    if (i >= left) continue;
+    if (p.mul) v[i] *= p.mul[k + i];
+    if (p.add) v[i] = __builtin_fmaf(p.add[k + i], db, v[i]);
+    if (p.dw_type == PS_TYPE_F32) {
+      float* d = (float*)p.dw + o + i;
+      *d = p.accumulate ? *d + v[i] : v[i];
+    } else if (p.dw_type == PS_TYPE_BF16) {
+      uint16_t* d = (uint16_t*)p.dw + o + i;
+      *d = (uint16_t)round2<PS_TYPE_BF16>(p.accumulate ? v[i] + bf16_lo(*d) : v[i], 0.0f);
+    } else {
+      _Float16* d = (_Float16*)p.dw + o + i;
+      *d = (_Float16)(p.accumulate ? v[i] + (float)*d : v[i]);
+    }
   }
 }
 
-template <int TYPE, class S>
-__global__ __launch_bounds__(kThreads) void k_wgrad(WgradArgs p) {
-  __shared__ __attribute__((aligned(16))) uint16_t lds[2][kStep * (S::N + S::K)];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
+template <int TYPE, bool SCALED, class S>
+__global__ __launch_bounds__(kThreads, 1) void k_wgrad(WgradArgs p) {
+  __shared__ __attribute__((aligned(16))) char lds[2 * S::BYTES];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int tiles = p.cut.tiles_n * p.cut.tiles_k;
   const int split = blockIdx.x / tiles, tile = blockIdx.x % tiles;
   const int n0 = tile % p.cut.tiles_n * S::N, k0 = tile / p.cut.tiles_n * S::K;
@@ -102,44 +188,65 @@ __global__ __launch_bounds__(kThreads) void k_wgrad(WgradArgs p) {
   const int64_t end = min(first + p.cut.per_split, p.tokens);
   const int wn = wave / S::WK * (S::FN * 32), wk = wave % S::WK * (S::FK * 32);
   const int k_blocks = (p.k + kActBlock - 1) / kActBlock;
+  const int64_t safe = min(end, min(safe_rows(p.tokens, p.lddy * 2, n0 * 2, S::N * 2, p.n * 2),
+                                    safe_rows(p.tokens, p.k, k0, S::K, p.k)));
 
-  constexpr int kA = (kStep * S::N / 8 + kThreads - 1) / kThreads, kB = (kStep * S::K / 8 + kThreads - 1) / kThreads;
-  Raw8<TYPE> ra[kA];
-  u32x2_any rb[kB];
-  float sb[kB];
-  auto fetch = [&](int64_t t0) {
+  // The next step's tiles on their way: registers between two loads and two writes.
+  constexpr int kA = (S::DY / 16 + kThreads - 1) / kThreads, kB = (S::CODE / 16 + kThreads - 1) / kThreads;
+  constexpr int kRowA = S::N / 8, kRowB = S::K / 16;   // chunks of a row
+  constexpr bool kWholeA = S::DY / 16 % kThreads == 0, kWholeB = S::CODE / 16 % kThreads == 0;
+  static_assert(S::STEP * S::KB <= kThreads, "a scale for each lane at most");
+  const char *dy = (const char*)p.dy + 2 * n0, *code = (const char*)p.code + k0;
+  u32x4 ra[kA], rb[kB];
+  float rs = 0;
+  auto load = [&](int64_t t0) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < kA; ++i) {
-      const int c = i * kThreads + threadIdx.x, q = c % (S::N / 8);
-      const int64_t t = t0 + c / (S::N / 8);
-      const int left = c < kStep * S::N / 8 && t < end ? left_from(t, p.tokens, p.lddy, n0 + q * 8, p.n) : 0;
-      ra[i] = load8<TYPE, false>(p.dy, t * p.lddy + n0 + q * 8, left);
+      const int c = i * kThreads + threadIdx.x;
+      if (kWholeA || c < S::DY / 16) ra[i] = *(const GLOBAL u32x4_any*)(dy + (t0 + c / kRowA) * (2 * p.lddy) + c % kRowA * 16);
     }
 #pragma unroll
     for (int i = 0; i < kB; ++i) {
-      const int c = i * kThreads + threadIdx.x, q = c % (S::K / 8);
-      const int64_t t = t0 + c / (S::K / 8);
-      const int left = c < kStep * S::K / 8 && t < end ? left_from(t, p.tokens, p.k, k0 + q * 8, p.k) : 0;
-      rb[i] = load_codes8(p.code, t * p.k + k0 + q * 8, left);
-      const int block = min((k0 + q * 8) / kActBlock, k_blocks - 1);
-      sb[i] = p.scale && left > 0 ? p.scale[t * k_blocks + block] : 1.0f;
+      const int c = i * kThreads + threadIdx.x;
+      if (kWholeB || c < S::CODE / 16) rb[i] = *(const GLOBAL u32x4_byte*)(code + (t0 + c / kRowB) * p.k + c % kRowB * 16);
     }
+    if (SCALED && threadIdx.x < S::STEP * S::KB)
+      rs = p.scale[(t0 + threadIdx.x / S::KB) * k_blocks + min(k0 / kActBlock + (int)threadIdx.x % S::KB, k_blocks - 1)];
   };
-  auto place = [&](uint16_t* tile_a, uint16_t* tile_b) {
+  auto place = [&](char* buf) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < kA; ++i) {
       const int c = i * kThreads + threadIdx.x;
-      if (c < kStep * S::N / 8) *(u32x4*)(tile_a + chunk_at<S::N>(c / (S::N / 8), c % (S::N / 8)) * 8) = ra[i].w[0];
+      if (kWholeA || c < S::DY / 16) *(u32x4*)(buf + chunk_at<2 * S::N, 64>(c / kRowA, c % kRowA)) = ra[i];
     }
 #pragma unroll
     for (int i = 0; i < kB; ++i) {
       const int c = i * kThreads + threadIdx.x;
-      float v[8];
-      codes_to_f32(rb[i], v);
-      u32x4 w;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = round2<TYPE>(v[2 * j] * sb[i], v[2 * j + 1] * sb[i]);
-      if (c < kStep * S::K / 8) *(u32x4*)(tile_b + chunk_at<S::K>(c / (S::K / 8), c % (S::K / 8)) * 8) = w;
+      if (kWholeB || c < S::CODE / 16) *(u32x4*)(buf + S::DY + chunk_at<S::K, 32>(c / kRowB, c % kRowB)) = rb[i];
+    }
+    // scales by block, then token, so that a lane reads those of its eight tokens at once
+    if (SCALED && threadIdx.x < S::STEP * S::KB)
+      ((float*)(buf + S::DY + S::CODE))[threadIdx.x % S::KB * S::STEP + threadIdx.x / S::KB] = rs;
+  };
+  // The same for a step at the end of the split or of the matrices.
+  auto load_and_place = [&](char* buf, int64_t t0) __attribute__((always_inline)) {
+#pragma unroll 1
+    for (int c = threadIdx.x; c < S::DY / 16; c += kThreads) {
+      const int64_t t = t0 + c / kRowA;
+      *(u32x4*)(buf + chunk_at<2 * S::N, 64>(c / kRowA, c % kRowA)) =
+          load16_guarded((const char*)p.dy, t, t < end ? p.tokens : 0, 2 * p.lddy, 2 * n0 + c % kRowA * 16, 2 * p.n);
+    }
+#pragma unroll 1
+    for (int c = threadIdx.x; c < S::CODE / 16; c += kThreads) {
+      const int64_t t = t0 + c / kRowB;
+      *(u32x4*)(buf + S::DY + chunk_at<S::K, 32>(c / kRowB, c % kRowB)) =
+          load16_guarded((const char*)p.code, t, t < end ? p.tokens : 0, p.k, k0 + c % kRowB * 16, p.k);
+    }
+    if (SCALED && threadIdx.x < S::STEP * S::KB) {
+      const int64_t t = t0 + threadIdx.x / S::KB;
+      const int block = min(k0 / kActBlock + (int)threadIdx.x % S::KB, k_blocks - 1);
+      ((float*)(buf + S::DY + S::CODE))[threadIdx.x % S::KB * S::STEP + threadIdx.x / S::KB] =
+          t < end ? p.scale[t * k_blocks + block] : 0.0f;
     }
   };
 
@@ -151,56 +258,134 @@ __global__ __launch_bounds__(kThreads) void k_wgrad(WgradArgs p) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
 
-  int buf = 0;
-  if (first < end) {
-    fetch(first);
-    place(lds[0], lds[0] + kStep * S::N);
-  }
-  __syncthreads();
-  for (int64_t t = first; t < end; t += kStep) {
-    const bool more = t + kStep < end;
-    if (more) fetch(t + kStep);
-    const uint16_t *ta = lds[buf], *tb = ta + kStep * S::N;
+  s16x8 a[2][S::FN];
+  i32x2 b[2][S::FK];
+  f32x4 sc[2][2];
+  auto read = [&](const char* buf, int u, int to) __attribute__((always_inline)) {
 #pragma unroll
-    for (int u = 0; u < kStep; u += 16) {
-      s16x8 a[S::FN], b[S::FK];
+    for (int i = 0; i < S::FN; ++i) a[to][i] = dy_fragment<S::N>(buf, u, wn + i * 32, lane);
 #pragma unroll
-      for (int i = 0; i < S::FN; ++i) a[i] = fragment<S::N>(ta, u, wn + i * 32, lane);
-#pragma unroll
-      for (int j = 0; j < S::FK; ++j) b[j] = fragment<S::K>(tb, u, wk + j * 32, lane);
-#pragma unroll
-      for (int i = 0; i < S::FN; ++i)
-#pragma unroll
-        for (int j = 0; j < S::FK; ++j) acc[i][j] = mfma<TYPE>(a[i], b[j], acc[i][j]);
+    for (int j = 0; j < S::FK; ++j) b[to][j] = code_fragment<S::K>(buf + S::DY, u, wk + j * 32, lane);
+    if (SCALED) {
+      const float* s = (const float*)(buf + S::DY + S::CODE) + wk / kActBlock * S::STEP + u + lane / 32 * 8;
+      sc[to][0] = *(const f32x4*)s;
+      sc[to][1] = *(const f32x4*)(s + 4);
     }
-    buf ^= 1;
-    if (more) place(lds[buf], lds[buf] + kStep * S::N);
+  };
+  auto multiply = [&](int from) __attribute__((always_inline)) {
+    float s[8];
+    if (SCALED) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i] = sc[from][i / 4][i % 4];
+    }
+#pragma unroll
+    for (int j = 0; j < S::FK; ++j) {
+      const s16x8 v = values<TYPE, SCALED>(b[from][j], s);
+#pragma unroll
+      for (int i = 0; i < S::FN; ++i) acc[i][j] = mfma<TYPE>(a[from][i], v, acc[i][j]);
+    }
+  };
+
+  // Two buffers: while one is multiplied the other is filled with the tiles that
+  // were loaded a step before. The fragments of 16 tokens are read ahead of the
+  // matrix instructions that use them, the first ones of a step before the last
+  // 16 tokens of the step before are multiplied.
+  constexpr int U = S::STEP / 16;
+  char* cur = lds;
+  char* nxt = lds + S::BYTES;
+  const int64_t whole = first + (safe > first ? (safe - first) / S::STEP * S::STEP : 0);
+  if (first < whole) {
+    load(first);
+    place(cur);
+    if (first + S::STEP < whole) load(first + S::STEP);
     __syncthreads();
+    read(cur, 0, 0);
+    for (int64_t t = first; t < whole; t += S::STEP) {
+      const bool more = t + S::STEP < whole;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (u + 1 < U) {
+          read(cur, (u + 1) * 16, (u + 1) & 1);
+        } else if (more) {
+          __syncthreads();
+          read(nxt, 0, (u + 1) & 1);
+        }
+        if (u == 0 && more) {
+          place(nxt);
+          if (t + 2 * S::STEP < whole) load(t + 2 * S::STEP);
+        }
+        multiply(u & 1);
+      }
+      char* was = cur;
+      cur = nxt;
+      nxt = was;
+    }
+  }
+  for (int64_t t = whole; t < end; t += S::STEP) {
+    __syncthreads();
+    load_and_place(cur, t);
+    __syncthreads();
+#pragma unroll 1
+    for (int u = 0; u < S::STEP; u += 16) {
+      read(cur, u, 0);
+      multiply(0);
+    }
   }
 
-  // Result e of a 32 x 32 product: row 8 (e / 4) + 4 (lane / 32) + e % 4, column lane % 32.
+  // Result e of a 32 x 32 product is row 8 (e / 4) + 4 (lane / 32) + e % 4, column
+  // lane % 32. A wave's 32 rows go through its part of shared memory, so that
+  // rows are stored four columns a lane.
+  constexpr int kCols = S::FK * 32, kLanes = kCols / 4;
+  static_assert(4 * 32 * kCols * 4 <= 2 * S::BYTES, "a part for each wave");
+  float* part = (float*)lds + wave * (32 * kCols);
 #pragma unroll
-  for (int i = 0; i < S::FN; ++i)
+  for (int i = 0; i < S::FN; ++i) {
+    __syncthreads();
 #pragma unroll
     for (int j = 0; j < S::FK; ++j)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int n = n0 + wn + i * 32 + 8 * (e / 4) + 4 * (lane / 32) + e % 4, k = k0 + wk + j * 32 + lane % 32;
-        if (n >= p.n || k >= p.k) continue;
-        if (p.cut.splits > 1)
-          p.part[((int64_t)split * p.n + n) * p.k + k] = acc[i][j][e];
-        else
-          store_dw(p, n, k, acc[i][j][e]);
+      for (int e = 0; e < 16; ++e)
+        part[(8 * (e / 4) + 4 * (lane / 32) + e % 4) * kCols + j * 32 + lane % 32] = acc[i][j][e];
+    __syncthreads();
+#pragma unroll 1
+    for (int c = lane; c < 32 * kLanes; c += 64) {
+      const int n = n0 + wn + i * 32 + c / kLanes, k = k0 + wk + c % kLanes * 4;
+      if (n >= p.n) break;
+      const f32x4 v = *(const f32x4*)(part + c * 4);
+      if (p.cut.splits > 1) {
+        float* d = p.part + ((int64_t)split * p.n + n) * p.k + k;
+        if (p.k - k >= 4) {
+          *(f32x4_any*)d = v;
+        } else {
+#pragma unroll
+          for (int x = 0; x < 3; ++x)
+            if (k + x < p.k) d[x] = v[x];
+        }
+      } else {
+        store_dw(p, n, k, p.k - k, v);
       }
+    }
+  }
 }
 
-// The splits' partial results added up in order.
+// The splits' partial results added up in order, four columns of a row a lane.
 __global__ __launch_bounds__(kThreads) void k_wgrad_join(WgradArgs p) {
+  const int quads = (p.k + 3) / 4;
   const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x, size = (int64_t)p.n * p.k;
-  if (i >= size) return;
-  float s = p.part[i];
-  for (int j = 1; j < p.cut.splits; ++j) s += p.part[j * size + i];
-  store_dw(p, (int)(i / p.k), (int)(i % p.k), s);
+  if (i >= (int64_t)p.n * quads) return;
+  const int n = (int)(i / quads), k = (int)(i % quads) * 4, left = p.k - k;
+  const float* d = p.part + (int64_t)n * p.k + k;
+  f32x4 s = {0, 0, 0, 0};
+  for (int j = 0; j < p.cut.splits; ++j, d += size) {
+    if (left >= 4) {
+      s += *(const f32x4_any*)d;
+    } else {
+#pragma unroll
+      for (int x = 0; x < 3; ++x)
+        if (x < left) s[x] += d[x];
+    }
+  }
+  store_dw(p, n, k, left, s);
 }
 
 // Sums of dy over a strip of tokens: 256 columns a workgroup, eight on a lane,
@@ -240,7 +425,11 @@ __global__ __launch_bounds__(kThreads) void k_column_join(WgradArgs p) {
 
 template <int TYPE, class S>
 void product(const WgradArgs& p, hipStream_t s) {
-  hipLaunchKernelGGL((k_wgrad<TYPE, S>), dim3(p.cut.tiles_n * p.cut.tiles_k * p.cut.splits), dim3(kThreads), 0, s, p);
+  const dim3 grid(p.cut.tiles_n * p.cut.tiles_k * p.cut.splits);
+  if (p.scale)
+    hipLaunchKernelGGL((k_wgrad<TYPE, true, S>), grid, dim3(kThreads), 0, s, p);
+  else
+    hipLaunchKernelGGL((k_wgrad<TYPE, false, S>), grid, dim3(kThreads), 0, s, p);
 }
 
 template <int TYPE>
@@ -259,7 +448,7 @@ ps_status product(const WgradArgs& p, hipStream_t s) {
   }
   if (ps_status st = hip_check(hipGetLastError(), "k_wgrad launch")) return st;
   if (p.cut.splits > 1) {
-    const int64_t size = (int64_t)p.n * p.k;
+    const int64_t size = (int64_t)p.n * ((p.k + 3) / 4);
     hipLaunchKernelGGL(k_wgrad_join, dim3((uint32_t)((size + kThreads - 1) / kThreads)), dim3(kThreads), 0, s, p);
     return hip_check(hipGetLastError(), "k_wgrad_join launch");
   }
@@ -269,6 +458,7 @@ ps_status product(const WgradArgs& p, hipStream_t s) {
 }  // namespace
 
 WgradCut wgrad_cut(int64_t tokens, int64_t n, int64_t k) {
+  constexpr int kStep = 64;
   static const int kN[] = {Large::N, Middle::N, FewRows::N, FewCols::N}, kK[] = {Large::K, Middle::K, FewRows::K, FewCols::K};
   WgradCut c = {};
   c.kind = n <= 32 ? 2 : k <= 32 ? 3 : n >= 1024 && k >= 1024 ? 0 : 1;
@@ -279,7 +469,7 @@ WgradCut wgrad_cut(int64_t tokens, int64_t n, int64_t k) {
   const int64_t want = tiles >= 256 ? 1 : (256 + tiles - 1) / tiles;
   const int64_t most = tokens < 512 ? 1 : tokens / 256;
   c.splits = (int32_t)(want < most ? want : most);
-  c.per_split = ((tokens + c.splits - 1) / c.splits + kStep - 1) / kStep * kStep;
+  c.per_split = ((tokens + c.splits - 1) / c.splits + kStep - 1) / kStep * kStep;   // whole steps
   if (c.per_split) c.splits = (int32_t)((tokens + c.per_split - 1) / c.per_split);
   c.per_strip = tokens < 64 * 64 ? 64 : (tokens + 63) / 64;
   c.strips = (int32_t)((tokens + c.per_strip - 1) / c.per_strip);
