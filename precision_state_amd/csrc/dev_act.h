@@ -23,35 +23,71 @@ __device__ __forceinline__ uint32_t div_by(uint32_t u, const FastDiv& f) { retur
 // Eight values of a row as they lie in memory.
 template <int TYPE>
 struct Raw8 {
-  u32x4 w[TYPE == PS_TYPE_F32 ? 2 : 1];
+  u32x4 w[TYPE == PS_TYPE_F32 ? 2 : 1];   // [1] is there for fp32 only
 };
 template <int TYPE>
 constexpr int kBytes = TYPE == PS_TYPE_F32 ? 4 : 2;
 
-// Element `at` on, the first `left` of eight (left <= 0: none); the others are 0.
+// The eight values from element `at` of a row on, of which `left` exist (left <=
+// 0: none). Where fewer than eight do, the load takes the row's last eight, so
+// that a lane at the end of a row costs no more than the others; widen8 puts
+// them in place. `wide`: the row has eight at all.
 template <int TYPE, bool STREAM = true>
-__device__ __forceinline__ Raw8<TYPE> load8(const void* base, int64_t at, int left) {
-  Raw8<TYPE> r;
-  if (left >= 8) {
+__device__ __forceinline__ Raw8<TYPE> load8(const void* base, int64_t at, int left, bool wide) {
+  Raw8<TYPE> r = {};
+  if (left <= 0) return r;
+  at -= left < 8 ? 8 - left : 0;
+  if (wide) {
     const GLOBAL u32x4_any* p = (const GLOBAL u32x4_any*)((const char*)base + at * kBytes<TYPE>);
 #pragma unroll
     for (int i = 0; i < (int)sizeof(r.w) / 16; ++i) r.w[i] = STREAM ? (u32x4)__builtin_nontemporal_load(p + i) : (u32x4)p[i];
     return r;
   }
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if (TYPE == PS_TYPE_F32) {
-      r.w[j / 4][j % 4] = j < left ? ((const GLOBAL uint32_t*)base)[at + j] : 0u;
-    } else {
-      const uint32_t h = j < left ? ((const GLOBAL uint16_t*)base)[at + j] : 0u;
-      r.w[0][j / 2] = j & 1 ? r.w[0][j / 2] | h << 16 : h;
-    }
+  for (int j = 1; j < 8; ++j) {
+    if (j < 8 - left) continue;
+    if (TYPE == PS_TYPE_F32)
+      r.w[j / 4][j % 4] = ((const GLOBAL uint32_t*)base)[at + j];
+    else
+      r.w[0][j / 2] |= (uint32_t)((const GLOBAL uint16_t*)base)[at + j] << (16 * (j & 1));
   }
   return r;
 }
 
+// 128 bits shifted down by 0 < n < 128.
+__device__ __forceinline__ u32x4 shift_down(u32x4 w, int n) {
+  uint64_t lo = (uint64_t)w[1] << 32 | w[0], hi = (uint64_t)w[3] << 32 | w[2];
+  if (n >= 64) {
+    lo = hi;
+    hi = 0;
+  }
+  n &= 63;
+  lo = lo >> n | (hi << 1) << (63 - n);
+  hi >>= n;
+  return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+}
+
 template <int TYPE>
-__device__ __forceinline__ void widen8(const Raw8<TYPE>& r, float* d) {
+__device__ __forceinline__ void widen8(Raw8<TYPE> r, int left, float* d) {
+  if (left > 0 && left < 8) {
+    const int k = 8 - left;
+    if (TYPE == PS_TYPE_F32) {
+      if (k & 4) {
+        r.w[0] = r.w[1];
+        r.w[1] = u32x4{0, 0, 0, 0};
+      }
+      if (k & 2) {
+        r.w[0] = u32x4{r.w[0][2], r.w[0][3], r.w[1][0], r.w[1][1]};
+        r.w[1] = u32x4{r.w[1][2], r.w[1][3], 0, 0};
+      }
+      if (k & 1) {
+        r.w[0] = u32x4{r.w[0][1], r.w[0][2], r.w[0][3], r.w[1][0]};
+        r.w[1] = u32x4{r.w[1][1], r.w[1][2], r.w[1][3], 0};
+      }
+    } else {
+      r.w[0] = shift_down(r.w[0], 16 * k);
+    }
+  }
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     if (TYPE == PS_TYPE_F32) {
@@ -105,13 +141,15 @@ __device__ __forceinline__ void store8(void* base, int64_t at, int left, const f
     }
 }
 
-// Eight codes.
-__device__ __forceinline__ u32x2_any load_codes8(const uint8_t* base, int64_t at, int left) {
-  if (left >= 8) return __builtin_nontemporal_load((const GLOBAL u32x2_any*)(base + at));
+// Eight codes, as load8.
+__device__ __forceinline__ u32x2_any load_codes8(const uint8_t* base, int64_t at, int left, bool wide) {
   u32x2_any r = {0, 0};
+  if (left <= 0) return r;
+  at -= left < 8 ? 8 - left : 0;
+  if (wide) return __builtin_nontemporal_load((const GLOBAL u32x2_any*)(base + at));
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (j < left) r[j / 4] |= (uint32_t)((const GLOBAL uint8_t*)base)[at + j] << (8 * (j % 4));
+  for (int j = 1; j < 8; ++j)
+    if (j >= 8 - left) r[j / 4] |= (uint32_t)((const GLOBAL uint8_t*)base)[at + j] << (8 * (j % 4));
   return r;
 }
 
@@ -125,19 +163,23 @@ __device__ __forceinline__ void store_codes8(uint8_t* base, int64_t at, int left
     if (j < left) ((GLOBAL uint8_t*)base)[at + j] = (uint8_t)(c[j / 4] >> (8 * (j % 4)));
 }
 
-__device__ __forceinline__ void codes_to_f32(u32x2_any c, float* d) {
+__device__ __forceinline__ void codes_to_f32(u32x2_any c, int left, float* d) {
+  if (left > 0 && left < 8) {
+    const uint64_t w = ((uint64_t)c[1] << 32 | c[0]) >> (8 * (8 - left));
+    c = u32x2_any{(uint32_t)w, (uint32_t)(w >> 32)};
+  }
   e4m3_unpack4(c[0], d);
   e4m3_unpack4(c[1], d + 4);
 }
 
 // Eight values of a vector of any type (uniform), kept in the caches.
-__device__ __forceinline__ void load_vec8(const void* v, int type, int64_t at, int left, float* d) {
+__device__ __forceinline__ void load_vec8(const void* v, int type, int64_t at, int left, bool wide, float* d) {
   if (type == PS_TYPE_F32)
-    widen8<PS_TYPE_F32>(load8<PS_TYPE_F32, false>(v, at, left), d);
+    widen8<PS_TYPE_F32>(load8<PS_TYPE_F32, false>(v, at, left, wide), left, d);
   else if (type == PS_TYPE_BF16)
-    widen8<PS_TYPE_BF16>(load8<PS_TYPE_BF16, false>(v, at, left), d);
+    widen8<PS_TYPE_BF16>(load8<PS_TYPE_BF16, false>(v, at, left, wide), left, d);
   else
-    widen8<PS_TYPE_F16>(load8<PS_TYPE_F16, false>(v, at, left), d);
+    widen8<PS_TYPE_F16>(load8<PS_TYPE_F16, false>(v, at, left, wide), left, d);
 }
 
 // Codes and scale of a block of 128 values, eight on each of a DPP row's 16
@@ -162,12 +204,18 @@ __device__ __forceinline__ u32x2_any encode_block(const float* x, float& s) {
   return c;
 }
 
-// Sum over the wave, on every lane, in an order of its own kind for all sizes.
-__device__ __forceinline__ float wave_sum(float x) {
+// Sums over a DPP row's 16 lanes and over the wave, on every lane, always in the
+// same order.
+__device__ __forceinline__ float row16_sum(float x) {
   x += dpp<0xB1>(x);
   x += dpp<0x4E>(x);
   x += dpp<0x141>(x);
   x += dpp<0x140>(x);
+  return x;
+}
+
+__device__ __forceinline__ float wave_sum(float x) {
+  x = row16_sum(x);
   const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   x = __uint_as_float(p[0]) + __uint_as_float(p[1]);
   const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);

@@ -38,14 +38,14 @@ __global__ __launch_bounds__(kThreads) void k_encode_act(ActGrid g, const void* 
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const Place p(g, unit_of(k, K));
-    raw[k] = load8<TYPE>(x, p.at(ld), p.left);
+    raw[k] = load8<TYPE>(x, p.at(ld), p.left, g.cols >= 8);
   }
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const uint32_t u = unit_of(k, K);
     const Place p(g, u);
     float v[8], s;
-    widen8<TYPE>(raw[k], v);
+    widen8<TYPE>(raw[k], p.left, v);
     const u32x2_any c = encode_block(v, s);
     store_codes8(code, p.at(g.cols), p.left, c);
     if (p.in && (threadIdx.x & 15) == 0) scale[u] = s;
@@ -61,14 +61,14 @@ __global__ __launch_bounds__(kThreads) void k_decode_act(ActGrid g, const uint8_
   for (int k = 0; k < K; ++k) {
     const uint32_t u = unit_of(k, K);
     const Place p(g, u);
-    c[k] = load_codes8(code, p.at(g.cols), p.left);
+    c[k] = load_codes8(code, p.at(g.cols), p.left, g.cols >= 8);
     s[k] = p.in ? scale[u] : 0.0f;
   }
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const Place p(g, unit_of(k, K));
     float v[8];
-    codes_to_f32(c[k], v);
+    codes_to_f32(c[k], p.left, v);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] *= s[k];
     store8<TYPE>(x, p.at(ld), p.left, v);
@@ -102,16 +102,16 @@ __global__ __launch_bounds__(kThreads) void k_glu_forward(ActGrid g, GluArgs t) 
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const Place p(g, unit_of(k, K));
-    ra[k] = load8<TYPE>(t.a, p.at(t.lda), p.left);
-    if (GATED) rb[k] = load8<TYPE>(t.b, p.at(t.ldb), p.left);
+    ra[k] = load8<TYPE>(t.a, p.at(t.lda), p.left, g.cols >= 8);
+    if (GATED) rb[k] = load8<TYPE>(t.b, p.at(t.ldb), p.left, g.cols >= 8);
   }
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const uint32_t u = unit_of(k, K);
     const Place p(g, u);
     float a[8], b[8], o[8], s;
-    widen8<TYPE>(ra[k], a);
-    if (GATED) widen8<TYPE>(rb[k], b);
+    widen8<TYPE>(ra[k], p.left, a);
+    if (GATED) widen8<TYPE>(rb[k], p.left, b);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       float slope;
@@ -142,11 +142,11 @@ __global__ __launch_bounds__(kThreads) void k_glu_backward(ActGrid g, GluArgs t)
   for (int k = 0; k < K; ++k) {
     const uint32_t u = unit_of(k, K);
     const Place p(g, u);
-    rd[k] = load8<TYPE>(t.dout, p.at(t.ldd), p.left);
-    ca[k] = load_codes8(t.a_code, p.at(g.cols), p.left);
+    rd[k] = load8<TYPE>(t.dout, p.at(t.ldd), p.left, g.cols >= 8);
+    ca[k] = load_codes8(t.a_code, p.at(g.cols), p.left, g.cols >= 8);
     sa[k] = p.in ? t.a_scale[u] : 0.0f;
     if (GATED) {
-      cb[k] = load_codes8(t.b_code, p.at(g.cols), p.left);
+      cb[k] = load_codes8(t.b_code, p.at(g.cols), p.left, g.cols >= 8);
       sb[k] = p.in ? t.b_scale[u] : 0.0f;
     }
   }
@@ -154,9 +154,9 @@ __global__ __launch_bounds__(kThreads) void k_glu_backward(ActGrid g, GluArgs t)
   for (int k = 0; k < K; ++k) {
     const Place p(g, unit_of(k, K));
     float d[8], a[8], b[8], da[8], db[8], o[8];
-    widen8<TYPE>(rd[k], d);
-    codes_to_f32(ca[k], a);
-    if (GATED) codes_to_f32(cb[k], b);
+    widen8<TYPE>(rd[k], p.left, d);
+    codes_to_f32(ca[k], p.left, a);
+    if (GATED) codes_to_f32(cb[k], p.left, b);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       float f, slope;

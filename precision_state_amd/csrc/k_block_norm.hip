@@ -11,31 +11,28 @@
 namespace ps {
 namespace {
 
-// Sums of a team of NT lanes, on every lane: a wave's alone, or those of its
-// waves through shared memory. `turn` alternates between two places, so that
-// one barrier a sum is enough.
-template <int NT, int N>
+// Sums of a team of lanes, on every lane: a wave's alone, or those of the
+// workgroup's waves through shared memory. `turn` alternates between two places,
+// so that one barrier a sum is enough.
+constexpr int kMostWaves = 16;
+template <int N>
 struct TeamSum {
-  static constexpr int kWaves = NT / 64;
-  float (*lds)[kWaves][N];
+  float (*lds)[kMostWaves][N];
+  int waves;
   int turn = 0;
   __device__ __forceinline__ void operator()(float* v) {
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
-    if (NT == 64) return;
-    const int wave = threadIdx.x / 64;
+    if (waves == 1) return;
     if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) lds[turn][wave][i] = v[i];
+      for (int i = 0; i < N; ++i) lds[turn][threadIdx.x / 64][i] = v[i];
     }
     __syncthreads();
+    // each row of 16 lanes reads all waves' sums at once
+    const int w = threadIdx.x & 15;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      float s = lds[turn][0][i];
-#pragma unroll
-      for (int w = 1; w < kWaves; ++w) s += lds[turn][w][i];
-      v[i] = s;
-    }
+    for (int i = 0; i < N; ++i) v[i] = row16_sum(w < waves ? lds[turn][w][i] : 0.0f);
     turn ^= 1;
   }
 };
@@ -62,8 +59,8 @@ __device__ __forceinline__ int64_t seg_offset(const NormArgs& p, uint32_t by_seg
 
 
 // z[0 .. V-1][8] of a row becomes its normalised values; the factor r is returned.
-template <int NT, int V, class Sum>
-__device__ __forceinline__ float normalise(const NormArgs& p, int kind, float eps, int lane, Sum& sum, float (*z)[8]) {
+template <int V, class Sum>
+__device__ __forceinline__ float normalise(const NormArgs& p, int kind, float eps, int lane, int nt, Sum& sum, float (*z)[8]) {
   float s[1];
   if (kind == PS_NORM_LAYER) {
     s[0] = 0;
@@ -76,7 +73,7 @@ __device__ __forceinline__ float normalise(const NormArgs& p, int kind, float ep
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) z[v][j] = (v * NT + lane) * 8 + j < p.cols ? z[v][j] - mean : 0.0f;
+      for (int j = 0; j < 8; ++j) z[v][j] = (v * nt + lane) * 8 + j < p.cols ? z[v][j] - mean : 0.0f;
   }
   s[0] = 0;
 #pragma unroll
@@ -99,39 +96,40 @@ __device__ __forceinline__ u32x2_any pack_codes(const float* z) {
   return c;
 }
 
-// Rows by teams of NT lanes, V times eight columns on each.
-template <int TYPE, int NT, int V>
-__global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_norm_forward(NormArgs p) {
-  constexpr int kRows = NT < 256 ? 256 / NT : 1;
-  __shared__ float lds[2][NT / 64][1];
-  TeamSum<NT, 1> sum{lds};
-  const int lane = threadIdx.x % NT;
-  int row = blockIdx.x * kRows + threadIdx.x / NT;
-  if (NT == 64) row = __builtin_amdgcn_readfirstlane(row);
+// A row by one team: the waves of a workgroup (V times eight columns on each
+// lane, as few lanes as hold the row), or, up to 1024 columns, a wave with three
+// others beside it.
+template <int TYPE, int V, bool WAVE>
+__global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_forward(NormArgs p) {
+  __shared__ float lds[2][kMostWaves][1];
+  const int nt = WAVE ? 64 : blockDim.x, lane = WAVE ? threadIdx.x & 63 : threadIdx.x;
+  TeamSum<1> sum{lds, nt / 64};
+  const int row = WAVE ? __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + threadIdx.x / 64) : blockIdx.x;
   if (row >= p.rows) return;   // whole teams leave
   int seg = 0;
   if (p.seg_start) {
     seg = find_seg(p.seg_start, p.n_segs, row);
     if (seg < 0) return;
   }
+  const bool wide = p.cols >= 8;
   float z[V][8];
   Raw8<TYPE> rx[V], ry[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int col = (v * NT + lane) * 8;
-    if (p.y) ry[v] = load8<TYPE>(p.y, (int64_t)row * p.ldy + col, p.cols - col);
-    rx[v] = load8<TYPE>(p.x, (int64_t)row * p.ldx + col, p.cols - col);
+    const int col = (v * nt + lane) * 8;
+    if (p.y) ry[v] = load8<TYPE>(p.y, (int64_t)row * p.ldy + col, p.cols - col, wide);
+    rx[v] = load8<TYPE>(p.x, (int64_t)row * p.ldx + col, p.cols - col, wide);
   }
   if (p.y) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) widen8<TYPE>(ry[v], z[v]);
+    for (int v = 0; v < V; ++v) widen8<TYPE>(ry[v], p.cols - (v * nt + lane) * 8, z[v]);
     if (p.post != PS_NORM_NONE) {
-      const float r = normalise<NT, V>(p, p.post, p.post_eps, lane, sum, z);
+      const float r = normalise<V>(p, p.post, p.post_eps, lane, nt, sum, z);
       if (p.y_rstd && lane == 0) p.y_rstd[row] = r;
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int col = (v * NT + lane) * 8, left = p.cols - col;
+      const int col = (v * nt + lane) * 8, left = p.cols - col;
       if (p.y_code) {
         u32x2_any c;
         if (p.post != PS_NORM_NONE) {
@@ -146,40 +144,40 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_norm_forward(NormArgs p
       }
       float m[8], x[8];
       if (p.w1) {
-        load_vec8(p.w1, p.vec_type, col, left, m);
+        load_vec8(p.w1, p.vec_type, col, left, wide, m);
 #pragma unroll
         for (int j = 0; j < 8; ++j) z[v][j] *= m[j];
       }
       if (p.gate) {
-        load_vec8(p.gate, p.vec_type, seg_offset(p, PS_NORM_GATE_BY_SEG, seg) + col, left, m);
+        load_vec8(p.gate, p.vec_type, seg_offset(p, PS_NORM_GATE_BY_SEG, seg) + col, left, wide, m);
 #pragma unroll
         for (int j = 0; j < 8; ++j) z[v][j] *= m[j];
       }
-      widen8<TYPE>(rx[v], x);
+      widen8<TYPE>(rx[v], left, x);
 #pragma unroll
       for (int j = 0; j < 8; ++j) z[v][j] = __builtin_fmaf(p.beta, z[v][j], p.alpha * x[j]);
       store8<TYPE>(p.h, (int64_t)row * p.ldh + col, left, z[v]);
     }
   } else {
 #pragma unroll
-    for (int v = 0; v < V; ++v) widen8<TYPE>(rx[v], z[v]);
+    for (int v = 0; v < V; ++v) widen8<TYPE>(rx[v], p.cols - (v * nt + lane) * 8, z[v]);
   }
-  const float r = normalise<NT, V>(p, p.pre, p.pre_eps, lane, sum, z);
+  const float r = normalise<V>(p, p.pre, p.pre_eps, lane, nt, sum, z);
   if (p.h_rstd && lane == 0) p.h_rstd[row] = r;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int col = (v * NT + lane) * 8, left = p.cols - col;
+    const int col = (v * nt + lane) * 8, left = p.cols - col;
     if (p.h_code) store_codes8(p.h_code, (int64_t)row * p.cols + col, left, pack_codes(z[v]));
     float m[8], a[8];
     const int64_t o = seg_offset(p, PS_NORM_MOD_BY_SEG, seg) + col;
     if (p.mul) {
-      load_vec8(p.mul, p.vec_type, o, left, m);
+      load_vec8(p.mul, p.vec_type, o, left, wide, m);
       const float one = p.flags & PS_NORM_MUL_PLUS_ONE ? 1.0f : 0.0f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) z[v][j] *= one + m[j];
     }
     if (p.add) {
-      load_vec8(p.add, p.vec_type, o, left, a);
+      load_vec8(p.add, p.vec_type, o, left, wide, a);
 #pragma unroll
       for (int j = 0; j < 8; ++j) z[v][j] += a[j];
     }
@@ -188,7 +186,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_norm_forward(NormArgs p
 }
 
 // g becomes back(g, z, r): r (g - [mean g] - z mean(g z)).
-template <int NT, int V, class Sum>
+template <int V, class Sum>
 __device__ __forceinline__ void back(const NormArgs& p, int kind, float r, Sum& sum, float (*g)[8], const float (*z)[8]) {
   float s[2] = {0, 0};
 #pragma unroll
@@ -206,34 +204,95 @@ __device__ __forceinline__ void back(const NormArgs& p, int kind, float r, Sum& 
     for (int j = 0; j < 8; ++j) g[v][j] = r * (__builtin_fmaf(-gz, z[v][j], g[v][j]) - m);
 }
 
+// A row's inputs of the backward pass as they lie in memory.
+template <int TYPE, int V>
+struct RowIn {
+  Raw8<TYPE> dn[V], dh[V];
+  u32x2_any ch[V], cy[V];
+  float s[V], h_rstd, y_rstd;
+};
+
 // A workgroup takes a strip of rows and keeps the column sums of its gradients
 // in registers; where the segment changes, and at the end, they go to the
-// strip's part of that segment.
-template <int TYPE, int NT, int V>
-__global__ __launch_bounds__(NT) void k_norm_backward(NormArgs p) {
-  __shared__ float lds[2][NT / 64][2];
-  TeamSum<NT, 2> sum{lds};
-  const int lane = threadIdx.x;
+// strip's part of that segment. The next row is loaded before the sums of this
+// one, whose barriers its latency would otherwise add to; a segment's vectors
+// stay in registers, since a load behind those of the next row would wait for
+// them. The widest rows (V > 1) leave no registers for either.
+template <int TYPE, int V>
+__global__ __launch_bounds__(V == 1 ? 1024 : 512) void k_norm_backward(NormArgs p) {
+  constexpr bool kAhead = V == 1;
+  __shared__ float lds[2][kMostWaves][2];
+  const int nt = blockDim.x, lane = threadIdx.x;
+  TeamSum<2> sum{lds, nt / 64};
   const int first = blockIdx.x * p.strip, last = min(p.rows - first, p.strip) + first;
   const int64_t n_part = (int64_t)p.slots * p.cols;
-  const bool branch = p.dy != nullptr;
-  const bool has_yh = branch && (p.post != PS_NORM_NONE || p.gate);
+  const bool branch = p.dy != nullptr, post = p.post != PS_NORM_NONE;
+  const bool wide = p.cols >= 8;
+  const bool has_yh = branch && (post || p.gate);
   float acc[3][V][8];
-  int seg = -1, seg_end = first;   // the segment of the sums, and where it ends
+  float km[V][8], ky[V][8];        // m, and branch_scale * gate * post_weight (0 for columns that do not exist)
+  int seg = -1, seg_end = first;   // the segment of the sums and vectors, and where it ends
 
-  auto flush = [&]() {
+  auto flush = [&]() __attribute__((always_inline)) {
     if (seg < 0) return;
     const int64_t o = (int64_t)(blockIdx.x + seg) * p.cols;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int col = (v * NT + lane) * 8, left = p.cols - col;
+      const int col = (v * nt + lane) * 8, left = p.cols - col;
       if (p.d_add) store8<PS_TYPE_F32, false>(p.part, o + col, left, acc[0][v]);
       if (p.d_mul) store8<PS_TYPE_F32, false>(p.part + n_part, o + col, left, acc[1][v]);
       if (p.d_gate || p.d_w1) store8<PS_TYPE_F32, false>(p.part + 2 * n_part, o + col, left, acc[2][v]);
     }
   };
+  auto vectors = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int col = (v * nt + lane) * 8, left = p.cols - col;
+      const float one = p.flags & PS_NORM_MUL_PLUS_ONE ? 1.0f : 0.0f;
+      float m[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) km[v][j] = 1.0f, ky[v][j] = j < left ? p.beta : 0.0f;
+      if (p.mul) {
+        load_vec8(p.mul, p.vec_type, seg_offset(p, PS_NORM_MOD_BY_SEG, seg) + col, left, wide, m);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) km[v][j] = one + m[j];
+      }
+      if (!branch) continue;
+      if (p.gate) {
+        load_vec8(p.gate, p.vec_type, seg_offset(p, PS_NORM_GATE_BY_SEG, seg) + col, left, wide, m);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ky[v][j] *= m[j];
+      }
+      if (p.w1) {
+        load_vec8(p.w1, p.vec_type, col, left, wide, m);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ky[v][j] *= m[j];
+      }
+    }
+  };
+  RowIn<TYPE, V> next;
+  auto load = [&](int row) __attribute__((always_inline)) {
+    next.h_rstd = p.h_rstd[row];
+    if (branch && post) next.y_rstd = p.y_rstd[row];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int col = (v * nt + lane) * 8, left = p.cols - col;
+      next.dn[v] = load8<TYPE>(p.dn, (int64_t)row * p.lddn + col, left, wide);
+      next.ch[v] = load_codes8(p.h_code, (int64_t)row * p.cols + col, left, wide);
+      if (p.dh) next.dh[v] = load8<TYPE>(p.dh, (int64_t)row * p.lddh + col, left, wide);
+      if (has_yh) {
+        next.cy[v] = load_codes8(p.y_code, (int64_t)row * p.cols + col, left, wide);
+        if (!post)
+          next.s[v] = left > 0 ? p.y_scale[(int64_t)row * ((p.cols + kActBlock - 1) / kActBlock) + col / kActBlock] : 0.0f;
+      }
+    }
+  };
 
+  if (kAhead) load(first);
   for (int row = first; row < last; ++row) {
+    if (!kAhead) load(row);
+    const RowIn<TYPE, V> in = next;
+    if (kAhead && row + 1 < last) load(row + 1);
     if (row >= seg_end) {   // the first row, or the first of another segment
       flush();
       seg = 0;
@@ -249,44 +308,31 @@ __global__ __launch_bounds__(NT) void k_norm_backward(NormArgs p) {
         for (int v = 0; v < V; ++v)
 #pragma unroll
           for (int j = 0; j < 8; ++j) acc[i][v][j] = 0;
+      if (kAhead && seg >= 0) vectors();
     }
     if (seg < 0) continue;
+    if (!kAhead) vectors();
     float g[V][8], z[V][8];
-    Raw8<TYPE> rdn[V], rdh[V];
-    u32x2_any ch[V], cy[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int col = (v * NT + lane) * 8, left = p.cols - col;
-      rdn[v] = load8<TYPE>(p.dn, (int64_t)row * p.lddn + col, left);
-      ch[v] = load_codes8(p.h_code, (int64_t)row * p.cols + col, left);
-      if (p.dh) rdh[v] = load8<TYPE>(p.dh, (int64_t)row * p.lddh + col, left);
-      if (has_yh) cy[v] = load_codes8(p.y_code, (int64_t)row * p.cols + col, left);
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int col = (v * NT + lane) * 8, left = p.cols - col;
-      widen8<TYPE>(rdn[v], g[v]);
-      codes_to_f32(ch[v], z[v]);
+      const int left = p.cols - (v * nt + lane) * 8;
+      widen8<TYPE>(in.dn[v], left, g[v]);
+      codes_to_f32(in.ch[v], left, z[v]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         acc[0][v][j] += g[v][j];
         acc[1][v][j] = __builtin_fmaf(g[v][j], z[v][j], acc[1][v][j]);
       }
-      if (p.mul) {
-        float m[8];
-        load_vec8(p.mul, p.vec_type, seg_offset(p, PS_NORM_MOD_BY_SEG, seg) + col, left, m);
-        const float one = p.flags & PS_NORM_MUL_PLUS_ONE ? 1.0f : 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) g[v][j] *= one + m[j];
-      }
+      for (int j = 0; j < 8; ++j) g[v][j] *= km[v][j];
     }
-    back<NT, V>(p, p.pre, p.h_rstd[row], sum, g, z);
+    back<V>(p, p.pre, in.h_rstd, sum, g, z);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int col = (v * NT + lane) * 8, left = p.cols - col;
+      const int col = (v * nt + lane) * 8, left = p.cols - col;
       if (p.dh) {
         float d[8];
-        widen8<TYPE>(rdh[v], d);
+        widen8<TYPE>(in.dh[v], left, d);
 #pragma unroll
         for (int j = 0; j < 8; ++j) g[v][j] += d[j];
       }
@@ -295,49 +341,38 @@ __global__ __launch_bounds__(NT) void k_norm_backward(NormArgs p) {
       for (int j = 0; j < 8; ++j) o[j] = p.alpha * g[v][j];
       store8<TYPE>(p.dx, (int64_t)row * p.lddx + col, left, o);
       if (!branch) continue;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) g[v][j] = left > j ? p.beta * g[v][j] : 0.0f;
       if (has_yh) {
-        codes_to_f32(cy[v], z[v]);
-        if (p.post == PS_NORM_NONE) {
-          const float s = left > 0 ? p.y_scale[(int64_t)row * ((p.cols + kActBlock - 1) / kActBlock) + col / kActBlock] : 0.0f;
+        codes_to_f32(in.cy[v], left, z[v]);
+        if (!post) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) z[v][j] *= s;
+          for (int j = 0; j < 8; ++j) z[v][j] *= in.s[v];
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[2][v][j] = __builtin_fmaf(g[v][j], z[v][j], acc[2][v][j]);
       }
-      float m[8];
-      if (p.gate) {
-        load_vec8(p.gate, p.vec_type, seg_offset(p, PS_NORM_GATE_BY_SEG, seg) + col, left, m);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) g[v][j] *= m[j];
-      }
-      if (p.w1) {
-        load_vec8(p.w1, p.vec_type, col, left, m);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) g[v][j] *= m[j];
-      }
+      for (int j = 0; j < 8; ++j) g[v][j] *= ky[v][j];
     }
     if (!branch) continue;
-    if (p.post != PS_NORM_NONE) back<NT, V>(p, p.post, p.y_rstd[row], sum, g, z);
+    if (post) back<V>(p, p.post, in.y_rstd, sum, g, z);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int col = (v * NT + lane) * 8;
+      const int col = (v * nt + lane) * 8;
       store8<TYPE>(p.dy, (int64_t)row * p.lddy + col, p.cols - col, g[v]);
     }
   }
   flush();
 }
 
-// The strips' parts, added up. A workgroup joins 64 columns of one gradient (and
-// one segment of it where it has one for each): 16 groups of lanes take every
-// 16th strip, and their sums are added in order.
-constexpr int kJoinCols = 64, kJoinGroups = 16;
+// The strips' parts, added up. A workgroup joins 32 columns of one gradient (and
+// one segment of it where it has one for each): its groups of 32 lanes take the
+// strips in turn, and their sums are added in order. 32 groups where there are
+// many strips to a segment, else 8.
+constexpr int kJoinCols = 32;
 
 struct JoinOf {
   float* out;
-  int which;      // 0 sum of dn, 1 of dn xh, 2 of p yh
+  int which;      // 0 sum of dn, 1 of dn xh, 2 of G yh
   bool by_seg;
   bool by_gate;   // times the gate (that of the segment), before the segments are added
   bool by_w1;     // times post_weight, at the end
@@ -349,6 +384,7 @@ __device__ __forceinline__ float vec1(const void* v, int type, int64_t at) {
   return (float)((const _Float16*)v)[at];
 }
 
+template <int kJoinGroups>
 __global__ __launch_bounds__(kJoinCols * kJoinGroups) void k_norm_join(NormArgs p, JoinOf j0, JoinOf j1, JoinOf j2, JoinOf j3) {
   const JoinOf j = blockIdx.y == 0 ? j0 : blockIdx.y == 1 ? j1 : blockIdx.y == 2 ? j2 : j3;
   if (!j.by_seg && blockIdx.z) return;
@@ -367,6 +403,7 @@ __global__ __launch_bounds__(kJoinCols * kJoinGroups) void k_norm_join(NormArgs 
       }
       if (hi <= lo) continue;
       float s = 0;
+#pragma unroll 8
       for (int strip = lo / p.strip + group; strip <= (hi - 1) / p.strip; strip += kJoinGroups)
         s += part[(int64_t)(strip + b) * p.cols + col];
       if (j.by_gate) s *= vec1(p.gate, p.vec_type, seg_offset(p, PS_NORM_GATE_BY_SEG, b) + col);
@@ -378,42 +415,41 @@ __global__ __launch_bounds__(kJoinCols * kJoinGroups) void k_norm_join(NormArgs 
   if (group || col >= p.cols) return;
 #pragma unroll
   for (int i = 1; i < kJoinGroups; ++i) total += lds[i][c];
+  if (j.which == 2) total *= p.beta;
   if (j.by_w1) total *= vec1(p.w1, p.vec_type, col);
   float* out = j.out + (j.by_seg ? (int64_t)blockIdx.z * p.cols : 0) + col;
   *out = p.accumulate ? *out + total : total;
 }
 
-template <int TYPE, int NT, int V>
+// Waves that hold `lanes` times eight columns, v times eight a lane.
+int waves_for(int lanes, int v) { return (lanes + 64 * v - 1) / (64 * v); }
+
+template <int TYPE>
 ps_status forward(const NormArgs& p, hipStream_t s) {
-  constexpr int kRows = NT < 256 ? 256 / NT : 1;
-  hipLaunchKernelGGL((k_norm_forward<TYPE, NT, V>), dim3((p.rows + kRows - 1) / kRows), dim3(NT * kRows), 0, s, p);
+  const int lanes = (p.cols + 7) / 8;
+  if (lanes <= 128) {
+    const dim3 grid((p.rows + 3) / 4);
+    if (lanes <= 64)
+      hipLaunchKernelGGL((k_norm_forward<TYPE, 1, true>), grid, dim3(256), 0, s, p);
+    else
+      hipLaunchKernelGGL((k_norm_forward<TYPE, 2, true>), grid, dim3(256), 0, s, p);
+  } else {
+    hipLaunchKernelGGL((k_norm_forward<TYPE, 2, false>), dim3(p.rows), dim3(waves_for(lanes, 2) * 64), 0, s, p);
+  }
   return hip_check(hipGetLastError(), "k_norm_forward launch");
 }
 
-template <int TYPE, int NT, int V>
+template <int TYPE>
 ps_status backward(const NormArgs& p, hipStream_t s) {
-  hipLaunchKernelGGL((k_norm_backward<TYPE, NT, V>), dim3((p.rows + p.strip - 1) / p.strip), dim3(NT), 0, s, p);
+  const int lanes = (p.cols + 7) / 8;
+  const dim3 grid((p.rows + p.strip - 1) / p.strip);
+  if (lanes <= 1024)
+    hipLaunchKernelGGL((k_norm_backward<TYPE, 1>), grid, dim3(waves_for(lanes, 1) * 64), 0, s, p);
+  else if (lanes <= 1536)
+    hipLaunchKernelGGL((k_norm_backward<TYPE, 3>), grid, dim3(waves_for(lanes, 3) * 64), 0, s, p);
+  else
+    hipLaunchKernelGGL((k_norm_backward<TYPE, 4>), grid, dim3(waves_for(lanes, 4) * 64), 0, s, p);
   return hip_check(hipGetLastError(), "k_norm_backward launch");
-}
-
-template <int TYPE>
-ps_status forward(const NormArgs& p, hipStream_t s) {
-  if (p.cols <= 512) return forward<TYPE, 64, 1>(p, s);
-  if (p.cols <= 1024) return forward<TYPE, 64, 2>(p, s);
-  if (p.cols <= 2048) return forward<TYPE, 256, 1>(p, s);
-  if (p.cols <= 4096) return forward<TYPE, 256, 2>(p, s);
-  if (p.cols <= 8192) return forward<TYPE, 512, 2>(p, s);
-  return forward<TYPE, 1024, 2>(p, s);
-}
-
-template <int TYPE>
-ps_status backward(const NormArgs& p, hipStream_t s) {
-  if (p.cols <= 512) return backward<TYPE, 64, 1>(p, s);
-  if (p.cols <= 1024) return backward<TYPE, 64, 2>(p, s);
-  if (p.cols <= 2048) return backward<TYPE, 256, 1>(p, s);
-  if (p.cols <= 4096) return backward<TYPE, 256, 2>(p, s);
-  if (p.cols <= 8192) return backward<TYPE, 512, 2>(p, s);
-  return backward<TYPE, 1024, 2>(p, s);
 }
 
 }  // namespace
@@ -449,8 +485,11 @@ ps_status launch_norm_backward(const NormArgs& p, int type, hipStream_t s) {
   add(p.d_gate, 2, p.flags & PS_NORM_GATE_BY_SEG, false, p.w1 != nullptr);
   add(p.d_w1, 2, false, p.gate != nullptr, false);
   if (!n) return PS_OK;
-  hipLaunchKernelGGL(k_norm_join, dim3((p.cols + kJoinCols - 1) / kJoinCols, n, by_seg ? p.n_segs : 1),
-                     dim3(kJoinCols * kJoinGroups), 0, s, p, j[0], j[1], j[2], j[3]);
+  const dim3 grid((p.cols + kJoinCols - 1) / kJoinCols, n, by_seg ? p.n_segs : 1);
+  if (p.slots / (by_seg ? p.n_segs : 1) > 128)
+    hipLaunchKernelGGL(k_norm_join<32>, grid, dim3(kJoinCols * 32), 0, s, p, j[0], j[1], j[2], j[3]);
+  else
+    hipLaunchKernelGGL(k_norm_join<8>, grid, dim3(kJoinCols * 8), 0, s, p, j[0], j[1], j[2], j[3]);
   return hip_check(hipGetLastError(), "k_norm_join launch");
 }
 

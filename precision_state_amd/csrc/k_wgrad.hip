@@ -143,9 +143,9 @@ __device__ __forceinline__ void store_dw(const WgradArgs& p, int n, int k, int l
 #pragma unroll
           for (int i = 0; i < 4; ++i) was[i] = w[i];
         } else if (p.dw_type == PS_TYPE_BF16) {
-          widen8<PS_TYPE_BF16>(Raw8<PS_TYPE_BF16>{{{(*h)[0], (*h)[1], 0, 0}}}, was);
+          widen8<PS_TYPE_BF16>(Raw8<PS_TYPE_BF16>{{{(*h)[0], (*h)[1], 0, 0}}}, 8, was);
         } else {
-          widen8<PS_TYPE_F16>(Raw8<PS_TYPE_F16>{{{(*h)[0], (*h)[1], 0, 0}}}, was);
+          widen8<PS_TYPE_F16>(Raw8<PS_TYPE_F16>{{{(*h)[0], (*h)[1], 0, 0}}}, 8, was);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] += was[i];
@@ -399,7 +399,7 @@ __global__ __launch_bounds__(kThreads) void k_column_sums(WgradArgs p) {
   float s[8] = {};
   for (int64_t t = first + group; t < end; t += 8) {
     float v[8];
-    widen8<TYPE>(load8<TYPE, false>(p.dy, t * p.lddy + col, p.n - col), v);
+    widen8<TYPE>(load8<TYPE, false>(p.dy, t * p.lddy + col, p.n - col, p.n >= 8), p.n - col, v);
 #pragma unroll
     for (int j = 0; j < 8; ++j) s[j] += v[j];
   }

@@ -172,8 +172,8 @@ NormArgs norm_args(const ps_block_norm& p) {
 }
 
 int64_t norm_slots(const ps_block_norm& p) {
-  if (p.rows == 0) return 0;
-  const int64_t strip = norm_strip_rows(p.rows);
+  if (p.rows == 0 || p.cols == 0) return 0;
+  const int64_t strip = norm_strip_rows(p.rows, p.cols);
   return (p.rows + strip - 1) / strip + (p.n_segs ? p.n_segs - 1 : 0);
 }
 
@@ -391,7 +391,7 @@ ps_status ps_block_norm_backward(const ps_block_norm* norm, const ps_block_norm_
   k.d_w1 = io->d_post_weight; k.d_gate = io->d_gate;
   k.d_mul = io->d_mul; k.d_add = io->d_add;
   k.part = (float*)io->workspace;
-  k.strip = rows ? norm_strip_rows(rows) : 1;
+  k.strip = rows ? norm_strip_rows(rows, cols) : 1;
   k.slots = (int32_t)norm_slots(p);
   k.accumulate = io->accumulate;
   return launch_norm_backward(k, p.type, (hipStream_t)stream);

@@ -62,12 +62,21 @@ struct NormArgs {
   void *dx, *dy;
   int64_t lddn, lddh, lddx, lddy;
   float *d_w1, *d_gate, *d_mul, *d_add;
-  float* part;              // [3][slots][cols]: sums of dn, dn * xh, p * yh over a strip's rows of a segment
+  float* part;              // [3][slots][cols]: sums of dn, dn * xh, G * yh over a strip's rows of a segment
   int32_t strip, slots;     // rows of a strip; strip i's part of segment b is slot i + b
   int32_t accumulate;
 };
-// Strips of the backward pass: how many rows each, and how many there are.
-inline int32_t norm_strip_rows(int64_t rows) { return (int32_t)((rows + 1023) / 1024); }
+// Rows of a strip of the backward pass. As many strips as workgroups are at
+// work at a time (16 waves a compute unit, 8 for the widest rows), but of 16 rows
+// at least, since a strip's sums cost as much memory traffic as one of its rows;
+// for few rows 256 strips all the same, since rows of a strip take turns.
+inline int32_t norm_strip_rows(int64_t rows, int64_t cols) {
+  const int64_t lanes = (cols + 7) / 8, waves = (lanes + 63) / 64;
+  const int64_t at_a_time = waves > 16 ? 256 : 256 * (16 / (waves > 0 ? waves : 1));
+  int64_t strips = at_a_time < rows / 16 ? at_a_time : rows / 16;
+  if (strips < 256) strips = 256;
+  return (int32_t)((rows + strips - 1) / strips);
+}
 ps_status launch_norm_forward(const NormArgs& p, int type, hipStream_t s);
 ps_status launch_norm_backward(const NormArgs& p, int type, hipStream_t s);
 
