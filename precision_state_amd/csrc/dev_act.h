@@ -11,6 +11,8 @@ namespace ps {
 // The hardware reads and writes global memory at any byte address; these types
 // let the compiler use the widest access for data aligned to its element only.
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32_any __attribute__((aligned(1)));
+typedef uint16_t u16_any __attribute__((aligned(1)));
 typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
 typedef uint32_t u32x4_byte __attribute__((ext_vector_type(4), aligned(1)));
 typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
@@ -28,32 +30,6 @@ struct Raw8 {
 template <int TYPE>
 constexpr int kBytes = TYPE == PS_TYPE_F32 ? 4 : 2;
 
-// The eight values from element `at` of a row on, of which `left` exist (left <=
-// 0: none). Where fewer than eight do, the load takes the row's last eight, so
-// that a lane at the end of a row costs no more than the others; widen8 puts
-// them in place. `wide`: the row has eight at all.
-template <int TYPE, bool STREAM = true>
-__device__ __forceinline__ Raw8<TYPE> load8(const void* base, int64_t at, int left, bool wide) {
-  Raw8<TYPE> r = {};
-  if (left <= 0) return r;
-  at -= left < 8 ? 8 - left : 0;
-  if (wide) {
-    const GLOBAL u32x4_any* p = (const GLOBAL u32x4_any*)((const char*)base + at * kBytes<TYPE>);
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(r.w) / 16; ++i) r.w[i] = STREAM ? (u32x4)__builtin_nontemporal_load(p + i) : (u32x4)p[i];
-    return r;
-  }
-#pragma unroll
-  for (int j = 1; j < 8; ++j) {
-    if (j < 8 - left) continue;
-    if (TYPE == PS_TYPE_F32)
-      r.w[j / 4][j % 4] = ((const GLOBAL uint32_t*)base)[at + j];
-    else
-      r.w[0][j / 2] |= (uint32_t)((const GLOBAL uint16_t*)base)[at + j] << (16 * (j & 1));
-  }
-  return r;
-}
-
 // 128 bits shifted down by 0 < n < 128.
 __device__ __forceinline__ u32x4 shift_down(u32x4 w, int n) {
   uint64_t lo = (uint64_t)w[1] << 32 | w[0], hi = (uint64_t)w[3] << 32 | w[2];
@@ -67,11 +43,49 @@ __device__ __forceinline__ u32x4 shift_down(u32x4 w, int n) {
   return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
 }
 
+// Eight columns of a row, those from `col` on, of which `left` exist (none if
+// left <= 0). Where fewer than eight do, loads take the row's last eight and
+// widen8 moves them into place, so that every lane loads alike: no branch around
+// a load, and no lane whose row ends costs more. Rows of fewer than eight (WIDE
+// false) are loaded one by one.
+template <bool WIDE>
+struct Cols {
+  int left, start;
+  __device__ __forceinline__ Cols(int col, int cols)
+      : left(cols - col), start(WIDE ? __builtin_elementwise_min(col, cols - 8) : col) {}
+};
+
+template <int TYPE, bool STREAM = true, bool WIDE>
+__device__ __forceinline__ Raw8<TYPE> load8(const void* row, const Cols<WIDE>& c) {
+  Raw8<TYPE> r = {};
+  if (WIDE) {
+    const GLOBAL u32x4_any* p = (const GLOBAL u32x4_any*)((const char*)row + (uint32_t)(c.start * kBytes<TYPE>));
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(r.w) / 16; ++i) r.w[i] = STREAM ? (u32x4)__builtin_nontemporal_load(p + i) : (u32x4)p[i];
+    return r;
+  }
+  // each pushes the ones before it down, so that they end where widen8 expects them
+#pragma unroll 1
+  for (int j = 0; j < c.left; ++j) {
+    if (TYPE == PS_TYPE_F32) {
+      u32x4& top = r.w[TYPE == PS_TYPE_F32 ? 1 : 0];
+      r.w[0] = u32x4{r.w[0][1], r.w[0][2], r.w[0][3], top[0]};
+      top = u32x4{top[1], top[2], top[3], ((const GLOBAL uint32_t*)row)[c.start + j]};
+    } else {
+      r.w[0] = shift_down(r.w[0], 16);
+      r.w[0][3] |= (uint32_t)((const GLOBAL uint16_t*)row)[c.start + j] << 16;
+    }
+  }
+  return r;
+}
+
 template <int TYPE>
 __device__ __forceinline__ void widen8(Raw8<TYPE> r, int left, float* d) {
-  if (left > 0 && left < 8) {
+  if (left < 8) {
     const int k = 8 - left;
-    if (TYPE == PS_TYPE_F32) {
+    if (left <= 0) {
+      r = Raw8<TYPE>{};
+    } else if (TYPE == PS_TYPE_F32) {
       if (k & 4) {
         r.w[0] = r.w[1];
         r.w[1] = u32x4{0, 0, 0, 0};
@@ -110,7 +124,7 @@ __device__ __forceinline__ uint32_t round2(float a, float b) {
 }
 
 template <int TYPE, bool STREAM = true>
-__device__ __forceinline__ void store8(void* base, int64_t at, int left, const float* s) {
+__device__ __forceinline__ void store8(void* row, int col, int left, const float* s) {
   if (left <= 0) return;
   Raw8<TYPE> r;
 #pragma unroll
@@ -120,8 +134,9 @@ __device__ __forceinline__ void store8(void* base, int64_t at, int left, const f
     else if (j % 2 == 0)
       r.w[0][j / 2] = round2<TYPE>(s[j], s[j + 1]);
   }
+  char* at = (char*)row + (uint32_t)(col * kBytes<TYPE>);
   if (left >= 8) {
-    GLOBAL u32x4_any* p = (GLOBAL u32x4_any*)((char*)base + at * kBytes<TYPE>);
+    GLOBAL u32x4_any* p = (GLOBAL u32x4_any*)at;
 #pragma unroll
     for (int i = 0; i < (int)sizeof(r.w) / 16; ++i) {
       if (STREAM)
@@ -131,41 +146,79 @@ __device__ __forceinline__ void store8(void* base, int64_t at, int left, const f
     }
     return;
   }
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (j < left) {
-      if (TYPE == PS_TYPE_F32)
-        ((GLOBAL uint32_t*)base)[at + j] = r.w[j / 4][j % 4];
-      else
-        ((GLOBAL uint16_t*)base)[at + j] = (uint16_t)(r.w[0][j / 2] >> (16 * (j & 1)));
+  // the end of a row: four, two and one of what is left
+  if (TYPE == PS_TYPE_F32) {
+    if (left & 4) {
+      *(GLOBAL u32x4_any*)at = r.w[0];
+      r.w[0] = r.w[TYPE == PS_TYPE_F32 ? 1 : 0];
+      at += 16;
     }
+    if (left & 2) {
+      *(GLOBAL u32x2_any*)at = u32x2_any{r.w[0][0], r.w[0][1]};
+      r.w[0][0] = r.w[0][2];
+      at += 8;
+    }
+    if (left & 1) *(GLOBAL uint32_t*)at = r.w[0][0];
+  } else {
+    if (left & 4) {
+      *(GLOBAL u32x2_any*)at = u32x2_any{r.w[0][0], r.w[0][1]};
+      r.w[0][0] = r.w[0][2];
+      r.w[0][1] = r.w[0][3];
+      at += 8;
+    }
+    if (left & 2) {
+      *(GLOBAL u32_any*)at = r.w[0][0];
+      r.w[0][0] = r.w[0][1];
+      at += 4;
+    }
+    if (left & 1) *(GLOBAL uint16_t*)at = (uint16_t)r.w[0][0];
+  }
 }
 
 // Eight codes, as load8.
-__device__ __forceinline__ u32x2_any load_codes8(const uint8_t* base, int64_t at, int left, bool wide) {
-  u32x2_any r = {0, 0};
-  if (left <= 0) return r;
-  at -= left < 8 ? 8 - left : 0;
-  if (wide) return __builtin_nontemporal_load((const GLOBAL u32x2_any*)(base + at));
-#pragma unroll
-  for (int j = 1; j < 8; ++j)
-    if (j >= 8 - left) r[j / 4] |= (uint32_t)((const GLOBAL uint8_t*)base)[at + j] << (8 * (j % 4));
-  return r;
+template <bool WIDE>
+__device__ __forceinline__ u32x2_any load_codes8(const uint8_t* row, const Cols<WIDE>& c) {
+  if (WIDE) return __builtin_nontemporal_load((const GLOBAL u32x2_any*)(row + (uint32_t)c.start));
+  uint64_t w = 0;
+#pragma unroll 1
+  for (int j = 0; j < c.left; ++j) w = w >> 8 | (uint64_t)((const GLOBAL uint8_t*)row)[c.start + j] << 56;
+  return u32x2_any{(uint32_t)w, (uint32_t)(w >> 32)};
 }
 
-__device__ __forceinline__ void store_codes8(uint8_t* base, int64_t at, int left, u32x2_any c) {
+__device__ __forceinline__ void store_codes8(uint8_t* row, int col, int left, u32x2_any c) {
   if (left >= 8) {
-    __builtin_nontemporal_store(c, (GLOBAL u32x2_any*)(base + at));
+    __builtin_nontemporal_store(c, (GLOBAL u32x2_any*)(row + (uint32_t)col));
     return;
   }
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (j < left) ((GLOBAL uint8_t*)base)[at + j] = (uint8_t)(c[j / 4] >> (8 * (j % 4)));
+  if (left <= 0) return;
+  GLOBAL uint8_t* at = (GLOBAL uint8_t*)row + (uint32_t)col;
+  uint32_t w = c[0];
+  if (left & 4) {
+    *(GLOBAL u32_any*)at = w;
+    w = c[1];
+    at += 4;
+  }
+  if (left & 2) {
+    *(GLOBAL u16_any*)at = (uint16_t)w;
+    w >>= 16;
+    at += 2;
+  }
+  if (left & 1) *at = (uint8_t)w;
+}
+
+// Row r of a matrix whose rows are ld elements apart.
+template <int TYPE>
+__device__ __forceinline__ const char* row_of(const void* p, int64_t r, int64_t ld) {
+  return (const char*)p + r * ld * kBytes<TYPE>;
+}
+template <int TYPE>
+__device__ __forceinline__ char* row_of(void* p, int64_t r, int64_t ld) {
+  return (char*)p + r * ld * kBytes<TYPE>;
 }
 
 __device__ __forceinline__ void codes_to_f32(u32x2_any c, int left, float* d) {
-  if (left > 0 && left < 8) {
-    const uint64_t w = ((uint64_t)c[1] << 32 | c[0]) >> (8 * (8 - left));
+  if (left < 8) {
+    const uint64_t w = left > 0 ? ((uint64_t)c[1] << 32 | c[0]) >> (8 * (8 - left)) : 0;
     c = u32x2_any{(uint32_t)w, (uint32_t)(w >> 32)};
   }
   e4m3_unpack4(c[0], d);
@@ -173,13 +226,14 @@ __device__ __forceinline__ void codes_to_f32(u32x2_any c, int left, float* d) {
 }
 
 // Eight values of a vector of any type (uniform), kept in the caches.
-__device__ __forceinline__ void load_vec8(const void* v, int type, int64_t at, int left, bool wide, float* d) {
+template <bool WIDE>
+__device__ __forceinline__ void load_vec8(const void* v, int type, int64_t first, const Cols<WIDE>& c, float* d) {
   if (type == PS_TYPE_F32)
-    widen8<PS_TYPE_F32>(load8<PS_TYPE_F32, false>(v, at, left, wide), left, d);
+    widen8<PS_TYPE_F32>(load8<PS_TYPE_F32, false>((const float*)v + first, c), c.left, d);
   else if (type == PS_TYPE_BF16)
-    widen8<PS_TYPE_BF16>(load8<PS_TYPE_BF16, false>(v, at, left, wide), left, d);
+    widen8<PS_TYPE_BF16>(load8<PS_TYPE_BF16, false>((const uint16_t*)v + first, c), c.left, d);
   else
-    widen8<PS_TYPE_F16>(load8<PS_TYPE_F16, false>(v, at, left, wide), left, d);
+    widen8<PS_TYPE_F16>(load8<PS_TYPE_F16, false>((const uint16_t*)v + first, c), c.left, d);
 }
 
 // Codes and scale of a block of 128 values, eight on each of a DPP row's 16

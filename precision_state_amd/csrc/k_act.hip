@@ -13,46 +13,50 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kTeams = kThreads / 16;   // blocks that a workgroup handles at a time
 
-// The lane's place in unit u.
+// The lane's place in unit u. Lanes of units that do not exist load from the
+// last one and store nothing.
+template <bool WIDE>
 struct Place {
   int64_t row;
-  int col, left;   // first column; how many of its eight exist
+  int col;
   bool in;
-  __device__ __forceinline__ Place(const ActGrid& g, uint32_t u) {
+  Cols<WIDE> c;
+  __device__ __forceinline__ Place(const ActGrid& g, uint32_t u) : c(0, 0) {
     in = u < g.units;
+    u = in ? u : g.units - 1;
     const uint32_t r = div_by(u, g.nb);
     row = r;
     col = (int)(u - r * g.nb.d) * kActBlock + (int)(threadIdx.x & 15) * 8;
-    left = in ? g.cols - col : 0;
+    c = Cols<WIDE>(col, g.cols);
   }
-  __device__ __forceinline__ int64_t at(int64_t ld) const { return row * ld + col; }
+  __device__ __forceinline__ int left() const { return in ? c.left : 0; }   // columns to store
 };
 
 __device__ __forceinline__ uint32_t unit_of(int k, int per) {
   return (blockIdx.x * per + k) * (uint32_t)kTeams + threadIdx.x / 16;
 }
 
-template <int TYPE, int K>
+template <int TYPE, bool WIDE, int K>
 __global__ __launch_bounds__(kThreads) void k_encode_act(ActGrid g, const void* x, int64_t ld, uint8_t* code, float* scale) {
   Raw8<TYPE> raw[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const Place p(g, unit_of(k, K));
-    raw[k] = load8<TYPE>(x, p.at(ld), p.left, g.cols >= 8);
+    const Place<WIDE> p(g, unit_of(k, K));
+    raw[k] = load8<TYPE>(row_of<TYPE>(x, p.row, ld), p.c);
   }
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const uint32_t u = unit_of(k, K);
-    const Place p(g, u);
+    const Place<WIDE> p(g, u);
     float v[8], s;
-    widen8<TYPE>(raw[k], p.left, v);
+    widen8<TYPE>(raw[k], p.c.left, v);
     const u32x2_any c = encode_block(v, s);
-    store_codes8(code, p.at(g.cols), p.left, c);
+    store_codes8(code + p.row * g.cols, p.col, p.left(), c);
     if (p.in && (threadIdx.x & 15) == 0) scale[u] = s;
   }
 }
 
-template <int TYPE, int K>
+template <int TYPE, bool WIDE, int K>
 __global__ __launch_bounds__(kThreads) void k_decode_act(ActGrid g, const uint8_t* code, const float* scale, void* x,
                                                          int64_t ld) {
   u32x2_any c[K];
@@ -60,18 +64,18 @@ __global__ __launch_bounds__(kThreads) void k_decode_act(ActGrid g, const uint8_
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const uint32_t u = unit_of(k, K);
-    const Place p(g, u);
-    c[k] = load_codes8(code, p.at(g.cols), p.left, g.cols >= 8);
-    s[k] = p.in ? scale[u] : 0.0f;
+    const Place<WIDE> p(g, u);
+    c[k] = load_codes8(code + p.row * g.cols, p.c);
+    s[k] = scale[p.in ? u : g.units - 1];
   }
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const Place p(g, unit_of(k, K));
+    const Place<WIDE> p(g, unit_of(k, K));
     float v[8];
-    codes_to_f32(c[k], p.left, v);
+    codes_to_f32(c[k], p.c.left, v);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] *= s[k];
-    store8<TYPE>(x, p.at(ld), p.left, v);
+    store8<TYPE>(row_of<TYPE>(x, p.row, ld), p.col, p.left(), v);
   }
 }
 
@@ -96,44 +100,44 @@ __device__ __forceinline__ void activation(float a, float& f, float& slope) {
   slope = __builtin_fmaf(f * (1.0f - q), du, q);
 }
 
-template <int TYPE, int ACT, bool GATED, bool SAVE, int K>
+template <int TYPE, int ACT, bool GATED, bool SAVE, bool WIDE, int K>
 __global__ __launch_bounds__(kThreads) void k_glu_forward(ActGrid g, GluArgs t) {
   Raw8<TYPE> ra[K], rb[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const Place p(g, unit_of(k, K));
-    ra[k] = load8<TYPE>(t.a, p.at(t.lda), p.left, g.cols >= 8);
-    if (GATED) rb[k] = load8<TYPE>(t.b, p.at(t.ldb), p.left, g.cols >= 8);
+    const Place<WIDE> p(g, unit_of(k, K));
+    ra[k] = load8<TYPE>(row_of<TYPE>(t.a, p.row, t.lda), p.c);
+    if (GATED) rb[k] = load8<TYPE>(row_of<TYPE>(t.b, p.row, t.ldb), p.c);
   }
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const uint32_t u = unit_of(k, K);
-    const Place p(g, u);
+    const Place<WIDE> p(g, u);
     float a[8], b[8], o[8], s;
-    widen8<TYPE>(ra[k], p.left, a);
-    if (GATED) widen8<TYPE>(rb[k], p.left, b);
+    widen8<TYPE>(ra[k], p.c.left, a);
+    if (GATED) widen8<TYPE>(rb[k], p.c.left, b);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       float slope;
       activation<ACT>(a[j], o[j], slope);
       if (GATED) o[j] *= b[j];
     }
-    store8<TYPE>(t.out, p.at(t.ldo), p.left, o);
+    store8<TYPE>(row_of<TYPE>(t.out, p.row, t.ldo), p.col, p.left(), o);
     if (SAVE) {
       const bool writes = p.in && (threadIdx.x & 15) == 0;
       const u32x2_any c = encode_block(a, s);
-      store_codes8(t.a_code, p.at(g.cols), p.left, c);
+      store_codes8(t.a_code + p.row * g.cols, p.col, p.left(), c);
       if (writes) t.a_scale[u] = s;
       if (GATED) {
         const u32x2_any d = encode_block(b, s);
-        store_codes8(t.b_code, p.at(g.cols), p.left, d);
+        store_codes8(t.b_code + p.row * g.cols, p.col, p.left(), d);
         if (writes) t.b_scale[u] = s;
       }
     }
   }
 }
 
-template <int TYPE, int ACT, bool GATED, int K>
+template <int TYPE, int ACT, bool GATED, bool WIDE, int K>
 __global__ __launch_bounds__(kThreads) void k_glu_backward(ActGrid g, GluArgs t) {
   Raw8<TYPE> rd[K];
   u32x2_any ca[K], cb[K];
@@ -141,22 +145,23 @@ __global__ __launch_bounds__(kThreads) void k_glu_backward(ActGrid g, GluArgs t)
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const uint32_t u = unit_of(k, K);
-    const Place p(g, u);
-    rd[k] = load8<TYPE>(t.dout, p.at(t.ldd), p.left, g.cols >= 8);
-    ca[k] = load_codes8(t.a_code, p.at(g.cols), p.left, g.cols >= 8);
-    sa[k] = p.in ? t.a_scale[u] : 0.0f;
+    const Place<WIDE> p(g, u);
+    rd[k] = load8<TYPE>(row_of<TYPE>(t.dout, p.row, t.ldd), p.c);
+    ca[k] = load_codes8(t.a_code + p.row * g.cols, p.c);
+    const uint32_t at = p.in ? u : g.units - 1;
+    sa[k] = t.a_scale[at];
     if (GATED) {
-      cb[k] = load_codes8(t.b_code, p.at(g.cols), p.left, g.cols >= 8);
-      sb[k] = p.in ? t.b_scale[u] : 0.0f;
+      cb[k] = load_codes8(t.b_code + p.row * g.cols, p.c);
+      sb[k] = t.b_scale[at];
     }
   }
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const Place p(g, unit_of(k, K));
+    const Place<WIDE> p(g, unit_of(k, K));
     float d[8], a[8], b[8], da[8], db[8], o[8];
-    widen8<TYPE>(rd[k], p.left, d);
-    codes_to_f32(ca[k], p.left, a);
-    if (GATED) codes_to_f32(cb[k], p.left, b);
+    widen8<TYPE>(rd[k], p.c.left, d);
+    codes_to_f32(ca[k], p.c.left, a);
+    if (GATED) codes_to_f32(cb[k], p.c.left, b);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       float f, slope;
@@ -171,45 +176,53 @@ __global__ __launch_bounds__(kThreads) void k_glu_backward(ActGrid g, GluArgs t)
         o[j] = f;
       }
     }
-    store8<TYPE>(t.da, p.at(t.lda), p.left, da);
-    if (GATED) store8<TYPE>(t.db, p.at(t.ldb), p.left, db);
-    if (t.out) store8<TYPE>(t.out, p.at(t.ldo), p.left, o);
+    store8<TYPE>(row_of<TYPE>(t.da, p.row, t.lda), p.col, p.left(), da);
+    if (GATED) store8<TYPE>(row_of<TYPE>(t.db, p.row, t.ldb), p.col, p.left(), db);
+    if (t.out) store8<TYPE>(row_of<TYPE>(t.out, p.row, t.ldo), p.col, p.left(), o);
   }
 }
 
 dim3 grid_of(const ActGrid& g, int k) { return dim3((g.units + kTeams * k - 1) / (kTeams * k)); }
 
-template <int TYPE, int ACT>
+// Blocks on a lane: two, so that four to six loads are under way at a time.
+constexpr int K = 2;
+
+template <int TYPE, int ACT, bool WIDE>
 ps_status glu_forward(const ActGrid& g, const GluArgs& p, hipStream_t s) {
-  constexpr int K = 2;
   const bool save = p.a_code != nullptr;
+  const dim3 grid = grid_of(g, K), wg(kThreads);
   if (p.b && save)
-    hipLaunchKernelGGL((k_glu_forward<TYPE, ACT, true, true, K>), grid_of(g, K), dim3(kThreads), 0, s, g, p);
+    hipLaunchKernelGGL((k_glu_forward<TYPE, ACT, true, true, WIDE, K>), grid, wg, 0, s, g, p);
   else if (p.b)
-    hipLaunchKernelGGL((k_glu_forward<TYPE, ACT, true, false, K>), grid_of(g, K), dim3(kThreads), 0, s, g, p);
+    hipLaunchKernelGGL((k_glu_forward<TYPE, ACT, true, false, WIDE, K>), grid, wg, 0, s, g, p);
   else if (save)
-    hipLaunchKernelGGL((k_glu_forward<TYPE, ACT, false, true, K>), grid_of(g, K), dim3(kThreads), 0, s, g, p);
+    hipLaunchKernelGGL((k_glu_forward<TYPE, ACT, false, true, WIDE, K>), grid, wg, 0, s, g, p);
   else
-    hipLaunchKernelGGL((k_glu_forward<TYPE, ACT, false, false, K>), grid_of(g, K), dim3(kThreads), 0, s, g, p);
+    hipLaunchKernelGGL((k_glu_forward<TYPE, ACT, false, false, WIDE, K>), grid, wg, 0, s, g, p);
   return hip_check(hipGetLastError(), "k_glu_forward launch");
 }
 
-template <int TYPE, int ACT>
+template <int TYPE, int ACT, bool WIDE>
 ps_status glu_backward(const ActGrid& g, const GluArgs& p, hipStream_t s) {
-  constexpr int K = 2;
   if (p.b_code)
-    hipLaunchKernelGGL((k_glu_backward<TYPE, ACT, true, K>), grid_of(g, K), dim3(kThreads), 0, s, g, p);
+    hipLaunchKernelGGL((k_glu_backward<TYPE, ACT, true, WIDE, K>), grid_of(g, K), dim3(kThreads), 0, s, g, p);
   else
-    hipLaunchKernelGGL((k_glu_backward<TYPE, ACT, false, K>), grid_of(g, K), dim3(kThreads), 0, s, g, p);
+    hipLaunchKernelGGL((k_glu_backward<TYPE, ACT, false, WIDE, K>), grid_of(g, K), dim3(kThreads), 0, s, g, p);
   return hip_check(hipGetLastError(), "k_glu_backward launch");
+}
+
+template <int TYPE, int ACT>
+ps_status glu(bool forward, const ActGrid& g, const GluArgs& p, hipStream_t s) {
+  if (g.cols < 8) return forward ? glu_forward<TYPE, ACT, false>(g, p, s) : glu_backward<TYPE, ACT, false>(g, p, s);
+  return forward ? glu_forward<TYPE, ACT, true>(g, p, s) : glu_backward<TYPE, ACT, true>(g, p, s);
 }
 
 template <int TYPE>
 ps_status glu(bool forward, const ActGrid& g, int act, const GluArgs& p, hipStream_t s) {
   switch (act) {
-    case PS_ACT_SILU: return forward ? glu_forward<TYPE, PS_ACT_SILU>(g, p, s) : glu_backward<TYPE, PS_ACT_SILU>(g, p, s);
-    case PS_ACT_GELU: return forward ? glu_forward<TYPE, PS_ACT_GELU>(g, p, s) : glu_backward<TYPE, PS_ACT_GELU>(g, p, s);
-    default: return forward ? glu_forward<TYPE, PS_ACT_GELU_TANH>(g, p, s) : glu_backward<TYPE, PS_ACT_GELU_TANH>(g, p, s);
+    case PS_ACT_SILU: return glu<TYPE, PS_ACT_SILU>(forward, g, p, s);
+    case PS_ACT_GELU: return glu<TYPE, PS_ACT_GELU>(forward, g, p, s);
+    default: return glu<TYPE, PS_ACT_GELU_TANH>(forward, g, p, s);
   }
 }
 
@@ -221,32 +234,42 @@ ps_status glu(bool forward, const ActGrid& g, int type, int act, const GluArgs& 
   }
 }
 
+template <int TYPE>
+ps_status encode(const ActGrid& g, const void* x, int64_t ld, uint8_t* code, float* scale, hipStream_t s) {
+  if (g.cols < 8)
+    hipLaunchKernelGGL((k_encode_act<TYPE, false, K>), grid_of(g, K), dim3(kThreads), 0, s, g, x, ld, code, scale);
+  else
+    hipLaunchKernelGGL((k_encode_act<TYPE, true, K>), grid_of(g, K), dim3(kThreads), 0, s, g, x, ld, code, scale);
+  return hip_check(hipGetLastError(), "k_encode_act launch");
+}
+
+template <int TYPE>
+ps_status decode(const ActGrid& g, const uint8_t* code, const float* scale, void* x, int64_t ld, hipStream_t s) {
+  if (g.cols < 8)
+    hipLaunchKernelGGL((k_decode_act<TYPE, false, K>), grid_of(g, K), dim3(kThreads), 0, s, g, code, scale, x, ld);
+  else
+    hipLaunchKernelGGL((k_decode_act<TYPE, true, K>), grid_of(g, K), dim3(kThreads), 0, s, g, code, scale, x, ld);
+  return hip_check(hipGetLastError(), "k_decode_act launch");
+}
+
 }  // namespace
 
 ps_status launch_encode_act(const ActGrid& g, int type, const void* x, int64_t ld, uint8_t* code, float* scale,
                             hipStream_t s) {
-  constexpr int K = 2;
-  const dim3 grid = grid_of(g, K), wg(kThreads);
-  if (type == PS_TYPE_F32)
-    hipLaunchKernelGGL((k_encode_act<PS_TYPE_F32, K>), grid, wg, 0, s, g, x, ld, code, scale);
-  else if (type == PS_TYPE_BF16)
-    hipLaunchKernelGGL((k_encode_act<PS_TYPE_BF16, K>), grid, wg, 0, s, g, x, ld, code, scale);
-  else
-    hipLaunchKernelGGL((k_encode_act<PS_TYPE_F16, K>), grid, wg, 0, s, g, x, ld, code, scale);
-  return hip_check(hipGetLastError(), "k_encode_act launch");
+  switch (type) {
+    case PS_TYPE_F32: return encode<PS_TYPE_F32>(g, x, ld, code, scale, s);
+    case PS_TYPE_BF16: return encode<PS_TYPE_BF16>(g, x, ld, code, scale, s);
+    default: return encode<PS_TYPE_F16>(g, x, ld, code, scale, s);
+  }
 }
 
 ps_status launch_decode_act(const ActGrid& g, int type, const uint8_t* code, const float* scale, void* x, int64_t ld,
                             hipStream_t s) {
-  constexpr int K = 2;
-  const dim3 grid = grid_of(g, K), wg(kThreads);
-  if (type == PS_TYPE_F32)
-    hipLaunchKernelGGL((k_decode_act<PS_TYPE_F32, K>), grid, wg, 0, s, g, code, scale, x, ld);
-  else if (type == PS_TYPE_BF16)
-    hipLaunchKernelGGL((k_decode_act<PS_TYPE_BF16, K>), grid, wg, 0, s, g, code, scale, x, ld);
-  else
-    hipLaunchKernelGGL((k_decode_act<PS_TYPE_F16, K>), grid, wg, 0, s, g, code, scale, x, ld);
-  return hip_check(hipGetLastError(), "k_decode_act launch");
+  switch (type) {
+    case PS_TYPE_F32: return decode<PS_TYPE_F32>(g, code, scale, x, ld, s);
+    case PS_TYPE_BF16: return decode<PS_TYPE_BF16>(g, code, scale, x, ld, s);
+    default: return decode<PS_TYPE_F16>(g, code, scale, x, ld, s);
+  }
 }
 
 ps_status launch_glu_forward(const ActGrid& g, int type, int act, const GluArgs& p, hipStream_t s) {

@@ -15,11 +15,11 @@ namespace {
 // workgroup's waves through shared memory. `turn` alternates between two places,
 // so that one barrier a sum is enough.
 constexpr int kMostWaves = 16;
-template <int N>
 struct TeamSum {
-  float (*lds)[kMostWaves][N];
+  float (*lds)[kMostWaves][2];
   int waves;
   int turn = 0;
+  template <int N>
   __device__ __forceinline__ void operator()(float* v) {
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
@@ -68,7 +68,7 @@ __device__ __forceinline__ float normalise(const NormArgs& p, int kind, float ep
     for (int v = 0; v < V; ++v)
 #pragma unroll
       for (int j = 0; j < 8; ++j) s[0] += z[v][j];
-    sum(s);
+    sum.template operator()<1>(s);
     const float mean = s[0] * p.inv_cols;
 #pragma unroll
     for (int v = 0; v < V; ++v)
@@ -80,7 +80,7 @@ __device__ __forceinline__ float normalise(const NormArgs& p, int kind, float ep
   for (int v = 0; v < V; ++v)
 #pragma unroll
     for (int j = 0; j < 8; ++j) s[0] = __builtin_fmaf(z[v][j], z[v][j], s[0]);
-  sum(s);
+  sum.template operator()<1>(s);
   const float r = 1.0f / __builtin_sqrtf(__builtin_fmaf(s[0], p.inv_cols, eps));
 #pragma unroll
   for (int v = 0; v < V; ++v)
@@ -99,11 +99,11 @@ __device__ __forceinline__ u32x2_any pack_codes(const float* z) {
 // A row by one team: the waves of a workgroup (V times eight columns on each
 // lane, as few lanes as hold the row), or, up to 1024 columns, a wave with three
 // others beside it.
-template <int TYPE, int V, bool WAVE>
+template <int TYPE, int V, bool WAVE, bool WIDE>
 __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_forward(NormArgs p) {
-  __shared__ float lds[2][kMostWaves][1];
+  __shared__ float lds[2][kMostWaves][2];
   const int nt = WAVE ? 64 : blockDim.x, lane = WAVE ? threadIdx.x & 63 : threadIdx.x;
-  TeamSum<1> sum{lds, nt / 64};
+  TeamSum sum{lds, nt / 64};
   const int row = WAVE ? __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + threadIdx.x / 64) : blockIdx.x;
   if (row >= p.rows) return;   // whole teams leave
   int seg = 0;
@@ -111,14 +111,13 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_forward(NormArgs p) 
     seg = find_seg(p.seg_start, p.n_segs, row);
     if (seg < 0) return;
   }
-  const bool wide = p.cols >= 8;
   float z[V][8];
   Raw8<TYPE> rx[V], ry[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int col = (v * nt + lane) * 8;
-    if (p.y) ry[v] = load8<TYPE>(p.y, (int64_t)row * p.ldy + col, p.cols - col, wide);
-    rx[v] = load8<TYPE>(p.x, (int64_t)row * p.ldx + col, p.cols - col, wide);
+    const Cols<WIDE> c((v * nt + lane) * 8, p.cols);
+    if (p.y) ry[v] = load8<TYPE>(row_of<TYPE>(p.y, row, p.ldy), c);
+    rx[v] = load8<TYPE>(row_of<TYPE>(p.x, row, p.ldx), c);
   }
   if (p.y) {
 #pragma unroll
@@ -129,7 +128,9 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_forward(NormArgs p) 
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int col = (v * nt + lane) * 8, left = p.cols - col;
+      const int col = (v * nt + lane) * 8;
+      const Cols<WIDE> c8(col, p.cols);
+      const int left = c8.left;
       if (p.y_code) {
         u32x2_any c;
         if (p.post != PS_NORM_NONE) {
@@ -140,23 +141,23 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_forward(NormArgs p) 
           if ((lane & 15) == 0 && left > 0)
             p.y_scale[(int64_t)row * ((p.cols + kActBlock - 1) / kActBlock) + col / kActBlock] = s;
         }
-        store_codes8(p.y_code, (int64_t)row * p.cols + col, left, c);
+        store_codes8(p.y_code + (int64_t)row * p.cols, col, left, c);
       }
       float m[8], x[8];
       if (p.w1) {
-        load_vec8(p.w1, p.vec_type, col, left, wide, m);
+        load_vec8(p.w1, p.vec_type, 0, c8, m);
 #pragma unroll
         for (int j = 0; j < 8; ++j) z[v][j] *= m[j];
       }
       if (p.gate) {
-        load_vec8(p.gate, p.vec_type, seg_offset(p, PS_NORM_GATE_BY_SEG, seg) + col, left, wide, m);
+        load_vec8(p.gate, p.vec_type, seg_offset(p, PS_NORM_GATE_BY_SEG, seg), c8, m);
 #pragma unroll
         for (int j = 0; j < 8; ++j) z[v][j] *= m[j];
       }
       widen8<TYPE>(rx[v], left, x);
 #pragma unroll
       for (int j = 0; j < 8; ++j) z[v][j] = __builtin_fmaf(p.beta, z[v][j], p.alpha * x[j]);
-      store8<TYPE>(p.h, (int64_t)row * p.ldh + col, left, z[v]);
+      store8<TYPE>(row_of<TYPE>(p.h, row, p.ldh), col, left, z[v]);
     }
   } else {
 #pragma unroll
@@ -166,202 +167,217 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_forward(NormArgs p) 
   if (p.h_rstd && lane == 0) p.h_rstd[row] = r;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int col = (v * nt + lane) * 8, left = p.cols - col;
-    if (p.h_code) store_codes8(p.h_code, (int64_t)row * p.cols + col, left, pack_codes(z[v]));
+    const int col = (v * nt + lane) * 8;
+    const Cols<WIDE> c8(col, p.cols);
+    const int left = c8.left;
+    if (p.h_code) store_codes8(p.h_code + (int64_t)row * p.cols, col, left, pack_codes(z[v]));
     float m[8], a[8];
-    const int64_t o = seg_offset(p, PS_NORM_MOD_BY_SEG, seg) + col;
+    const int64_t o = seg_offset(p, PS_NORM_MOD_BY_SEG, seg);
     if (p.mul) {
-      load_vec8(p.mul, p.vec_type, o, left, wide, m);
+      load_vec8(p.mul, p.vec_type, o, c8, m);
       const float one = p.flags & PS_NORM_MUL_PLUS_ONE ? 1.0f : 0.0f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) z[v][j] *= one + m[j];
     }
     if (p.add) {
-      load_vec8(p.add, p.vec_type, o, left, wide, a);
+      load_vec8(p.add, p.vec_type, o, c8, a);
 #pragma unroll
       for (int j = 0; j < 8; ++j) z[v][j] += a[j];
     }
-    store8<TYPE>(p.n, (int64_t)row * p.ldn + col, left, z[v]);
+    store8<TYPE>(row_of<TYPE>(p.n, row, p.ldn), col, left, z[v]);
   }
 }
 
-// g becomes back(g, z, r): r (g - [mean g] - z mean(g z)).
+// The sums that back(g, z, r) = r (g - [mean g] - z mean(g z)) needs, as the
+// factors of its form fma(r, g, fma(-c, z, -d)): c = r mean(g z), d = r mean g.
 template <int V, class Sum>
-__device__ __forceinline__ void back(const NormArgs& p, int kind, float r, Sum& sum, float (*g)[8], const float (*z)[8]) {
+__device__ __forceinline__ void back_sums(const NormArgs& p, int kind, float r, Sum& sum, const float (*g)[8],
+                                          const float (*z)[8], float& c, float& d) {
   float s[2] = {0, 0};
 #pragma unroll
   for (int v = 0; v < V; ++v)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      s[0] = __builtin_fmaf(g[v][j], z[v][j], s[0]);
-      s[1] += g[v][j];
-    }
-  sum(s);
-  const float gz = s[0] * p.inv_cols, m = kind == PS_NORM_LAYER ? s[1] * p.inv_cols : 0.0f;
+    for (int j = 0; j < 8; ++j) s[0] = __builtin_fmaf(g[v][j], z[v][j], s[0]);
+  d = 0.0f;
+  if (kind == PS_NORM_LAYER) {
 #pragma unroll
-  for (int v = 0; v < V; ++v)
+    for (int v = 0; v < V; ++v)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) g[v][j] = r * (__builtin_fmaf(-gz, z[v][j], g[v][j]) - m);
+      for (int j = 0; j < 8; ++j) s[1] += g[v][j];
+    sum.template operator()<2>(s);
+    d = r * (s[1] * p.inv_cols);
+  } else {
+    sum.template operator()<1>(s);
+  }
+  c = r * (s[0] * p.inv_cols);
 }
 
-// A row's inputs of the backward pass as they lie in memory.
-template <int TYPE, int V>
-struct RowIn {
-  Raw8<TYPE> dn[V], dh[V];
-  u32x2_any ch[V], cy[V];
-  float s[V], h_rstd, y_rstd;
-};
+// What the backward pass finds of the branch: nothing saved, its values (a gate
+// without a norm), or its normalised ones.
+enum { kNoBranch = 0, kPlain = 1, kNormed = 2 };
 
-// A workgroup takes a strip of rows and keeps the column sums of its gradients
-// in registers; where the segment changes, and at the end, they go to the
-// strip's part of that segment. The next row is loaded before the sums of this
-// one, whose barriers its latency would otherwise add to; a segment's vectors
+// A workgroup takes a strip of rows, one segment's after the other's, and keeps
+// the column sums of its gradients in registers until a segment's rows end; then
+// they go to the strip's part of that segment. Each half of the next row is
+// loaded into the registers of this one's as soon as it is used, before the sums
+// whose barriers the load's latency would otherwise add to; a segment's vectors
 // stay in registers, since a load behind those of the next row would wait for
 // them. The widest rows (V > 1) leave no registers for either.
-template <int TYPE, int V>
+template <int TYPE, int V, int SAVED, bool WIDE>
 __global__ __launch_bounds__(V == 1 ? 1024 : 512) void k_norm_backward(NormArgs p) {
   constexpr bool kAhead = V == 1;
   __shared__ float lds[2][kMostWaves][2];
   const int nt = blockDim.x, lane = threadIdx.x;
-  TeamSum<2> sum{lds, nt / 64};
+  TeamSum sum{lds, nt / 64};
   const int first = blockIdx.x * p.strip, last = min(p.rows - first, p.strip) + first;
   const int64_t n_part = (int64_t)p.slots * p.cols;
-  const bool branch = p.dy != nullptr, post = p.post != PS_NORM_NONE;
-  const bool wide = p.cols >= 8;
-  const bool has_yh = branch && (post || p.gate);
-  float acc[3][V][8];
-  float km[V][8], ky[V][8];        // m, and branch_scale * gate * post_weight (0 for columns that do not exist)
-  int seg = -1, seg_end = first;   // the segment of the sums and vectors, and where it ends
+  const int blocks = (p.cols + kActBlock - 1) / kActBlock;
+  const bool branch = p.dy != nullptr;
 
-  auto flush = [&]() __attribute__((always_inline)) {
-    if (seg < 0) return;
-    const int64_t o = (int64_t)(blockIdx.x + seg) * p.cols;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int col = (v * nt + lane) * 8, left = p.cols - col;
-      if (p.d_add) store8<PS_TYPE_F32, false>(p.part, o + col, left, acc[0][v]);
-      if (p.d_mul) store8<PS_TYPE_F32, false>(p.part + n_part, o + col, left, acc[1][v]);
-      if (p.d_gate || p.d_w1) store8<PS_TYPE_F32, false>(p.part + 2 * n_part, o + col, left, acc[2][v]);
-    }
-  };
-  auto vectors = [&]() __attribute__((always_inline)) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int col = (v * nt + lane) * 8, left = p.cols - col;
-      const float one = p.flags & PS_NORM_MUL_PLUS_ONE ? 1.0f : 0.0f;
-      float m[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) km[v][j] = 1.0f, ky[v][j] = j < left ? p.beta : 0.0f;
-      if (p.mul) {
-        load_vec8(p.mul, p.vec_type, seg_offset(p, PS_NORM_MOD_BY_SEG, seg) + col, left, wide, m);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) km[v][j] = one + m[j];
+  for (int row = first; row < last;) {
+    int seg = 0, end = last;
+    if (p.seg_start) {
+      seg = find_seg(p.seg_start, p.n_segs, row);
+      if (seg < 0) {
+        ++row;
+        continue;
       }
+      end = min(max(p.seg_start[seg + 1], row + 1), last);
+    }
+    // m, and branch_scale * gate * post_weight (0 for columns that do not exist)
+    float km[V][8], ky[V][8], acc[3][V][8];
+    auto vectors = [&]() __attribute__((always_inline)) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const Cols<WIDE> c((v * nt + lane) * 8, p.cols);
+        const float one = p.flags & PS_NORM_MUL_PLUS_ONE ? 1.0f : 0.0f;
+        float m[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) km[v][j] = 1.0f, ky[v][j] = j < c.left ? p.beta : 0.0f;
+        if (p.mul) {
+          load_vec8(p.mul, p.vec_type, seg_offset(p, PS_NORM_MOD_BY_SEG, seg), c, m);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) km[v][j] = one + m[j];
+        }
+        if (p.gate) {
+          load_vec8(p.gate, p.vec_type, seg_offset(p, PS_NORM_GATE_BY_SEG, seg), c, m);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) ky[v][j] *= m[j];
+        }
+        if (p.w1) {
+          load_vec8(p.w1, p.vec_type, 0, c, m);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) ky[v][j] *= m[j];
+        }
+      }
+    };
+    Raw8<TYPE> dn[V], dh[V];
+    u32x2_any ch[V], cy[V];
+    float ys[V], h_rstd, y_rstd;
+    auto load_first = [&](int r) __attribute__((always_inline)) {
+      h_rstd = p.h_rstd[r];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const Cols<WIDE> c((v * nt + lane) * 8, p.cols);
+        dn[v] = load8<TYPE>(row_of<TYPE>(p.dn, r, p.lddn), c);
+        ch[v] = load_codes8(p.h_code + (int64_t)r * p.cols, c);
+      }
+    };
+    auto load_second = [&](int r) __attribute__((always_inline)) {
+      if (SAVED == kNormed) y_rstd = p.y_rstd[r];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const Cols<WIDE> c((v * nt + lane) * 8, p.cols);
+        dh[v] = Raw8<TYPE>{};
+        if (p.dh) dh[v] = load8<TYPE>(row_of<TYPE>(p.dh, r, p.lddh), c);
+        if (SAVED != kNoBranch) cy[v] = load_codes8(p.y_code + (int64_t)r * p.cols, c);
+        if (SAVED == kPlain) ys[v] = p.y_scale[(int64_t)r * blocks + min((v * nt + lane) * 8, p.cols - 1) / kActBlock];
+      }
+    };
+    if (kAhead) {
+      vectors();
+      load_first(row);
+      load_second(row);
+    }
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[i][v][j] = 0;
+
+    for (; row < end; ++row) {
+      if (!kAhead) {
+        vectors();
+        load_first(row);
+        load_second(row);
+      }
+      const int ahead = min(row + 1, end - 1);   // the last row is loaded twice
+      float g[V][8], z[V][8], c, d;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int left = p.cols - (v * nt + lane) * 8;
+        widen8<TYPE>(dn[v], left, g[v]);
+        codes_to_f32(ch[v], left, z[v]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          acc[0][v][j] += g[v][j];
+          acc[1][v][j] = __builtin_fmaf(g[v][j], z[v][j], acc[1][v][j]);
+          g[v][j] *= km[v][j];
+        }
+      }
+      const float r1 = h_rstd;
+      if (kAhead) load_first(ahead);
+      back_sums<V>(p, p.pre, r1, sum, g, z, c, d);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int col = (v * nt + lane) * 8, left = p.cols - col;
+        float o[8];
+        widen8<TYPE>(dh[v], left, o);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          g[v][j] = __builtin_fmaf(-c, z[v][j], __builtin_fmaf(r1, g[v][j], o[j] - d));
+          o[j] = p.alpha * g[v][j];
+        }
+        store8<TYPE>(row_of<TYPE>(p.dx, row, p.lddx), col, left, o);
+        if (SAVED != kNoBranch) {
+          codes_to_f32(cy[v], left, z[v]);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if (SAVED == kPlain) z[v][j] *= ys[v];
+            acc[2][v][j] = __builtin_fmaf(g[v][j], z[v][j], acc[2][v][j]);
+          }
+        }
+      }
+      const float r2 = y_rstd;
+      if (kAhead) load_second(ahead);
       if (!branch) continue;
-      if (p.gate) {
-        load_vec8(p.gate, p.vec_type, seg_offset(p, PS_NORM_GATE_BY_SEG, seg) + col, left, wide, m);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ky[v][j] *= m[j];
-      }
-      if (p.w1) {
-        load_vec8(p.w1, p.vec_type, col, left, wide, m);
+      for (int v = 0; v < V; ++v)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ky[v][j] *= m[j];
-      }
-    }
-  };
-  RowIn<TYPE, V> next;
-  auto load = [&](int row) __attribute__((always_inline)) {
-    next.h_rstd = p.h_rstd[row];
-    if (branch && post) next.y_rstd = p.y_rstd[row];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int col = (v * nt + lane) * 8, left = p.cols - col;
-      next.dn[v] = load8<TYPE>(p.dn, (int64_t)row * p.lddn + col, left, wide);
-      next.ch[v] = load_codes8(p.h_code, (int64_t)row * p.cols + col, left, wide);
-      if (p.dh) next.dh[v] = load8<TYPE>(p.dh, (int64_t)row * p.lddh + col, left, wide);
-      if (has_yh) {
-        next.cy[v] = load_codes8(p.y_code, (int64_t)row * p.cols + col, left, wide);
-        if (!post)
-          next.s[v] = left > 0 ? p.y_scale[(int64_t)row * ((p.cols + kActBlock - 1) / kActBlock) + col / kActBlock] : 0.0f;
-      }
-    }
-  };
-
-  if (kAhead) load(first);
-  for (int row = first; row < last; ++row) {
-    if (!kAhead) load(row);
-    const RowIn<TYPE, V> in = next;
-    if (kAhead && row + 1 < last) load(row + 1);
-    if (row >= seg_end) {   // the first row, or the first of another segment
-      flush();
-      seg = 0;
-      seg_end = last;
-      if (p.seg_start) {
-        seg = find_seg(p.seg_start, p.n_segs, row);
-        // the next row to look again at: the segment's end, or the next one where there is none
-        seg_end = seg < 0 ? row + 1 : min(max(p.seg_start[seg + 1], row + 1), last);
-      }
-#pragma unroll
-      for (int i = 0; i < 3; ++i)
+        for (int j = 0; j < 8; ++j) g[v][j] *= ky[v][j];
+      if (SAVED == kNormed) {
+        back_sums<V>(p, p.post, r2, sum, g, z, c, d);
 #pragma unroll
         for (int v = 0; v < V; ++v)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) acc[i][v][j] = 0;
-      if (kAhead && seg >= 0) vectors();
-    }
-    if (seg < 0) continue;
-    if (!kAhead) vectors();
-    float g[V][8], z[V][8];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int left = p.cols - (v * nt + lane) * 8;
-      widen8<TYPE>(in.dn[v], left, g[v]);
-      codes_to_f32(in.ch[v], left, z[v]);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        acc[0][v][j] += g[v][j];
-        acc[1][v][j] = __builtin_fmaf(g[v][j], z[v][j], acc[1][v][j]);
+          for (int j = 0; j < 8; ++j) g[v][j] = __builtin_fmaf(-c, z[v][j], __builtin_fmaf(r2, g[v][j], -d));
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) g[v][j] *= km[v][j];
+      for (int v = 0; v < V; ++v) {
+        const int col = (v * nt + lane) * 8;
+        store8<TYPE>(row_of<TYPE>(p.dy, row, p.lddy), col, p.cols - col, g[v]);
+      }
     }
-    back<V>(p, p.pre, in.h_rstd, sum, g, z);
+    float* part = p.part + (int64_t)(blockIdx.x + seg) * p.cols;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int col = (v * nt + lane) * 8, left = p.cols - col;
-      if (p.dh) {
-        float d[8];
-        widen8<TYPE>(in.dh[v], left, d);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) g[v][j] += d[j];
-      }
-      float o[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = p.alpha * g[v][j];
-      store8<TYPE>(p.dx, (int64_t)row * p.lddx + col, left, o);
-      if (!branch) continue;
-      if (has_yh) {
-        codes_to_f32(in.cy[v], left, z[v]);
-        if (!post) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) z[v][j] *= in.s[v];
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[2][v][j] = __builtin_fmaf(g[v][j], z[v][j], acc[2][v][j]);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) g[v][j] *= ky[v][j];
-    }
-    if (!branch) continue;
-    if (post) back<V>(p, p.post, in.y_rstd, sum, g, z);
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int col = (v * nt + lane) * 8;
-      store8<TYPE>(p.dy, (int64_t)row * p.lddy + col, p.cols - col, g[v]);
+      if (p.d_add) store8<PS_TYPE_F32, false>(part, col, left, acc[0][v]);
+      if (p.d_mul) store8<PS_TYPE_F32, false>(part + n_part, col, left, acc[1][v]);
+      if (p.d_gate || p.d_w1) store8<PS_TYPE_F32, false>(part + 2 * n_part, col, left, acc[2][v]);
     }
   }
-  flush();
 }
 
 // The strips' parts, added up. A workgroup joins 32 columns of one gradient (and
@@ -427,29 +443,37 @@ int waves_for(int lanes, int v) { return (lanes + 64 * v - 1) / (64 * v); }
 template <int TYPE>
 ps_status forward(const NormArgs& p, hipStream_t s) {
   const int lanes = (p.cols + 7) / 8;
-  if (lanes <= 128) {
-    const dim3 grid((p.rows + 3) / 4);
-    if (lanes <= 64)
-      hipLaunchKernelGGL((k_norm_forward<TYPE, 1, true>), grid, dim3(256), 0, s, p);
-    else
-      hipLaunchKernelGGL((k_norm_forward<TYPE, 2, true>), grid, dim3(256), 0, s, p);
-  } else {
-    hipLaunchKernelGGL((k_norm_forward<TYPE, 2, false>), dim3(p.rows), dim3(waves_for(lanes, 2) * 64), 0, s, p);
-  }
+  const dim3 four((p.rows + 3) / 4);
+  if (p.cols < 8)
+    hipLaunchKernelGGL((k_norm_forward<TYPE, 1, true, false>), four, dim3(256), 0, s, p);
+  else if (lanes <= 64)
+    hipLaunchKernelGGL((k_norm_forward<TYPE, 1, true, true>), four, dim3(256), 0, s, p);
+  else if (lanes <= 128)
+    hipLaunchKernelGGL((k_norm_forward<TYPE, 2, true, true>), four, dim3(256), 0, s, p);
+  else
+    hipLaunchKernelGGL((k_norm_forward<TYPE, 2, false, true>), dim3(p.rows), dim3(waves_for(lanes, 2) * 64), 0, s, p);
   return hip_check(hipGetLastError(), "k_norm_forward launch");
+}
+
+template <int TYPE, int SAVED>
+ps_status backward(const NormArgs& p, hipStream_t s) {
+  const int lanes = (p.cols + 7) / 8;
+  const dim3 grid((p.rows + p.strip - 1) / p.strip);
+  if (p.cols < 8)
+    hipLaunchKernelGGL((k_norm_backward<TYPE, 1, SAVED, false>), grid, dim3(64), 0, s, p);
+  else if (lanes <= 1024)
+    hipLaunchKernelGGL((k_norm_backward<TYPE, 1, SAVED, true>), grid, dim3(waves_for(lanes, 1) * 64), 0, s, p);
+  else if (lanes <= 1536)
+    hipLaunchKernelGGL((k_norm_backward<TYPE, 3, SAVED, true>), grid, dim3(waves_for(lanes, 3) * 64), 0, s, p);
+  else
+    hipLaunchKernelGGL((k_norm_backward<TYPE, 4, SAVED, true>), grid, dim3(waves_for(lanes, 4) * 64), 0, s, p);
+  return hip_check(hipGetLastError(), "k_norm_backward launch");
 }
 
 template <int TYPE>
 ps_status backward(const NormArgs& p, hipStream_t s) {
-  const int lanes = (p.cols + 7) / 8;
-  const dim3 grid((p.rows + p.strip - 1) / p.strip);
-  if (lanes <= 1024)
-    hipLaunchKernelGGL((k_norm_backward<TYPE, 1>), grid, dim3(waves_for(lanes, 1) * 64), 0, s, p);
-  else if (lanes <= 1536)
-    hipLaunchKernelGGL((k_norm_backward<TYPE, 3>), grid, dim3(waves_for(lanes, 3) * 64), 0, s, p);
-  else
-    hipLaunchKernelGGL((k_norm_backward<TYPE, 4>), grid, dim3(waves_for(lanes, 4) * 64), 0, s, p);
-  return hip_check(hipGetLastError(), "k_norm_backward launch");
+  if (!p.dy || (p.post == PS_NORM_NONE && !p.gate)) return backward<TYPE, kNoBranch>(p, s);
+  return p.post == PS_NORM_NONE ? backward<TYPE, kPlain>(p, s) : backward<TYPE, kNormed>(p, s);
 }
 
 }  // namespace
