@@ -44,22 +44,25 @@ __device__ __forceinline__ u32x4 shift_down(u32x4 w, int n) {
 }
 
 // Eight columns of a row, those from `col` on, of which `left` exist (none if
-// left <= 0). Where fewer than eight do, loads take the row's last eight and
-// widen8 moves them into place, so that every lane loads alike: no branch around
-// a load, and no lane whose row ends costs more. Rows of fewer than eight (WIDE
-// false) are loaded one by one.
-template <bool WIDE>
+// left <= 0). END says how rows end: at a multiple of eight (kWhole); anywhere
+// (kPart), where a lane with fewer than eight loads the row's last eight, which
+// widen8 moves into place, so that every lane loads alike: no branch around a
+// load, and no lane whose row ends costs more; or before eight (kShort), loaded
+// one by one.
+enum { kWhole = 0, kPart = 1, kShort = 2 };
+inline int end_of(int cols) { return cols < 8 ? kShort : cols % 8 ? kPart : kWhole; }
+template <int END>
 struct Cols {
   int left, start;
   __device__ __forceinline__ Cols(int col, int cols)
-      : left(cols - col), start(WIDE ? __builtin_elementwise_min(col, cols - 8) : col) {}
+      : left(cols - col), start(END == kShort ? col : __builtin_elementwise_min(col, cols - 8)) {}
 };
 
-template <int TYPE, bool STREAM = true, bool WIDE>
-__device__ __forceinline__ Raw8<TYPE> load8(const void* row, const Cols<WIDE>& c) {
+template <int TYPE, bool STREAM = true, int END>
+__device__ __forceinline__ Raw8<TYPE> load8(const GLOBAL char* row, const Cols<END>& c) {
   Raw8<TYPE> r = {};
-  if (WIDE) {
-    const GLOBAL u32x4_any* p = (const GLOBAL u32x4_any*)((const char*)row + (uint32_t)(c.start * kBytes<TYPE>));
+  if (END != kShort) {
+    const GLOBAL u32x4_any* p = (const GLOBAL u32x4_any*)(row + (uint32_t)(c.start * kBytes<TYPE>));
 #pragma unroll
     for (int i = 0; i < (int)sizeof(r.w) / 16; ++i) r.w[i] = STREAM ? (u32x4)__builtin_nontemporal_load(p + i) : (u32x4)p[i];
     return r;
@@ -79,11 +82,11 @@ __device__ __forceinline__ Raw8<TYPE> load8(const void* row, const Cols<WIDE>& c
   return r;
 }
 
-template <int TYPE>
-__device__ __forceinline__ void widen8(Raw8<TYPE> r, int left, float* d) {
-  if (left < 8) {
-    const int k = 8 - left;
-    if (left <= 0) {
+template <int TYPE, int END>
+__device__ __forceinline__ void widen8(Raw8<TYPE> r, const Cols<END>& c, float* d) {
+  if (c.left < (END == kWhole ? 1 : 8)) {
+    const int k = 8 - c.left;
+    if (c.left <= 0) {
       r = Raw8<TYPE>{};
     } else if (TYPE == PS_TYPE_F32) {
       if (k & 4) {
@@ -123,8 +126,10 @@ __device__ __forceinline__ uint32_t round2(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
 }
 
-template <int TYPE, bool STREAM = true>
-__device__ __forceinline__ void store8(void* row, int col, int left, const float* s) {
+// Eight values to columns col .. of a row, those that exist; `c.left` may be made less.
+template <int TYPE, bool STREAM = true, int END>
+__device__ __forceinline__ void store8(GLOBAL char* row, int col, const Cols<END>& c, const float* s) {
+  const int left = c.left;
   if (left <= 0) return;
   Raw8<TYPE> r;
 #pragma unroll
@@ -134,8 +139,8 @@ __device__ __forceinline__ void store8(void* row, int col, int left, const float
     else if (j % 2 == 0)
       r.w[0][j / 2] = round2<TYPE>(s[j], s[j + 1]);
   }
-  char* at = (char*)row + (uint32_t)(col * kBytes<TYPE>);
-  if (left >= 8) {
+  GLOBAL char* at = row + (uint32_t)(col * kBytes<TYPE>);
+  if (END == kWhole || left >= 8) {
     GLOBAL u32x4_any* p = (GLOBAL u32x4_any*)at;
 #pragma unroll
     for (int i = 0; i < (int)sizeof(r.w) / 16; ++i) {
@@ -176,22 +181,24 @@ __device__ __forceinline__ void store8(void* row, int col, int left, const float
 }
 
 // Eight codes, as load8.
-template <bool WIDE>
-__device__ __forceinline__ u32x2_any load_codes8(const uint8_t* row, const Cols<WIDE>& c) {
-  if (WIDE) return __builtin_nontemporal_load((const GLOBAL u32x2_any*)(row + (uint32_t)c.start));
+template <int END>
+__device__ __forceinline__ u32x2_any load_codes8(const GLOBAL char* row, const Cols<END>& c) {
+  if (END != kShort) return __builtin_nontemporal_load((const GLOBAL u32x2_any*)(row + (uint32_t)c.start));
   uint64_t w = 0;
 #pragma unroll 1
   for (int j = 0; j < c.left; ++j) w = w >> 8 | (uint64_t)((const GLOBAL uint8_t*)row)[c.start + j] << 56;
   return u32x2_any{(uint32_t)w, (uint32_t)(w >> 32)};
 }
 
-__device__ __forceinline__ void store_codes8(uint8_t* row, int col, int left, u32x2_any c) {
-  if (left >= 8) {
+template <int END>
+__device__ __forceinline__ void store_codes8(GLOBAL char* row, int col, const Cols<END>& at8, u32x2_any c) {
+  const int left = at8.left;
+  if (left <= 0) return;
+  if (END == kWhole || left >= 8) {
     __builtin_nontemporal_store(c, (GLOBAL u32x2_any*)(row + (uint32_t)col));
     return;
   }
-  if (left <= 0) return;
-  GLOBAL uint8_t* at = (GLOBAL uint8_t*)row + (uint32_t)col;
+  GLOBAL char* at = row + (uint32_t)col;
   uint32_t w = c[0];
   if (left & 4) {
     *(GLOBAL u32_any*)at = w;
@@ -203,22 +210,27 @@ __device__ __forceinline__ void store_codes8(uint8_t* row, int col, int left, u3
     w >>= 16;
     at += 2;
   }
-  if (left & 1) *at = (uint8_t)w;
+  if (left & 1) *at = (char)w;
 }
 
-// Row r of a matrix whose rows are ld elements apart.
+// Row r of a matrix whose rows are ld elements, or bytes, apart. Global pointers
+// from here on: a uniform one with a lane's 32-bit offset is one access.
 template <int TYPE>
-__device__ __forceinline__ const char* row_of(const void* p, int64_t r, int64_t ld) {
-  return (const char*)p + r * ld * kBytes<TYPE>;
+__device__ __forceinline__ GLOBAL char* row_of(const void* p, int64_t r, int64_t ld) {
+  return (GLOBAL char*)p + r * ld * kBytes<TYPE>;
 }
-template <int TYPE>
-__device__ __forceinline__ char* row_of(void* p, int64_t r, int64_t ld) {
-  return (char*)p + r * ld * kBytes<TYPE>;
+// The same for a row that the whole workgroup or wave is at, held in scalar registers.
+__device__ __forceinline__ GLOBAL char* scalar_pointer(GLOBAL char* p) {
+  uint64_t u = (uint64_t)p;
+  asm("" : "+s"(u));   // no instruction: keeps the lane's offset out of it
+  return (GLOBAL char*)u;
 }
+__device__ __forceinline__ GLOBAL char* codes_of(const uint8_t* p, int64_t r, int64_t ld) { return (GLOBAL char*)p + r * ld; }
 
-__device__ __forceinline__ void codes_to_f32(u32x2_any c, int left, float* d) {
-  if (left < 8) {
-    const uint64_t w = left > 0 ? ((uint64_t)c[1] << 32 | c[0]) >> (8 * (8 - left)) : 0;
+template <int END>
+__device__ __forceinline__ void codes_to_f32(u32x2_any c, const Cols<END>& at, float* d) {
+  if (at.left < (END == kWhole ? 1 : 8)) {
+    const uint64_t w = at.left > 0 ? ((uint64_t)c[1] << 32 | c[0]) >> (8 * (8 - at.left)) : 0;
     c = u32x2_any{(uint32_t)w, (uint32_t)(w >> 32)};
   }
   e4m3_unpack4(c[0], d);
@@ -226,14 +238,14 @@ __device__ __forceinline__ void codes_to_f32(u32x2_any c, int left, float* d) {
 }
 
 // Eight values of a vector of any type (uniform), kept in the caches.
-template <bool WIDE>
-__device__ __forceinline__ void load_vec8(const void* v, int type, int64_t first, const Cols<WIDE>& c, float* d) {
+template <int END>
+__device__ __forceinline__ void load_vec8(const void* v, int type, int64_t first, const Cols<END>& c, float* d) {
   if (type == PS_TYPE_F32)
-    widen8<PS_TYPE_F32>(load8<PS_TYPE_F32, false>((const float*)v + first, c), c.left, d);
+    widen8<PS_TYPE_F32>(load8<PS_TYPE_F32, false>(row_of<PS_TYPE_F32>(v, first, 1), c), c, d);
   else if (type == PS_TYPE_BF16)
-    widen8<PS_TYPE_BF16>(load8<PS_TYPE_BF16, false>((const uint16_t*)v + first, c), c.left, d);
+    widen8<PS_TYPE_BF16>(load8<PS_TYPE_BF16, false>(row_of<PS_TYPE_BF16>(v, first, 1), c), c, d);
   else
-    widen8<PS_TYPE_F16>(load8<PS_TYPE_F16, false>((const uint16_t*)v + first, c), c.left, d);
+    widen8<PS_TYPE_F16>(load8<PS_TYPE_F16, false>(row_of<PS_TYPE_F16>(v, first, 1), c), c, d);
 }
 
 // Codes and scale of a block of 128 values, eight on each of a DPP row's 16

@@ -15,48 +15,52 @@ constexpr int kTeams = kThreads / 16;   // blocks that a workgroup handles at a 
 
 // The lane's place in unit u. Lanes of units that do not exist load from the
 // last one and store nothing.
-template <bool WIDE>
+template <int END>
 struct Place {
   int64_t row;
   int col;
   bool in;
-  Cols<WIDE> c;
+  Cols<END> c;
   __device__ __forceinline__ Place(const ActGrid& g, uint32_t u) : c(0, 0) {
     in = u < g.units;
     u = in ? u : g.units - 1;
     const uint32_t r = div_by(u, g.nb);
     row = r;
     col = (int)(u - r * g.nb.d) * kActBlock + (int)(threadIdx.x & 15) * 8;
-    c = Cols<WIDE>(col, g.cols);
+    c = Cols<END>(col, g.cols);
   }
-  __device__ __forceinline__ int left() const { return in ? c.left : 0; }   // columns to store
+  __device__ __forceinline__ Cols<END> to_store() const {
+    Cols<END> s = c;
+    if (!in) s.left = 0;
+    return s;
+  }
 };
 
 __device__ __forceinline__ uint32_t unit_of(int k, int per) {
   return (blockIdx.x * per + k) * (uint32_t)kTeams + threadIdx.x / 16;
 }
 
-template <int TYPE, bool WIDE, int K>
+template <int TYPE, int END, int K>
 __global__ __launch_bounds__(kThreads) void k_encode_act(ActGrid g, const void* x, int64_t ld, uint8_t* code, float* scale) {
   Raw8<TYPE> raw[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const Place<WIDE> p(g, unit_of(k, K));
+    const Place<END> p(g, unit_of(k, K));
     raw[k] = load8<TYPE>(row_of<TYPE>(x, p.row, ld), p.c);
   }
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const uint32_t u = unit_of(k, K);
-    const Place<WIDE> p(g, u);
+    const Place<END> p(g, u);
     float v[8], s;
-    widen8<TYPE>(raw[k], p.c.left, v);
+    widen8<TYPE>(raw[k], p.c, v);
     const u32x2_any c = encode_block(v, s);
-    store_codes8(code + p.row * g.cols, p.col, p.left(), c);
+    store_codes8(codes_of(code, p.row, g.cols), p.col, p.to_store(), c);
     if (p.in && (threadIdx.x & 15) == 0) scale[u] = s;
   }
 }
 
-template <int TYPE, bool WIDE, int K>
+template <int TYPE, int END, int K>
 __global__ __launch_bounds__(kThreads) void k_decode_act(ActGrid g, const uint8_t* code, const float* scale, void* x,
                                                          int64_t ld) {
   u32x2_any c[K];
@@ -64,18 +68,18 @@ __global__ __launch_bounds__(kThreads) void k_decode_act(ActGrid g, const uint8_
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const uint32_t u = unit_of(k, K);
-    const Place<WIDE> p(g, u);
-    c[k] = load_codes8(code + p.row * g.cols, p.c);
+    const Place<END> p(g, u);
+    c[k] = load_codes8(codes_of(code, p.row, g.cols), p.c);
     s[k] = scale[p.in ? u : g.units - 1];
   }
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const Place<WIDE> p(g, unit_of(k, K));
+    const Place<END> p(g, unit_of(k, K));
     float v[8];
-    codes_to_f32(c[k], p.c.left, v);
+    codes_to_f32(c[k], p.c, v);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] *= s[k];
-    store8<TYPE>(row_of<TYPE>(x, p.row, ld), p.col, p.left(), v);
+    store8<TYPE>(row_of<TYPE>(x, p.row, ld), p.col, p.to_store(), v);
   }
 }
 
@@ -100,44 +104,44 @@ __device__ __forceinline__ void activation(float a, float& f, float& slope) {
   slope = __builtin_fmaf(f * (1.0f - q), du, q);
 }
 
-template <int TYPE, int ACT, bool GATED, bool SAVE, bool WIDE, int K>
+template <int TYPE, int ACT, bool GATED, bool SAVE, int END, int K>
 __global__ __launch_bounds__(kThreads) void k_glu_forward(ActGrid g, GluArgs t) {
   Raw8<TYPE> ra[K], rb[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const Place<WIDE> p(g, unit_of(k, K));
+    const Place<END> p(g, unit_of(k, K));
     ra[k] = load8<TYPE>(row_of<TYPE>(t.a, p.row, t.lda), p.c);
     if (GATED) rb[k] = load8<TYPE>(row_of<TYPE>(t.b, p.row, t.ldb), p.c);
   }
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const uint32_t u = unit_of(k, K);
-    const Place<WIDE> p(g, u);
+    const Place<END> p(g, u);
     float a[8], b[8], o[8], s;
-    widen8<TYPE>(ra[k], p.c.left, a);
-    if (GATED) widen8<TYPE>(rb[k], p.c.left, b);
+    widen8<TYPE>(ra[k], p.c, a);
+    if (GATED) widen8<TYPE>(rb[k], p.c, b);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       float slope;
       activation<ACT>(a[j], o[j], slope);
       if (GATED) o[j] *= b[j];
     }
-    store8<TYPE>(row_of<TYPE>(t.out, p.row, t.ldo), p.col, p.left(), o);
+    store8<TYPE>(row_of<TYPE>(t.out, p.row, t.ldo), p.col, p.to_store(), o);
     if (SAVE) {
       const bool writes = p.in && (threadIdx.x & 15) == 0;
       const u32x2_any c = encode_block(a, s);
-      store_codes8(t.a_code + p.row * g.cols, p.col, p.left(), c);
+      store_codes8(codes_of(t.a_code, p.row, g.cols), p.col, p.to_store(), c);
       if (writes) t.a_scale[u] = s;
       if (GATED) {
         const u32x2_any d = encode_block(b, s);
-        store_codes8(t.b_code + p.row * g.cols, p.col, p.left(), d);
+        store_codes8(codes_of(t.b_code, p.row, g.cols), p.col, p.to_store(), d);
         if (writes) t.b_scale[u] = s;
       }
     }
   }
 }
 
-template <int TYPE, int ACT, bool GATED, bool WIDE, int K>
+template <int TYPE, int ACT, bool GATED, int END, int K>
 __global__ __launch_bounds__(kThreads) void k_glu_backward(ActGrid g, GluArgs t) {
   Raw8<TYPE> rd[K];
   u32x2_any ca[K], cb[K];
@@ -145,23 +149,23 @@ __global__ __launch_bounds__(kThreads) void k_glu_backward(ActGrid g, GluArgs t)
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const uint32_t u = unit_of(k, K);
-    const Place<WIDE> p(g, u);
+    const Place<END> p(g, u);
     rd[k] = load8<TYPE>(row_of<TYPE>(t.dout, p.row, t.ldd), p.c);
-    ca[k] = load_codes8(t.a_code + p.row * g.cols, p.c);
+    ca[k] = load_codes8(codes_of(t.a_code, p.row, g.cols), p.c);
     const uint32_t at = p.in ? u : g.units - 1;
     sa[k] = t.a_scale[at];
     if (GATED) {
-      cb[k] = load_codes8(t.b_code + p.row * g.cols, p.c);
+      cb[k] = load_codes8(codes_of(t.b_code, p.row, g.cols), p.c);
       sb[k] = t.b_scale[at];
     }
   }
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const Place<WIDE> p(g, unit_of(k, K));
+    const Place<END> p(g, unit_of(k, K));
     float d[8], a[8], b[8], da[8], db[8], o[8];
-    widen8<TYPE>(rd[k], p.c.left, d);
-    codes_to_f32(ca[k], p.c.left, a);
-    if (GATED) codes_to_f32(cb[k], p.c.left, b);
+    widen8<TYPE>(rd[k], p.c, d);
+    codes_to_f32(ca[k], p.c, a);
+    if (GATED) codes_to_f32(cb[k], p.c, b);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       float f, slope;
@@ -176,9 +180,9 @@ __global__ __launch_bounds__(kThreads) void k_glu_backward(ActGrid g, GluArgs t)
         o[j] = f;
       }
     }
-    store8<TYPE>(row_of<TYPE>(t.da, p.row, t.lda), p.col, p.left(), da);
-    if (GATED) store8<TYPE>(row_of<TYPE>(t.db, p.row, t.ldb), p.col, p.left(), db);
-    if (t.out) store8<TYPE>(row_of<TYPE>(t.out, p.row, t.ldo), p.col, p.left(), o);
+    store8<TYPE>(row_of<TYPE>(t.da, p.row, t.lda), p.col, p.to_store(), da);
+    if (GATED) store8<TYPE>(row_of<TYPE>(t.db, p.row, t.ldb), p.col, p.to_store(), db);
+    if (t.out) store8<TYPE>(row_of<TYPE>(t.out, p.row, t.ldo), p.col, p.to_store(), o);
   }
 }
 
@@ -187,34 +191,37 @@ dim3 grid_of(const ActGrid& g, int k) { return dim3((g.units + kTeams * k - 1) /
 // Blocks on a lane: two, so that four to six loads are under way at a time.
 constexpr int K = 2;
 
-template <int TYPE, int ACT, bool WIDE>
+template <int TYPE, int ACT, int END>
 ps_status glu_forward(const ActGrid& g, const GluArgs& p, hipStream_t s) {
   const bool save = p.a_code != nullptr;
   const dim3 grid = grid_of(g, K), wg(kThreads);
   if (p.b && save)
-    hipLaunchKernelGGL((k_glu_forward<TYPE, ACT, true, true, WIDE, K>), grid, wg, 0, s, g, p);
+    hipLaunchKernelGGL((k_glu_forward<TYPE, ACT, true, true, END, K>), grid, wg, 0, s, g, p);
   else if (p.b)
-    hipLaunchKernelGGL((k_glu_forward<TYPE, ACT, true, false, WIDE, K>), grid, wg, 0, s, g, p);
+    hipLaunchKernelGGL((k_glu_forward<TYPE, ACT, true, false, END, K>), grid, wg, 0, s, g, p);
   else if (save)
-    hipLaunchKernelGGL((k_glu_forward<TYPE, ACT, false, true, WIDE, K>), grid, wg, 0, s, g, p);
+    hipLaunchKernelGGL((k_glu_forward<TYPE, ACT, false, true, END, K>), grid, wg, 0, s, g, p);
   else
-    hipLaunchKernelGGL((k_glu_forward<TYPE, ACT, false, false, WIDE, K>), grid, wg, 0, s, g, p);
+    hipLaunchKernelGGL((k_glu_forward<TYPE, ACT, false, false, END, K>), grid, wg, 0, s, g, p);
   return hip_check(hipGetLastError(), "k_glu_forward launch");
 }
 
-template <int TYPE, int ACT, bool WIDE>
+template <int TYPE, int ACT, int END>
 ps_status glu_backward(const ActGrid& g, const GluArgs& p, hipStream_t s) {
   if (p.b_code)
-    hipLaunchKernelGGL((k_glu_backward<TYPE, ACT, true, WIDE, K>), grid_of(g, K), dim3(kThreads), 0, s, g, p);
+    hipLaunchKernelGGL((k_glu_backward<TYPE, ACT, true, END, K>), grid_of(g, K), dim3(kThreads), 0, s, g, p);
   else
-    hipLaunchKernelGGL((k_glu_backward<TYPE, ACT, false, WIDE, K>), grid_of(g, K), dim3(kThreads), 0, s, g, p);
+    hipLaunchKernelGGL((k_glu_backward<TYPE, ACT, false, END, K>), grid_of(g, K), dim3(kThreads), 0, s, g, p);
   return hip_check(hipGetLastError(), "k_glu_backward launch");
 }
 
 template <int TYPE, int ACT>
 ps_status glu(bool forward, const ActGrid& g, const GluArgs& p, hipStream_t s) {
-  if (g.cols < 8) return forward ? glu_forward<TYPE, ACT, false>(g, p, s) : glu_backward<TYPE, ACT, false>(g, p, s);
-  return forward ? glu_forward<TYPE, ACT, true>(g, p, s) : glu_backward<TYPE, ACT, true>(g, p, s);
+  switch (end_of(g.cols)) {
+    case kWhole: return forward ? glu_forward<TYPE, ACT, kWhole>(g, p, s) : glu_backward<TYPE, ACT, kWhole>(g, p, s);
+    case kPart: return forward ? glu_forward<TYPE, ACT, kPart>(g, p, s) : glu_backward<TYPE, ACT, kPart>(g, p, s);
+    default: return forward ? glu_forward<TYPE, ACT, kShort>(g, p, s) : glu_backward<TYPE, ACT, kShort>(g, p, s);
+  }
 }
 
 template <int TYPE>
@@ -236,19 +243,23 @@ ps_status glu(bool forward, const ActGrid& g, int type, int act, const GluArgs& 
 
 template <int TYPE>
 ps_status encode(const ActGrid& g, const void* x, int64_t ld, uint8_t* code, float* scale, hipStream_t s) {
-  if (g.cols < 8)
-    hipLaunchKernelGGL((k_encode_act<TYPE, false, K>), grid_of(g, K), dim3(kThreads), 0, s, g, x, ld, code, scale);
-  else
-    hipLaunchKernelGGL((k_encode_act<TYPE, true, K>), grid_of(g, K), dim3(kThreads), 0, s, g, x, ld, code, scale);
+  const dim3 grid = grid_of(g, K), wg(kThreads);
+  switch (end_of(g.cols)) {
+    case kWhole: hipLaunchKernelGGL((k_encode_act<TYPE, kWhole, K>), grid, wg, 0, s, g, x, ld, code, scale); break;
+    case kPart: hipLaunchKernelGGL((k_encode_act<TYPE, kPart, K>), grid, wg, 0, s, g, x, ld, code, scale); break;
+    default: hipLaunchKernelGGL((k_encode_act<TYPE, kShort, K>), grid, wg, 0, s, g, x, ld, code, scale); break;
+  }
   return hip_check(hipGetLastError(), "k_encode_act launch");
 }
 
 template <int TYPE>
 ps_status decode(const ActGrid& g, const uint8_t* code, const float* scale, void* x, int64_t ld, hipStream_t s) {
-  if (g.cols < 8)
-    hipLaunchKernelGGL((k_decode_act<TYPE, false, K>), grid_of(g, K), dim3(kThreads), 0, s, g, code, scale, x, ld);
-  else
-    hipLaunchKernelGGL((k_decode_act<TYPE, true, K>), grid_of(g, K), dim3(kThreads), 0, s, g, code, scale, x, ld);
+  const dim3 grid = grid_of(g, K), wg(kThreads);
+  switch (end_of(g.cols)) {
+    case kWhole: hipLaunchKernelGGL((k_decode_act<TYPE, kWhole, K>), grid, wg, 0, s, g, code, scale, x, ld); break;
+    case kPart: hipLaunchKernelGGL((k_decode_act<TYPE, kPart, K>), grid, wg, 0, s, g, code, scale, x, ld); break;
+    default: hipLaunchKernelGGL((k_decode_act<TYPE, kShort, K>), grid, wg, 0, s, g, code, scale, x, ld); break;
+  }
   return hip_check(hipGetLastError(), "k_decode_act launch");
 }
 

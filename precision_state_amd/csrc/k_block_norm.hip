@@ -99,7 +99,7 @@ __device__ __forceinline__ u32x2_any pack_codes(const float* z) {
 // A row by one team: the waves of a workgroup (V times eight columns on each
 // lane, as few lanes as hold the row), or, up to 1024 columns, a wave with three
 // others beside it.
-template <int TYPE, int V, bool WAVE, bool WIDE>
+template <int TYPE, int V, bool WAVE, int END>
 __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_forward(NormArgs p) {
   __shared__ float lds[2][kMostWaves][2];
   const int nt = WAVE ? 64 : blockDim.x, lane = WAVE ? threadIdx.x & 63 : threadIdx.x;
@@ -115,13 +115,13 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_forward(NormArgs p) 
   Raw8<TYPE> rx[V], ry[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const Cols<WIDE> c((v * nt + lane) * 8, p.cols);
-    if (p.y) ry[v] = load8<TYPE>(row_of<TYPE>(p.y, row, p.ldy), c);
-    rx[v] = load8<TYPE>(row_of<TYPE>(p.x, row, p.ldx), c);
+    const Cols<END> c((v * nt + lane) * 8, p.cols);
+    if (p.y) ry[v] = load8<TYPE>(scalar_pointer(row_of<TYPE>(p.y, row, p.ldy)), c);
+    rx[v] = load8<TYPE>(scalar_pointer(row_of<TYPE>(p.x, row, p.ldx)), c);
   }
   if (p.y) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) widen8<TYPE>(ry[v], p.cols - (v * nt + lane) * 8, z[v]);
+    for (int v = 0; v < V; ++v) widen8<TYPE>(ry[v], Cols<END>((v * nt + lane) * 8, p.cols), z[v]);
     if (p.post != PS_NORM_NONE) {
       const float r = normalise<V>(p, p.post, p.post_eps, lane, nt, sum, z);
       if (p.y_rstd && lane == 0) p.y_rstd[row] = r;
@@ -129,19 +129,18 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_forward(NormArgs p) 
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int col = (v * nt + lane) * 8;
-      const Cols<WIDE> c8(col, p.cols);
-      const int left = c8.left;
-      if (p.y_code) {
+      const Cols<END> c8(col, p.cols);
+        if (p.y_code) {
         u32x2_any c;
         if (p.post != PS_NORM_NONE) {
           c = pack_codes(z[v]);
         } else {
           float s;
           c = encode_block(z[v], s);
-          if ((lane & 15) == 0 && left > 0)
+          if ((lane & 15) == 0 && c8.left > 0)
             p.y_scale[(int64_t)row * ((p.cols + kActBlock - 1) / kActBlock) + col / kActBlock] = s;
         }
-        store_codes8(p.y_code + (int64_t)row * p.cols, col, left, c);
+        store_codes8(scalar_pointer(codes_of(p.y_code, row, p.cols)), col, c8, c);
       }
       float m[8], x[8];
       if (p.w1) {
@@ -154,23 +153,22 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_forward(NormArgs p) 
 #pragma unroll
         for (int j = 0; j < 8; ++j) z[v][j] *= m[j];
       }
-      widen8<TYPE>(rx[v], left, x);
+      widen8<TYPE>(rx[v], c8, x);
 #pragma unroll
       for (int j = 0; j < 8; ++j) z[v][j] = __builtin_fmaf(p.beta, z[v][j], p.alpha * x[j]);
-      store8<TYPE>(row_of<TYPE>(p.h, row, p.ldh), col, left, z[v]);
+      store8<TYPE>(scalar_pointer(row_of<TYPE>(p.h, row, p.ldh)), col, c8, z[v]);
     }
   } else {
 #pragma unroll
-    for (int v = 0; v < V; ++v) widen8<TYPE>(rx[v], p.cols - (v * nt + lane) * 8, z[v]);
+    for (int v = 0; v < V; ++v) widen8<TYPE>(rx[v], Cols<END>((v * nt + lane) * 8, p.cols), z[v]);
   }
   const float r = normalise<V>(p, p.pre, p.pre_eps, lane, nt, sum, z);
   if (p.h_rstd && lane == 0) p.h_rstd[row] = r;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int col = (v * nt + lane) * 8;
-    const Cols<WIDE> c8(col, p.cols);
-    const int left = c8.left;
-    if (p.h_code) store_codes8(p.h_code + (int64_t)row * p.cols, col, left, pack_codes(z[v]));
+    const Cols<END> c8(col, p.cols);
+    if (p.h_code) store_codes8(scalar_pointer(codes_of(p.h_code, row, p.cols)), col, c8, pack_codes(z[v]));
     float m[8], a[8];
     const int64_t o = seg_offset(p, PS_NORM_MOD_BY_SEG, seg);
     if (p.mul) {
@@ -184,7 +182,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_forward(NormArgs p) 
 #pragma unroll
       for (int j = 0; j < 8; ++j) z[v][j] += a[j];
     }
-    store8<TYPE>(row_of<TYPE>(p.n, row, p.ldn), col, left, z[v]);
+    store8<TYPE>(scalar_pointer(row_of<TYPE>(p.n, row, p.ldn)), col, c8, z[v]);
   }
 }
 
@@ -223,7 +221,7 @@ enum { kNoBranch = 0, kPlain = 1, kNormed = 2 };
 // whose barriers the load's latency would otherwise add to; a segment's vectors
 // stay in registers, since a load behind those of the next row would wait for
 // them. The widest rows (V > 1) leave no registers for either.
-template <int TYPE, int V, int SAVED, bool WIDE>
+template <int TYPE, int V, int SAVED, int END>
 __global__ __launch_bounds__(V == 1 ? 1024 : 512) void k_norm_backward(NormArgs p) {
   constexpr bool kAhead = V == 1;
   __shared__ float lds[2][kMostWaves][2];
@@ -249,7 +247,7 @@ __global__ __launch_bounds__(V == 1 ? 1024 : 512) void k_norm_backward(NormArgs 
     auto vectors = [&]() __attribute__((always_inline)) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const Cols<WIDE> c((v * nt + lane) * 8, p.cols);
+        const Cols<END> c((v * nt + lane) * 8, p.cols);
         const float one = p.flags & PS_NORM_MUL_PLUS_ONE ? 1.0f : 0.0f;
         float m[8];
 #pragma unroll
@@ -278,19 +276,19 @@ __global__ __launch_bounds__(V == 1 ? 1024 : 512) void k_norm_backward(NormArgs 
       h_rstd = p.h_rstd[r];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const Cols<WIDE> c((v * nt + lane) * 8, p.cols);
-        dn[v] = load8<TYPE>(row_of<TYPE>(p.dn, r, p.lddn), c);
-        ch[v] = load_codes8(p.h_code + (int64_t)r * p.cols, c);
+        const Cols<END> c((v * nt + lane) * 8, p.cols);
+        dn[v] = load8<TYPE>(scalar_pointer(row_of<TYPE>(p.dn, r, p.lddn)), c);
+        ch[v] = load_codes8(scalar_pointer(codes_of(p.h_code, r, p.cols)), c);
       }
     };
     auto load_second = [&](int r) __attribute__((always_inline)) {
       if (SAVED == kNormed) y_rstd = p.y_rstd[r];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const Cols<WIDE> c((v * nt + lane) * 8, p.cols);
+        const Cols<END> c((v * nt + lane) * 8, p.cols);
         dh[v] = Raw8<TYPE>{};
-        if (p.dh) dh[v] = load8<TYPE>(row_of<TYPE>(p.dh, r, p.lddh), c);
-        if (SAVED != kNoBranch) cy[v] = load_codes8(p.y_code + (int64_t)r * p.cols, c);
+        if (p.dh) dh[v] = load8<TYPE>(scalar_pointer(row_of<TYPE>(p.dh, r, p.lddh)), c);
+        if (SAVED != kNoBranch) cy[v] = load_codes8(scalar_pointer(codes_of(p.y_code, r, p.cols)), c);
         if (SAVED == kPlain) ys[v] = p.y_scale[(int64_t)r * blocks + min((v * nt + lane) * 8, p.cols - 1) / kActBlock];
       }
     };
@@ -316,9 +314,9 @@ __global__ __launch_bounds__(V == 1 ? 1024 : 512) void k_norm_backward(NormArgs 
       float g[V][8], z[V][8], c, d;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const int left = p.cols - (v * nt + lane) * 8;
-        widen8<TYPE>(dn[v], left, g[v]);
-        codes_to_f32(ch[v], left, z[v]);
+        const Cols<END> c8((v * nt + lane) * 8, p.cols);
+        widen8<TYPE>(dn[v], c8, g[v]);
+        codes_to_f32(ch[v], c8, z[v]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           acc[0][v][j] += g[v][j];
@@ -331,17 +329,18 @@ __global__ __launch_bounds__(V == 1 ? 1024 : 512) void k_norm_backward(NormArgs 
       back_sums<V>(p, p.pre, r1, sum, g, z, c, d);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const int col = (v * nt + lane) * 8, left = p.cols - col;
+        const int col = (v * nt + lane) * 8;
+        const Cols<END> c8(col, p.cols);
         float o[8];
-        widen8<TYPE>(dh[v], left, o);
+        widen8<TYPE>(dh[v], c8, o);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           g[v][j] = __builtin_fmaf(-c, z[v][j], __builtin_fmaf(r1, g[v][j], o[j] - d));
           o[j] = p.alpha * g[v][j];
         }
-        store8<TYPE>(row_of<TYPE>(p.dx, row, p.lddx), col, left, o);
+        store8<TYPE>(scalar_pointer(row_of<TYPE>(p.dx, row, p.lddx)), col, c8, o);
         if (SAVED != kNoBranch) {
-          codes_to_f32(cy[v], left, z[v]);
+          codes_to_f32(cy[v], c8, z[v]);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             if (SAVED == kPlain) z[v][j] *= ys[v];
@@ -366,16 +365,17 @@ __global__ __launch_bounds__(V == 1 ? 1024 : 512) void k_norm_backward(NormArgs 
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int col = (v * nt + lane) * 8;
-        store8<TYPE>(row_of<TYPE>(p.dy, row, p.lddy), col, p.cols - col, g[v]);
+        store8<TYPE>(scalar_pointer(row_of<TYPE>(p.dy, row, p.lddy)), col, Cols<END>(col, p.cols), g[v]);
       }
     }
-    float* part = p.part + (int64_t)(blockIdx.x + seg) * p.cols;
+    GLOBAL char* part = scalar_pointer(row_of<PS_TYPE_F32>(p.part, blockIdx.x + seg, p.cols));
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int col = (v * nt + lane) * 8, left = p.cols - col;
-      if (p.d_add) store8<PS_TYPE_F32, false>(part, col, left, acc[0][v]);
-      if (p.d_mul) store8<PS_TYPE_F32, false>(part + n_part, col, left, acc[1][v]);
-      if (p.d_gate || p.d_w1) store8<PS_TYPE_F32, false>(part + 2 * n_part, col, left, acc[2][v]);
+      const int col = (v * nt + lane) * 8;
+      const Cols<END> c8(col, p.cols);
+      if (p.d_add) store8<PS_TYPE_F32, false>(part, col, c8, acc[0][v]);
+      if (p.d_mul) store8<PS_TYPE_F32, false>(part + 4 * n_part, col, c8, acc[1][v]);
+      if (p.d_gate || p.d_w1) store8<PS_TYPE_F32, false>(part + 8 * n_part, col, c8, acc[2][v]);
     }
   }
 }
@@ -440,34 +440,50 @@ __global__ __launch_bounds__(kJoinCols * kJoinGroups) void k_norm_join(NormArgs 
 // Waves that hold `lanes` times eight columns, v times eight a lane.
 int waves_for(int lanes, int v) { return (lanes + 64 * v - 1) / (64 * v); }
 
-template <int TYPE>
+template <int TYPE, int END>
 ps_status forward(const NormArgs& p, hipStream_t s) {
   const int lanes = (p.cols + 7) / 8;
   const dim3 four((p.rows + 3) / 4);
-  if (p.cols < 8)
-    hipLaunchKernelGGL((k_norm_forward<TYPE, 1, true, false>), four, dim3(256), 0, s, p);
-  else if (lanes <= 64)
-    hipLaunchKernelGGL((k_norm_forward<TYPE, 1, true, true>), four, dim3(256), 0, s, p);
+  if (END == kShort || lanes <= 64)
+    hipLaunchKernelGGL((k_norm_forward<TYPE, 1, true, END>), four, dim3(256), 0, s, p);
   else if (lanes <= 128)
-    hipLaunchKernelGGL((k_norm_forward<TYPE, 2, true, true>), four, dim3(256), 0, s, p);
+    hipLaunchKernelGGL((k_norm_forward<TYPE, 2, true, END == kShort ? kPart : END>), four, dim3(256), 0, s, p);
   else
-    hipLaunchKernelGGL((k_norm_forward<TYPE, 2, false, true>), dim3(p.rows), dim3(waves_for(lanes, 2) * 64), 0, s, p);
+    hipLaunchKernelGGL((k_norm_forward<TYPE, 2, false, END == kShort ? kPart : END>), dim3(p.rows),
+                       dim3(waves_for(lanes, 2) * 64), 0, s, p);
   return hip_check(hipGetLastError(), "k_norm_forward launch");
+}
+
+template <int TYPE>
+ps_status forward(const NormArgs& p, hipStream_t s) {
+  switch (end_of(p.cols)) {
+    case kWhole: return forward<TYPE, kWhole>(p, s);
+    case kPart: return forward<TYPE, kPart>(p, s);
+    default: return forward<TYPE, kShort>(p, s);
+  }
+}
+
+template <int TYPE, int SAVED, int END>
+ps_status backward(const NormArgs& p, hipStream_t s) {
+  constexpr int kWideEnd = END == kShort ? kPart : END;
+  const int lanes = (p.cols + 7) / 8;
+  const dim3 grid((p.rows + p.strip - 1) / p.strip);
+  if (lanes <= 1024)
+    hipLaunchKernelGGL((k_norm_backward<TYPE, 1, SAVED, END>), grid, dim3(waves_for(lanes, 1) * 64), 0, s, p);
+  else if (lanes <= 1536)
+    hipLaunchKernelGGL((k_norm_backward<TYPE, 3, SAVED, kWideEnd>), grid, dim3(waves_for(lanes, 3) * 64), 0, s, p);
+  else
+    hipLaunchKernelGGL((k_norm_backward<TYPE, 4, SAVED, kWideEnd>), grid, dim3(waves_for(lanes, 4) * 64), 0, s, p);
+  return hip_check(hipGetLastError(), "k_norm_backward launch");
 }
 
 template <int TYPE, int SAVED>
 ps_status backward(const NormArgs& p, hipStream_t s) {
-  const int lanes = (p.cols + 7) / 8;
-  const dim3 grid((p.rows + p.strip - 1) / p.strip);
-  if (p.cols < 8)
-    hipLaunchKernelGGL((k_norm_backward<TYPE, 1, SAVED, false>), grid, dim3(64), 0, s, p);
-  else if (lanes <= 1024)
-    hipLaunchKernelGGL((k_norm_backward<TYPE, 1, SAVED, true>), grid, dim3(waves_for(lanes, 1) * 64), 0, s, p);
-  else if (lanes <= 1536)
-    hipLaunchKernelGGL((k_norm_backward<TYPE, 3, SAVED, true>), grid, dim3(waves_for(lanes, 3) * 64), 0, s, p);
-  else
-    hipLaunchKernelGGL((k_norm_backward<TYPE, 4, SAVED, true>), grid, dim3(waves_for(lanes, 4) * 64), 0, s, p);
-  return hip_check(hipGetLastError(), "k_norm_backward launch");
+  switch (end_of(p.cols)) {
+    case kWhole: return backward<TYPE, SAVED, kWhole>(p, s);
+    case kPart: return backward<TYPE, SAVED, kPart>(p, s);
+    default: return backward<TYPE, SAVED, kShort>(p, s);
+  }
 }
 
 template <int TYPE>

@@ -143,9 +143,9 @@ __device__ __forceinline__ void store_dw(const WgradArgs& p, int n, int k, int l
 #pragma unroll
           for (int i = 0; i < 4; ++i) was[i] = w[i];
         } else if (p.dw_type == PS_TYPE_BF16) {
-          widen8<PS_TYPE_BF16>(Raw8<PS_TYPE_BF16>{{{(*h)[0], (*h)[1], 0, 0}}}, 8, was);
+          widen8<PS_TYPE_BF16>(Raw8<PS_TYPE_BF16>{{{(*h)[0], (*h)[1], 0, 0}}}, Cols<kWhole>(0, 8), was);
         } else {
-          widen8<PS_TYPE_F16>(Raw8<PS_TYPE_F16>{{{(*h)[0], (*h)[1], 0, 0}}}, 8, was);
+          widen8<PS_TYPE_F16>(Raw8<PS_TYPE_F16>{{{(*h)[0], (*h)[1], 0, 0}}}, Cols<kWhole>(0, 8), was);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] += was[i];
@@ -390,17 +390,17 @@ __global__ __launch_bounds__(kThreads) void k_wgrad_join(WgradArgs p) {
 
 // Sums of dy over a strip of tokens: 256 columns a workgroup, eight on a lane,
 // every eighth token on a group of lanes.
-template <int TYPE, bool WIDE>
+template <int TYPE, int END>
 __global__ __launch_bounds__(kThreads) void k_column_sums(WgradArgs p) {
   __shared__ float lds[8][256];
   const int q = threadIdx.x % 32, group = threadIdx.x / 32;
   const int col = blockIdx.x * 256 + q * 8;
   const int64_t first = (int64_t)blockIdx.y * p.cut.per_strip, end = min(first + p.cut.per_strip, p.tokens);
-  const Cols<WIDE> c8(col, p.n);
+  const Cols<END> c8(col, p.n);
   float s[8] = {};
   for (int64_t t = first + group; t < end; t += 8) {
     float v[8];
-    widen8<TYPE>(load8<TYPE, false>(row_of<TYPE>(p.dy, t, p.lddy), c8), c8.left, v);
+    widen8<TYPE>(load8<TYPE, false>(row_of<TYPE>(p.dy, t, p.lddy), c8), c8, v);
 #pragma unroll
     for (int j = 0; j < 8; ++j) s[j] += v[j];
   }
@@ -438,9 +438,9 @@ ps_status product(const WgradArgs& p, hipStream_t s) {
   if (p.db || p.add) {
     const dim3 grid((p.n + 255) / 256, p.cut.strips);
     if (p.cut.strips && p.n < 8)
-      hipLaunchKernelGGL((k_column_sums<TYPE, false>), grid, dim3(kThreads), 0, s, p);
+      hipLaunchKernelGGL((k_column_sums<TYPE, kShort>), grid, dim3(kThreads), 0, s, p);
     else if (p.cut.strips)
-      hipLaunchKernelGGL((k_column_sums<TYPE, true>), grid, dim3(kThreads), 0, s, p);
+      hipLaunchKernelGGL((k_column_sums<TYPE, kPart>), grid, dim3(kThreads), 0, s, p);
     if (ps_status st = hip_check(hipGetLastError(), "k_column_sums launch")) return st;
     hipLaunchKernelGGL(k_column_join, dim3((p.n + kThreads - 1) / kThreads), dim3(kThreads), 0, s, p);
     if (ps_status st = hip_check(hipGetLastError(), "k_column_join launch")) return st;
