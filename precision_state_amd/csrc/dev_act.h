@@ -237,15 +237,26 @@ __device__ __forceinline__ void codes_to_f32(u32x2_any c, const Cols<END>& at, f
   e4m3_unpack4(c[1], d + 4);
 }
 
-// Eight values of a vector of any type (uniform), kept in the caches.
+// Eight values of a vector of any type (uniform), kept in the caches: loaded, and
+// later widened, so that several vectors are under way at a time.
+typedef Raw8<PS_TYPE_F32> RawVec;
 template <int END>
-__device__ __forceinline__ void load_vec8(const void* v, int type, int64_t first, const Cols<END>& c, float* d) {
+__device__ __forceinline__ RawVec load_vec(const void* v, int type, int64_t first, const Cols<END>& c) {
+  RawVec r;
   if (type == PS_TYPE_F32)
-    widen8<PS_TYPE_F32>(load8<PS_TYPE_F32, false>(row_of<PS_TYPE_F32>(v, first, 1), c), c, d);
-  else if (type == PS_TYPE_BF16)
-    widen8<PS_TYPE_BF16>(load8<PS_TYPE_BF16, false>(row_of<PS_TYPE_BF16>(v, first, 1), c), c, d);
+    r = load8<PS_TYPE_F32, false>(row_of<PS_TYPE_F32>(v, first, 1), c);
   else
-    widen8<PS_TYPE_F16>(load8<PS_TYPE_F16, false>(row_of<PS_TYPE_F16>(v, first, 1), c), c, d);
+    r.w[0] = load8<PS_TYPE_BF16, false>(row_of<PS_TYPE_BF16>(v, first, 1), c).w[0];
+  return r;
+}
+template <int END>
+__device__ __forceinline__ void widen_vec(const RawVec& r, int type, const Cols<END>& c, float* d) {
+  if (type == PS_TYPE_F32)
+    widen8<PS_TYPE_F32>(r, c, d);
+  else if (type == PS_TYPE_BF16)
+    widen8<PS_TYPE_BF16>(Raw8<PS_TYPE_BF16>{{r.w[0]}}, c, d);
+  else
+    widen8<PS_TYPE_F16>(Raw8<PS_TYPE_F16>{{r.w[0]}}, c, d);
 }
 
 // Codes and scale of a block of 128 values, eight on each of a DPP row's 16

@@ -113,11 +113,17 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_forward(NormArgs p) 
   }
   float z[V][8];
   Raw8<TYPE> rx[V], ry[V];
+  RawVec rw[V], rg[V], rm[V], ra[V];   // all loads of the row at once
+  const int64_t mod = seg_offset(p, PS_NORM_MOD_BY_SEG, seg);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const Cols<END> c((v * nt + lane) * 8, p.cols);
     if (p.y) ry[v] = load8<TYPE>(scalar_pointer(row_of<TYPE>(p.y, row, p.ldy)), c);
     rx[v] = load8<TYPE>(scalar_pointer(row_of<TYPE>(p.x, row, p.ldx)), c);
+    if (p.w1) rw[v] = load_vec(p.w1, p.vec_type, 0, c);
+    if (p.gate) rg[v] = load_vec(p.gate, p.vec_type, seg_offset(p, PS_NORM_GATE_BY_SEG, seg), c);
+    if (p.mul) rm[v] = load_vec(p.mul, p.vec_type, mod, c);
+    if (p.add) ra[v] = load_vec(p.add, p.vec_type, mod, c);
   }
   if (p.y) {
 #pragma unroll
@@ -144,12 +150,12 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_forward(NormArgs p) 
       }
       float m[8], x[8];
       if (p.w1) {
-        load_vec8(p.w1, p.vec_type, 0, c8, m);
+        widen_vec(rw[v], p.vec_type, c8, m);
 #pragma unroll
         for (int j = 0; j < 8; ++j) z[v][j] *= m[j];
       }
       if (p.gate) {
-        load_vec8(p.gate, p.vec_type, seg_offset(p, PS_NORM_GATE_BY_SEG, seg), c8, m);
+        widen_vec(rg[v], p.vec_type, c8, m);
 #pragma unroll
         for (int j = 0; j < 8; ++j) z[v][j] *= m[j];
       }
@@ -170,15 +176,14 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_forward(NormArgs p) 
     const Cols<END> c8(col, p.cols);
     if (p.h_code) store_codes8(scalar_pointer(codes_of(p.h_code, row, p.cols)), col, c8, pack_codes(z[v]));
     float m[8], a[8];
-    const int64_t o = seg_offset(p, PS_NORM_MOD_BY_SEG, seg);
     if (p.mul) {
-      load_vec8(p.mul, p.vec_type, o, c8, m);
+      widen_vec(rm[v], p.vec_type, c8, m);
       const float one = p.flags & PS_NORM_MUL_PLUS_ONE ? 1.0f : 0.0f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) z[v][j] *= one + m[j];
     }
     if (p.add) {
-      load_vec8(p.add, p.vec_type, o, c8, a);
+      widen_vec(ra[v], p.vec_type, c8, a);
 #pragma unroll
       for (int j = 0; j < 8; ++j) z[v][j] += a[j];
     }
@@ -227,7 +232,11 @@ __global__ __launch_bounds__(V == 1 ? 1024 : 512) void k_norm_backward(NormArgs 
   __shared__ float lds[2][kMostWaves][2];
   const int nt = blockDim.x, lane = threadIdx.x;
   TeamSum sum{lds, nt / 64};
-  const int first = blockIdx.x * p.strip, last = min(p.rows - first, p.strip) + first;
+  // Without segments a strip takes every gridDim.x-th row, so that all workgroups
+  // sweep the matrices from front to back together.
+  const int step = p.seg_start ? 1 : gridDim.x;
+  const int first = p.seg_start ? blockIdx.x * p.strip : blockIdx.x;
+  const int last = p.seg_start ? min(p.rows - first, p.strip) + first : p.rows;
   const int64_t n_part = (int64_t)p.slots * p.cols;
   const int blocks = (p.cols + kActBlock - 1) / kActBlock;
   const bool branch = p.dy != nullptr;
@@ -249,21 +258,25 @@ __global__ __launch_bounds__(V == 1 ? 1024 : 512) void k_norm_backward(NormArgs 
       for (int v = 0; v < V; ++v) {
         const Cols<END> c((v * nt + lane) * 8, p.cols);
         const float one = p.flags & PS_NORM_MUL_PLUS_ONE ? 1.0f : 0.0f;
+        RawVec rm, rg, rw;
+        if (p.mul) rm = load_vec(p.mul, p.vec_type, seg_offset(p, PS_NORM_MOD_BY_SEG, seg), c);
+        if (p.gate) rg = load_vec(p.gate, p.vec_type, seg_offset(p, PS_NORM_GATE_BY_SEG, seg), c);
+        if (p.w1) rw = load_vec(p.w1, p.vec_type, 0, c);
         float m[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) km[v][j] = 1.0f, ky[v][j] = j < c.left ? p.beta : 0.0f;
         if (p.mul) {
-          load_vec8(p.mul, p.vec_type, seg_offset(p, PS_NORM_MOD_BY_SEG, seg), c, m);
+          widen_vec(rm, p.vec_type, c, m);
 #pragma unroll
           for (int j = 0; j < 8; ++j) km[v][j] = one + m[j];
         }
         if (p.gate) {
-          load_vec8(p.gate, p.vec_type, seg_offset(p, PS_NORM_GATE_BY_SEG, seg), c, m);
+          widen_vec(rg, p.vec_type, c, m);
 #pragma unroll
           for (int j = 0; j < 8; ++j) ky[v][j] *= m[j];
         }
         if (p.w1) {
-          load_vec8(p.w1, p.vec_type, 0, c, m);
+          widen_vec(rw, p.vec_type, c, m);
 #pragma unroll
           for (int j = 0; j < 8; ++j) ky[v][j] *= m[j];
         }
@@ -293,9 +306,9 @@ __global__ __launch_bounds__(V == 1 ? 1024 : 512) void k_norm_backward(NormArgs 
       }
     };
     if (kAhead) {
-      vectors();
       load_first(row);
       load_second(row);
+      vectors();
     }
 #pragma unroll
     for (int i = 0; i < 3; ++i)
@@ -304,13 +317,13 @@ __global__ __launch_bounds__(V == 1 ? 1024 : 512) void k_norm_backward(NormArgs 
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[i][v][j] = 0;
 
-    for (; row < end; ++row) {
+    for (; row < end; row += step) {
       if (!kAhead) {
-        vectors();
         load_first(row);
         load_second(row);
+        vectors();
       }
-      const int ahead = min(row + 1, end - 1);   // the last row is loaded twice
+      const int ahead = row + step < end ? row + step : row;   // the last row is loaded twice
       float g[V][8], z[V][8], c, d;
 #pragma unroll
       for (int v = 0; v < V; ++v) {

@@ -66,15 +66,16 @@ struct NormArgs {
   int32_t strip, slots;     // rows of a strip; strip i's part of segment b is slot i + b
   int32_t accumulate;
 };
-// Rows of a strip of the backward pass. As many strips as workgroups are at
-// work at a time (16 waves a compute unit, 8 for the widest rows), but of 16 rows
-// at least, since a strip's sums cost as much memory traffic as one of its rows;
-// for few rows 256 strips all the same, since rows of a strip take turns.
+// Rows of a strip of the backward pass. At most as many strips as workgroups are
+// at work at a time (16 waves a compute unit, 8 for the widest rows); of 16 rows
+// at least, since a strip's sums cost as much memory traffic as one of its rows,
+// but of two where that leaves less than 1024 strips, since rows take turns.
 inline int32_t norm_strip_rows(int64_t rows, int64_t cols) {
   const int64_t lanes = (cols + 7) / 8, waves = (lanes + 63) / 64;
   const int64_t at_a_time = waves > 16 ? 256 : 256 * (16 / (waves > 0 ? waves : 1));
-  int64_t strips = at_a_time < rows / 16 ? at_a_time : rows / 16;
-  if (strips < 256) strips = 256;
+  int64_t strips = rows / 2 < 1024 ? (rows + 1) / 2 : 1024;
+  if (strips < rows / 16) strips = rows / 16;
+  if (strips > at_a_time) strips = at_a_time;
   return (int32_t)((rows + strips - 1) / strips);
 }
 ps_status launch_norm_forward(const NormArgs& p, int type, hipStream_t s);
