@@ -122,11 +122,10 @@ __device__ __forceinline__ int64_t safe_rows(int64_t rows, int64_t pitch, int64_
 }
 
 // Four results of a row to memory, `left` of them inside: dw = mul acc + add db [+ dw].
-__device__ __forceinline__ void store_dw(const WgradArgs& p, int n, int k, int left, f32x4 acc) {
+__device__ __forceinline__ void store_dw(const WgradArgs& p, int n, int k, int left, f32x4 acc, float db) {
   if (left <= 0) return;
   const int64_t o = (int64_t)n * p.lddw + k;
   float v[8] = {acc[0], acc[1], acc[2], acc[3], 0, 0, 0, 0};
-  const float db = p.add ? p.db_sum[n] : 0.0f;
   if (left >= 4) {
     f32x4_any* f = (f32x4_any*)((float*)p.dw + o);
     u32x2_any* h = (u32x2_any*)((uint16_t*)p.dw + o);
@@ -177,7 +176,8 @@ __device__ __forceinline__ void store_dw(const WgradArgs& p, int n, int k, int l
   }
 }
 
-template <int TYPE, bool SCALED, class S>
+// SUMS: the column sums of dy too, for db or add.
+template <int TYPE, bool SCALED, bool SUMS, class S>
 __global__ __launch_bounds__(kThreads, 1) void k_wgrad(WgradArgs p) {
   __shared__ __attribute__((aligned(16))) char lds[2 * S::BYTES];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -191,63 +191,79 @@ __global__ __launch_bounds__(kThreads, 1) void k_wgrad(WgradArgs p) {
   const int64_t safe = min(end, min(safe_rows(p.tokens, p.lddy * 2, n0 * 2, S::N * 2, p.n * 2),
                                     safe_rows(p.tokens, p.k, k0, S::K, p.k)));
 
-  // The next step's tiles on their way: registers between two loads and two writes.
-  constexpr int kA = (S::DY / 16 + kThreads - 1) / kThreads, kB = (S::CODE / 16 + kThreads - 1) / kThreads;
-  constexpr int kRowA = S::N / 8, kRowB = S::K / 16;   // chunks of a row
-  constexpr bool kWholeA = S::DY / 16 % kThreads == 0, kWholeB = S::CODE / 16 % kThreads == 0;
+  // The next step's tiles on their way: registers between a load and a write. A
+  // lane takes the same columns of every kPassA-th or kPassB-th row.
+  constexpr int kRowA = S::N / 8, kRowB = S::K / 16;   // chunks of 16 bytes of a row
+  constexpr int kPassA = kThreads / kRowA, kPassB = kThreads / kRowB;
+  constexpr int kA = (S::STEP + kPassA - 1) / kPassA, kB = (S::STEP + kPassB - 1) / kPassB;
+  static_assert(kA * kPassA == S::STEP && (kB * kPassB == S::STEP || kB == 1), "whole passes");
   static_assert(S::STEP * S::KB <= kThreads, "a scale for each lane at most");
-  const char *dy = (const char*)p.dy + 2 * n0, *code = (const char*)p.code + k0;
+  const int ta = threadIdx.x / kRowA, qa = threadIdx.x % kRowA, tb = threadIdx.x / kRowB, qb = threadIdx.x % kRowB;
+  const bool has_b = kB * kPassB == S::STEP || tb < S::STEP;
+  const uint32_t from_a = (uint32_t)ta * (uint32_t)(2 * p.lddy) + qa * 16, from_b = (uint32_t)tb * (uint32_t)p.k + qb * 16;
+  const int to_a = chunk_at<2 * S::N, 64>(ta, qa), to_b = S::DY + chunk_at<S::K, 32>(tb, qb);
+  const int scale_block = min(k0 / kActBlock + (int)threadIdx.x % S::KB, k_blocks - 1);
+  const int to_s = S::DY + S::CODE + (threadIdx.x % S::KB * S::STEP + threadIdx.x / S::KB) * 4;
+  const bool has_s = SCALED && threadIdx.x < S::STEP * S::KB;
   u32x4 ra[kA], rb[kB];
   float rs = 0;
-  auto load = [&](int64_t t0) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < kA; ++i) {
-      const int c = i * kThreads + threadIdx.x;
-      if (kWholeA || c < S::DY / 16) ra[i] = *(const GLOBAL u32x4_any*)(dy + (t0 + c / kRowA) * (2 * p.lddy) + c % kRowA * 16);
-    }
-#pragma unroll
-    for (int i = 0; i < kB; ++i) {
-      const int c = i * kThreads + threadIdx.x;
-      if (kWholeB || c < S::CODE / 16) rb[i] = *(const GLOBAL u32x4_byte*)(code + (t0 + c / kRowB) * p.k + c % kRowB * 16);
-    }
-    if (SCALED && threadIdx.x < S::STEP * S::KB)
-      rs = p.scale[(t0 + threadIdx.x / S::KB) * k_blocks + min(k0 / kActBlock + (int)threadIdx.x % S::KB, k_blocks - 1)];
+  float sums[8] = {};
+  auto load_a = [&](int i, int64_t t0) __attribute__((always_inline)) {
+    const GLOBAL char* row = scalar_pointer((GLOBAL char*)p.dy + (t0 + i * kPassA) * (2 * p.lddy) + 2 * n0);
+    ra[i] = *(const GLOBAL u32x4_any*)(row + from_a);
   };
-  auto place = [&](char* buf) __attribute__((always_inline)) {
+  auto load_b = [&](int i, int64_t t0) __attribute__((always_inline)) {
+    const GLOBAL char* row = scalar_pointer((GLOBAL char*)p.code + (t0 + i * kPassB) * p.k + k0);
+    if (has_b) rb[i] = *(const GLOBAL u32x4_byte*)(row + from_b);
+  };
+  auto load_s = [&](int64_t t0) __attribute__((always_inline)) {
+    if (has_s) rs = p.scale[(t0 + threadIdx.x / S::KB) * k_blocks + scale_block];
+  };
+  auto add_up = [&](const u32x4& w, bool counts) __attribute__((always_inline)) {
+    if (!SUMS) return;
+    float v[8];
+    widen8<TYPE>(Raw8<TYPE>{{w & (counts ? 0xFFFFFFFFu : 0u)}}, Cols<kWhole>(0, 8), v);
 #pragma unroll
-    for (int i = 0; i < kA; ++i) {
-      const int c = i * kThreads + threadIdx.x;
-      if (kWholeA || c < S::DY / 16) *(u32x4*)(buf + chunk_at<2 * S::N, 64>(c / kRowA, c % kRowA)) = ra[i];
+    for (int j = 0; j < 8; ++j) sums[j] += v[j];
+  };
+  // i-th part of as many as there are groups of 16 tokens: what was loaded goes to
+  // the buffer, and the same rows of the step after are loaded.
+  constexpr int U = S::STEP / 16;
+  auto renew = [&](char* buf, int part, int64_t t0, bool counts) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = part * kA / U; i < (part + 1) * kA / U; ++i) {
+      *(u32x4*)(buf + to_a + i * kPassA * 2 * S::N) = ra[i];
+      add_up(ra[i], counts);
+      load_a(i, t0);
     }
 #pragma unroll
-    for (int i = 0; i < kB; ++i) {
-      const int c = i * kThreads + threadIdx.x;
-      if (kWholeB || c < S::CODE / 16) *(u32x4*)(buf + S::DY + chunk_at<S::K, 32>(c / kRowB, c % kRowB)) = rb[i];
+    for (int i = part * kB / U; i < (part + 1) * kB / U; ++i) {
+      if (has_b) *(u32x4*)(buf + to_b + i * kPassB * S::K) = rb[i];
+      load_b(i, t0);
     }
-    // scales by block, then token, so that a lane reads those of its eight tokens at once
-    if (SCALED && threadIdx.x < S::STEP * S::KB)
-      ((float*)(buf + S::DY + S::CODE))[threadIdx.x % S::KB * S::STEP + threadIdx.x / S::KB] = rs;
+    if (part == 0) {
+      if (has_s) *(float*)(buf + to_s) = rs;
+      load_s(t0);
+    }
   };
   // The same for a step at the end of the split or of the matrices.
   auto load_and_place = [&](char* buf, int64_t t0) __attribute__((always_inline)) {
 #pragma unroll 1
-    for (int c = threadIdx.x; c < S::DY / 16; c += kThreads) {
-      const int64_t t = t0 + c / kRowA;
-      *(u32x4*)(buf + chunk_at<2 * S::N, 64>(c / kRowA, c % kRowA)) =
-          load16_guarded((const char*)p.dy, t, t < end ? p.tokens : 0, 2 * p.lddy, 2 * n0 + c % kRowA * 16, 2 * p.n);
+    for (int i = 0; i < kA; ++i) {
+      const int64_t t = t0 + i * kPassA + ta;
+      const u32x4 w = load16_guarded((const char*)p.dy, t, t < end ? p.tokens : 0, 2 * p.lddy, 2 * n0 + qa * 16, 2 * p.n);
+      *(u32x4*)(buf + to_a + i * kPassA * 2 * S::N) = w;
+      add_up(w, true);
     }
 #pragma unroll 1
-    for (int c = threadIdx.x; c < S::CODE / 16; c += kThreads) {
-      const int64_t t = t0 + c / kRowB;
-      *(u32x4*)(buf + S::DY + chunk_at<S::K, 32>(c / kRowB, c % kRowB)) =
-          load16_guarded((const char*)p.code, t, t < end ? p.tokens : 0, p.k, k0 + c % kRowB * 16, p.k);
+    for (int i = 0; i < kB; ++i) {
+      const int64_t t = t0 + i * kPassB + tb;
+      if (has_b)
+        *(u32x4*)(buf + to_b + i * kPassB * S::K) =
+            load16_guarded((const char*)p.code, t, t < end ? p.tokens : 0, p.k, k0 + qb * 16, p.k);
     }
-    if (SCALED && threadIdx.x < S::STEP * S::KB) {
-      const int64_t t = t0 + threadIdx.x / S::KB;
-      const int block = min(k0 / kActBlock + (int)threadIdx.x % S::KB, k_blocks - 1);
-      ((float*)(buf + S::DY + S::CODE))[threadIdx.x % S::KB * S::STEP + threadIdx.x / S::KB] =
-          t < end ? p.scale[t * k_blocks + block] : 0.0f;
-    }
+    const int64_t t = t0 + threadIdx.x / S::KB;
+    if (has_s) *(float*)(buf + to_s) = t < end ? p.scale[t * k_blocks + scale_block] : 0.0f;
   };
 
   f32x16 acc[S::FN][S::FK];
@@ -289,45 +305,48 @@ __global__ __launch_bounds__(kThreads, 1) void k_wgrad(WgradArgs p) {
   // Two buffers: while one is multiplied the other is filled with the tiles that
   // were loaded a step before. The fragments of 16 tokens are read ahead of the
   // matrix instructions that use them, the first ones of a step before the last
-  // 16 tokens of the step before are multiplied.
-  constexpr int U = S::STEP / 16;
-  char* cur = lds;
-  char* nxt = lds + S::BYTES;
+  // 16 tokens of the step before are multiplied. The last steps load and place
+  // the last tiles again, so that no branch cuts a step.
   const int64_t whole = first + (safe > first ? (safe - first) / S::STEP * S::STEP : 0);
-  if (first < whole) {
-    load(first);
-    place(cur);
-    if (first + S::STEP < whole) load(first + S::STEP);
-    __syncthreads();
-    read(cur, 0, 0);
-    for (int64_t t = first; t < whole; t += S::STEP) {
-      const bool more = t + S::STEP < whole;
+  auto step = [&](char* cur, char* nxt, int64_t t) __attribute__((always_inline)) {
+    const int64_t later = min(t + 2 * S::STEP, whole - S::STEP);
+    const bool more = t + S::STEP < whole;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (u + 1 < U) {
-          read(cur, (u + 1) * 16, (u + 1) & 1);
-        } else if (more) {
-          __syncthreads();
-          read(nxt, 0, (u + 1) & 1);
-        }
-        if (u == 0 && more) {
-          place(nxt);
-          if (t + 2 * S::STEP < whole) load(t + 2 * S::STEP);
-        }
-        multiply(u & 1);
-      }
-      char* was = cur;
-      cur = nxt;
-      nxt = was;
+    for (int u = 0; u < U; ++u) {
+      if (u + 1 == U) __syncthreads();
+      read(u + 1 < U ? cur : nxt, (u + 1) % U * 16, (u + 1) & 1);
+      __builtin_amdgcn_sched_barrier(0);
+      if (u + 1 < U) renew(nxt, u, later, more);
+      if (u + 2 == U) renew(nxt, u + 1, later, more);
+      multiply(u & 1);
+      __builtin_amdgcn_sched_barrier(0);
     }
+  };
+  if (first < whole) {
+    char *one = lds, *two = lds + S::BYTES;
+#pragma unroll
+    for (int i = 0; i < kA; ++i) load_a(i, first);
+#pragma unroll
+    for (int i = 0; i < kB; ++i) load_b(i, first);
+    load_s(first);
+#pragma unroll
+    for (int u = 0; u < U; ++u) renew(one, u, min(first + S::STEP, whole - S::STEP), true);
+    __syncthreads();
+    read(one, 0, 0);
+    int64_t t = first;
+    for (; t + S::STEP < whole; t += 2 * S::STEP) {
+      step(one, two, t);
+      step(two, one, t + S::STEP);
+    }
+    if (t < whole) step(one, two, t);
   }
   for (int64_t t = whole; t < end; t += S::STEP) {
     __syncthreads();
-    load_and_place(cur, t);
+    load_and_place(lds, t);
     __syncthreads();
 #pragma unroll 1
     for (int u = 0; u < S::STEP; u += 16) {
-      read(cur, u, 0);
+      read(lds, u, 0);
       multiply(0);
     }
   }
@@ -336,8 +355,29 @@ __global__ __launch_bounds__(kThreads, 1) void k_wgrad(WgradArgs p) {
   // lane % 32. A wave's 32 rows go through its part of shared memory, so that
   // rows are stored four columns a lane.
   constexpr int kCols = S::FK * 32, kLanes = kCols / 4;
-  static_assert(4 * 32 * kCols * 4 <= 2 * S::BYTES, "a part for each wave");
+  static_assert(4 * 32 * kCols * 4 + S::N * 4 <= 2 * S::BYTES, "a part for each wave, and the column sums");
   float* part = (float*)lds + wave * (32 * kCols);
+  float* db = (float*)(lds + 2 * S::BYTES) - S::N;
+  if (SUMS) {
+    float* rows = (float*)lds;   // [kPassA][N]
+    static_assert(kPassA * S::N * 4 + S::N * 4 <= 2 * S::BYTES, "a row for each pass");
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) rows[ta * S::N + qa * 8 + j] = sums[j];
+    __syncthreads();
+    if (threadIdx.x < S::N) {
+      float s = rows[threadIdx.x];
+      for (int i = 1; i < kPassA; ++i) s += rows[i * S::N + threadIdx.x];
+      db[threadIdx.x] = s;
+      const int n = n0 + threadIdx.x;
+      if (k0 == 0 && n < p.n) {
+        if (p.cut.splits > 1)
+          p.db_part[(int64_t)split * p.n + n] = s;
+        else if (p.db)
+          p.db[n] = p.accumulate ? p.db[n] + s : s;
+      }
+    }
+  }
 #pragma unroll
   for (int i = 0; i < S::FN; ++i) {
     __syncthreads();
@@ -349,7 +389,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_wgrad(WgradArgs p) {
     __syncthreads();
 #pragma unroll 1
     for (int c = lane; c < 32 * kLanes; c += 64) {
-      const int n = n0 + wn + i * 32 + c / kLanes, k = k0 + wk + c % kLanes * 4;
+      const int row = wn + i * 32 + c / kLanes, n = n0 + row, k = k0 + wk + c % kLanes * 4;
       if (n >= p.n) break;
       const f32x4 v = *(const f32x4*)(part + c * 4);
       if (p.cut.splits > 1) {
@@ -362,89 +402,61 @@ __global__ __launch_bounds__(kThreads, 1) void k_wgrad(WgradArgs p) {
             if (k + x < p.k) d[x] = v[x];
         }
       } else {
-        store_dw(p, n, k, p.k - k, v);
+        store_dw(p, n, k, p.k - k, v, SUMS ? db[row] : 0.0f);
       }
     }
   }
 }
 
-// The splits' partial results added up in order, four columns of a row a lane.
+// The splits' partial results added up in order, four columns of a row a lane;
+// behind them db, one of its values a lane.
 __global__ __launch_bounds__(kThreads) void k_wgrad_join(WgradArgs p) {
   const int quads = (p.k + 3) / 4;
   const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x, size = (int64_t)p.n * p.k;
-  if (i >= (int64_t)p.n * quads) return;
+  auto db_of = [&](int n) {
+    float s = 0;
+#pragma unroll 8
+    for (int j = 0; j < p.cut.splits; ++j) s += p.db_part[(int64_t)j * p.n + n];
+    return s;
+  };
+  if (i >= (int64_t)p.n * quads) {
+    const int64_t n = i - (int64_t)p.n * quads;
+    if (!p.db || n >= p.n) return;
+    const float s = db_of((int)n);
+    p.db[n] = p.accumulate ? p.db[n] + s : s;
+    return;
+  }
   const int n = (int)(i / quads), k = (int)(i % quads) * 4, left = p.k - k;
   const float* d = p.part + (int64_t)n * p.k + k;
   f32x4 s = {0, 0, 0, 0};
-  for (int j = 0; j < p.cut.splits; ++j, d += size) {
-    if (left >= 4) {
-      s += *(const f32x4_any*)d;
-    } else {
+  if (left >= 4) {
+#pragma unroll 8
+    for (int j = 0; j < p.cut.splits; ++j) s += *(const f32x4_any*)(d + j * size);
+  } else {
+    for (int j = 0; j < p.cut.splits; ++j)
 #pragma unroll
       for (int x = 0; x < 3; ++x)
-        if (x < left) s[x] += d[x];
-    }
+        if (x < left) s[x] += d[j * size + x];
   }
-  store_dw(p, n, k, left, s);
-}
-
-// Sums of dy over a strip of tokens: 256 columns a workgroup, eight on a lane,
-// every eighth token on a group of lanes.
-template <int TYPE, int END>
-__global__ __launch_bounds__(kThreads) void k_column_sums(WgradArgs p) {
-  __shared__ float lds[8][256];
-  const int q = threadIdx.x % 32, group = threadIdx.x / 32;
-  const int col = blockIdx.x * 256 + q * 8;
-  const int64_t first = (int64_t)blockIdx.y * p.cut.per_strip, end = min(first + p.cut.per_strip, p.tokens);
-  const Cols<END> c8(col, p.n);
-  float s[8] = {};
-  for (int64_t t = first + group; t < end; t += 8) {
-    float v[8];
-    widen8<TYPE>(load8<TYPE, false>(row_of<TYPE>(p.dy, t, p.lddy), c8), c8, v);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) s[j] += v[j];
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) lds[group][q * 8 + j] = s[j];
-  __syncthreads();
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= p.n) return;
-  float total = lds[0][threadIdx.x];
-#pragma unroll
-  for (int g = 1; g < 8; ++g) total += lds[g][threadIdx.x];
-  p.db_part[(int64_t)blockIdx.y * p.n + c] = total;
-}
-
-__global__ __launch_bounds__(kThreads) void k_column_join(WgradArgs p) {
-  const int c = blockIdx.x * kThreads + threadIdx.x;
-  if (c >= p.n) return;
-  float s = 0;
-  for (int i = 0; i < p.cut.strips; ++i) s += p.db_part[(int64_t)i * p.n + c];
-  if (p.add) p.db_sum[c] = s;
-  if (p.db) p.db[c] = p.accumulate ? p.db[c] + s : s;
+  store_dw(p, n, k, left, s, p.add ? db_of(n) : 0.0f);
 }
 
 template <int TYPE, class S>
 void product(const WgradArgs& p, hipStream_t s) {
   const dim3 grid(p.cut.tiles_n * p.cut.tiles_k * p.cut.splits);
-  if (p.scale)
-    hipLaunchKernelGGL((k_wgrad<TYPE, true, S>), grid, dim3(kThreads), 0, s, p);
+  const bool sums = p.db || p.add;
+  if (p.scale && sums)
+    hipLaunchKernelGGL((k_wgrad<TYPE, true, true, S>), grid, dim3(kThreads), 0, s, p);
+  else if (p.scale)
+    hipLaunchKernelGGL((k_wgrad<TYPE, true, false, S>), grid, dim3(kThreads), 0, s, p);
+  else if (sums)
+    hipLaunchKernelGGL((k_wgrad<TYPE, false, true, S>), grid, dim3(kThreads), 0, s, p);
   else
-    hipLaunchKernelGGL((k_wgrad<TYPE, false, S>), grid, dim3(kThreads), 0, s, p);
+    hipLaunchKernelGGL((k_wgrad<TYPE, false, false, S>), grid, dim3(kThreads), 0, s, p);
 }
 
 template <int TYPE>
 ps_status product(const WgradArgs& p, hipStream_t s) {
-  if (p.db || p.add) {
-    const dim3 grid((p.n + 255) / 256, p.cut.strips);
-    if (p.cut.strips && p.n < 8)
-      hipLaunchKernelGGL((k_column_sums<TYPE, kShort>), grid, dim3(kThreads), 0, s, p);
-    else if (p.cut.strips)
-      hipLaunchKernelGGL((k_column_sums<TYPE, kPart>), grid, dim3(kThreads), 0, s, p);
-    if (ps_status st = hip_check(hipGetLastError(), "k_column_sums launch")) return st;
-    hipLaunchKernelGGL(k_column_join, dim3((p.n + kThreads - 1) / kThreads), dim3(kThreads), 0, s, p);
-    if (ps_status st = hip_check(hipGetLastError(), "k_column_join launch")) return st;
-  }
   switch (p.cut.kind) {
     case 0: product<TYPE, Large>(p, s); break;
     case 1: product<TYPE, Middle>(p, s); break;
@@ -453,8 +465,8 @@ ps_status product(const WgradArgs& p, hipStream_t s) {
   }
   if (ps_status st = hip_check(hipGetLastError(), "k_wgrad launch")) return st;
   if (p.cut.splits > 1) {
-    const int64_t size = (int64_t)p.n * ((p.k + 3) / 4);
-    hipLaunchKernelGGL(k_wgrad_join, dim3((uint32_t)((size + kThreads - 1) / kThreads)), dim3(kThreads), 0, s, p);
+    const int64_t lanes = (int64_t)p.n * ((p.k + 3) / 4) + (p.db ? p.n : 0);
+    hipLaunchKernelGGL(k_wgrad_join, dim3((uint32_t)((lanes + kThreads - 1) / kThreads)), dim3(kThreads), 0, s, p);
     return hip_check(hipGetLastError(), "k_wgrad_join launch");
   }
   return PS_OK;
@@ -470,14 +482,12 @@ WgradCut wgrad_cut(int64_t tokens, int64_t n, int64_t k) {
   c.tiles_n = (int32_t)((n + kN[c.kind] - 1) / kN[c.kind]);
   c.tiles_k = (int32_t)((k + kK[c.kind] - 1) / kK[c.kind]);
   const int64_t tiles = (int64_t)c.tiles_n * c.tiles_k;
-  // enough workgroups for the 256 compute units, but 256 tokens or more for each
+  // enough workgroups for the 256 compute units, but 128 tokens or more for each
   const int64_t want = tiles >= 256 ? 1 : (256 + tiles - 1) / tiles;
-  const int64_t most = tokens < 512 ? 1 : tokens / 256;
+  const int64_t most = tokens < 256 ? 1 : tokens / 128;
   c.splits = (int32_t)(want < most ? want : most);
   c.per_split = ((tokens + c.splits - 1) / c.splits + kStep - 1) / kStep * kStep;   // whole steps
   if (c.per_split) c.splits = (int32_t)((tokens + c.per_split - 1) / c.per_split);
-  c.per_strip = tokens < 64 * 64 ? 64 : (tokens + 63) / 64;
-  c.strips = (int32_t)((tokens + c.per_strip - 1) / c.per_strip);
   if (c.splits < 1) c.splits = 1;
   return c;
 }

@@ -179,16 +179,14 @@ int64_t norm_slots(const ps_block_norm& p) {
 
 size_t norm_workspace(const ps_block_norm& p) { return up256((size_t)norm_slots(p) * (size_t)p.cols * 3 * sizeof(float)); }
 
+// The splits' partial results and column sums; a product of one split needs no workspace.
 struct WgradLayout {
-  size_t part, db_part, db_sum, bytes;
+  size_t db_part, bytes;
 };
 WgradLayout wgrad_layout(const WgradCut& c, int64_t n, int64_t k) {
-  WgradLayout l;
-  l.part = 0;
-  l.db_part = up256(c.splits > 1 ? (size_t)c.splits * (size_t)n * (size_t)k * sizeof(float) : 0);
-  l.db_sum = l.db_part + up256((size_t)c.strips * (size_t)n * sizeof(float));
-  l.bytes = l.db_sum + up256((size_t)n * sizeof(float));
-  return l;
+  if (c.splits == 1) return {0, 0};
+  const size_t part = up256((size_t)c.splits * (size_t)n * (size_t)k * sizeof(float));
+  return {part, part + up256((size_t)c.splits * (size_t)n * sizeof(float))};
 }
 
 ps_status check_wgrad_shape(int64_t tokens, int64_t n, int64_t k) {
@@ -421,6 +419,7 @@ ps_status ps_linear_wgrad(const ps_linear_wgrad_args* args, ps_stream_t stream) 
   if (n == 0 || k == 0) return PS_OK;
   Arrays v;
   if (t) {
+    if (a.lddy > kMaxCols) return fail(PS_ERR_SHAPE, "lddy %lld is more than 2^24", (long long)a.lddy);
     v.add(a.dy, "dy", t, n, a.lddy, 2, false);
     v.codes(a.code, "code", t, k, false);
     if (a.scale) v.scales(a.scale, "scale", t, k, false);
@@ -431,9 +430,11 @@ ps_status ps_linear_wgrad(const ps_linear_wgrad_args* args, ps_stream_t stream) 
   v.optional(a.db, "db", 1, n, n, 4, true);
   const WgradCut cut = wgrad_cut(t, n, k);
   const WgradLayout l = wgrad_layout(cut, n, k);
-  if (a.workspace_bytes < l.bytes)
-    return fail(PS_ERR_WORKSPACE, "workspace has %zu bytes, %zu are needed", a.workspace_bytes, l.bytes);
-  v.add(a.workspace, "workspace", 1, (int64_t)(l.bytes / 16), (int64_t)(l.bytes / 16), 16, true);
+  if (l.bytes) {
+    if (a.workspace_bytes < l.bytes)
+      return fail(PS_ERR_WORKSPACE, "workspace has %zu bytes, %zu are needed", a.workspace_bytes, l.bytes);
+    v.add(a.workspace, "workspace", 1, (int64_t)(l.bytes / 16), (int64_t)(l.bytes / 16), 16, true);
+  }
   if (ps_status s = v.check()) return s;
   WgradArgs p = {};
   p.tokens = t;
@@ -449,9 +450,8 @@ ps_status ps_linear_wgrad(const ps_linear_wgrad_args* args, ps_stream_t stream) 
   p.lddw = a.lddw;
   p.db = a.db;
   char* ws = (char*)a.workspace;
-  p.part = (float*)(ws + l.part);
+  p.part = (float*)ws;
   p.db_part = (float*)(ws + l.db_part);
-  p.db_sum = (float*)(ws + l.db_sum);
   p.dy_type = a.dy_type;
   p.dw_type = a.dw_type;
   p.accumulate = a.accumulate;

@@ -89,8 +89,6 @@ struct WgradCut {
   int32_t tiles_n, tiles_k;
   int32_t splits;
   int64_t per_split;         // tokens, a multiple of the step
-  int32_t strips;            // column sums of dy: strips of tokens
-  int64_t per_strip;
 };
 WgradCut wgrad_cut(int64_t tokens, int64_t n, int64_t k);
 
@@ -106,8 +104,7 @@ struct WgradArgs {
   int64_t lddw;
   float* db;                 // the caller's, or NULL
   float* part;               // [splits][n][k], splits > 1
-  float* db_part;            // [strips][n]
-  float* db_sum;             // [n], if add is given
+  float* db_part;            // [splits][n], splits > 1
   int32_t dy_type, dw_type, accumulate;
   WgradCut cut;
 };

@@ -165,5 +165,7 @@ def test_refusals_of_the_binding(ps):
             ps.linear_wgrad(**a)
     with pytest.raises(ps.PSError, match="dy_type"):
         ps.linear_wgrad(dy.float(), code, w, scale=scale)
+    dy, code, scale, _ = inputs(1024, 8, 128, "bf16", True)      # tokens enough to be split
+    assert ps.linear_wgrad_workspace_size(1024, 8, 128) > 0
     with pytest.raises(ps.PSError, match="workspace"):
-        ps.linear_wgrad(dy, code, w, scale=scale, workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
+        ps.linear_wgrad(dy.cuda(), code, w, scale=scale, workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
