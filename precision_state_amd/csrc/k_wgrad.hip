@@ -176,14 +176,38 @@ __device__ __forceinline__ void store_dw(const WgradArgs& p, int n, int k, int l
   }
 }
 
+// Which tile a workgroup takes. Workgroups go to the XCDs in turn, each with an
+// L2 of its own; this gives the 32 of an XCD that run together (one to a compute
+// unit) eight by four neighbouring tiles, which share their rows of dy and codes.
+struct Tile {
+  int split, n, k;
+  __device__ __forceinline__ Tile(const WgradCut& c) {
+    constexpr int kGroup = 4;   // tiles of codes side by side
+    const uint32_t total = gridDim.x, wg = blockIdx.x, round = kXcdCount * 32;
+    uint32_t o = wg;
+    if (wg < total / round * round) {
+      o = xcd_item<32>(wg, total);
+    } else {   // the last round, as far as it can be shared out evenly
+      const uint32_t base = total / round * round, each = (total - base) / kXcdCount, i = wg - base;
+      if (i < each * kXcdCount) o = base + i % kXcdCount * each + i / kXcdCount;
+    }
+    const int tiles = c.tiles_n * c.tiles_k;
+    split = o / tiles;
+    o -= split * tiles;
+    const int group = o / (kGroup * c.tiles_n), wide = min(kGroup, c.tiles_k - group * kGroup);
+    o -= group * kGroup * c.tiles_n;
+    n = o / wide;
+    k = group * kGroup + o % wide;
+  }
+};
+
 // SUMS: the column sums of dy too, for db or add.
 template <int TYPE, bool SCALED, bool SUMS, class S>
 __global__ __launch_bounds__(kThreads, 1) void k_wgrad(WgradArgs p) {
   __shared__ __attribute__((aligned(16))) char lds[2 * S::BYTES];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  const int tiles = p.cut.tiles_n * p.cut.tiles_k;
-  const int split = blockIdx.x / tiles, tile = blockIdx.x % tiles;
-  const int n0 = tile % p.cut.tiles_n * S::N, k0 = tile / p.cut.tiles_n * S::K;
+  const Tile tile(p.cut);
+  const int split = tile.split, n0 = tile.n * S::N, k0 = tile.k * S::K;
   const int64_t first = (int64_t)split * p.cut.per_split;
   const int64_t end = min(first + p.cut.per_split, p.tokens);
   const int wn = wave / S::WK * (S::FN * 32), wk = wave % S::WK * (S::FK * 32);
