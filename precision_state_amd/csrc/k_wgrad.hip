@@ -201,6 +201,28 @@ struct Tile {
   }
 };
 
+// The order in which the instructions of 16 tokens are issued: between two matrix
+// instructions, whose 32 cycles leave room for seven others, a few conversions,
+// one read of the next fragments, and now and then a write and a load of the
+// tiles to come. One wave a SIMD issues one instruction every four cycles, so
+// what comes in a bunch leaves the matrix cores idle.
+template <class S, bool SCALED>
+__device__ __forceinline__ void interleave() {
+  constexpr int kMfma = S::FN * S::FK, kReads = 2 * S::FN + S::FK + (SCALED ? 2 : 0), kConvert = SCALED ? 16 : 4;
+  constexpr int kEach = (kReads + kMfma - 1) / kMfma;
+  __builtin_amdgcn_sched_group_barrier(0x2, kConvert, 0);
+#pragma unroll
+  for (int m = 0; m < kMfma; ++m) {
+    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);                                // a matrix instruction
+    __builtin_amdgcn_sched_group_barrier(0x100, kEach, 0);                          // reads
+    __builtin_amdgcn_sched_group_barrier(0x2, (kConvert + S::FN - 1) / S::FN, 0);   // vector instructions
+    if (m % 4 == 3) {
+      __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);                            // a write
+      __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);                             // a load
+    }
+  }
+}
+
 // SUMS: the column sums of dy too, for db or add.
 template <int TYPE, bool SCALED, bool SUMS, class S>
 __global__ __launch_bounds__(kThreads, 1) void k_wgrad(WgradArgs p) {
@@ -250,18 +272,18 @@ __global__ __launch_bounds__(kThreads, 1) void k_wgrad(WgradArgs p) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) sums[j] += v[j];
   };
-  // i-th part of as many as there are groups of 16 tokens: what was loaded goes to
-  // the buffer, and the same rows of the step after are loaded.
-  constexpr int U = S::STEP / 16;
+  // The i-th part of three: what was loaded goes to the buffer, and the same rows
+  // of the step after are loaded.
+  constexpr int U = S::STEP / 16, kParts = U - 1;
   auto renew = [&](char* buf, int part, int64_t t0, bool counts) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = part * kA / U; i < (part + 1) * kA / U; ++i) {
+    for (int i = part * kA / kParts; i < (part + 1) * kA / kParts; ++i) {
       *(u32x4*)(buf + to_a + i * kPassA * 2 * S::N) = ra[i];
       add_up(ra[i], counts);
       load_a(i, t0);
     }
 #pragma unroll
-    for (int i = part * kB / U; i < (part + 1) * kB / U; ++i) {
+    for (int i = part * kB / kParts; i < (part + 1) * kB / kParts; ++i) {
       if (has_b) *(u32x4*)(buf + to_b + i * kPassB * S::K) = rb[i];
       load_b(i, t0);
     }
@@ -339,10 +361,9 @@ __global__ __launch_bounds__(kThreads, 1) void k_wgrad(WgradArgs p) {
     for (int u = 0; u < U; ++u) {
       if (u + 1 == U) __syncthreads();
       read(u + 1 < U ? cur : nxt, (u + 1) % U * 16, (u + 1) & 1);
-      __builtin_amdgcn_sched_barrier(0);
       if (u + 1 < U) renew(nxt, u, later, more);
-      if (u + 2 == U) renew(nxt, u + 1, later, more);
       multiply(u & 1);
+      interleave<S, SCALED>();
       __builtin_amdgcn_sched_barrier(0);
     }
   };
@@ -354,7 +375,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_wgrad(WgradArgs p) {
     for (int i = 0; i < kB; ++i) load_b(i, first);
     load_s(first);
 #pragma unroll
-    for (int u = 0; u < U; ++u) renew(one, u, min(first + S::STEP, whole - S::STEP), true);
+    for (int u = 0; u < kParts; ++u) renew(one, u, min(first + S::STEP, whole - S::STEP), true);
     __syncthreads();
     read(one, 0, 0);
     int64_t t = first;
