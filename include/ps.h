@@ -638,7 +638,7 @@ ps_status ps_block_norm_backward(const ps_block_norm* norm, const ps_block_norm_
  * and sums are fp32, in an order that depends on the sizes only. dw of dw_type
  * (PS_TYPE_*) with distance lddw between rows; db float[out], NULL: not wanted;
  * mul, add float[in]. accumulate 1: dw and db are added to what the arrays
- * hold, in fp32, and rounded once. lddy <= 2^24. workspace as for a block norm's
+ * hold, in fp32, and rounded once. tokens <= 2^30, lddy <= 2^24. workspace as for a block norm's
  * backward call, ps_linear_wgrad_workspace_size bytes (0 of them: NULL). */
 typedef struct ps_linear_wgrad_args {
   int64_t tokens;

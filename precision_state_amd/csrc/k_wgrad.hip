@@ -20,20 +20,21 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 #define LOCAL __attribute__((address_space(3)))
 
-constexpr int kThreads = 256;  // four waves
+constexpr int kThreads = 256;   // of the join
 
-// Tiles of the result: rows (columns of dy) by columns (of z), how the four
-// waves share it, and the tokens in shared memory at a time.
+// Tiles of the result: rows (columns of dy) by columns (of z), how the waves share
+// it, and the tokens in shared memory at a time.
 template <int N_, int K_, int WN_, int WK_, int STEP_>
 struct Shape {
   static constexpr int N = N_, K = K_, WN = WN_, WK = WK_, STEP = STEP_;
   static constexpr int FN = N / WN / 32, FK = K / WK / 32;   // 32 x 32 results of a wave
-  static_assert(WN * WK == 4 && FN * WN * 32 == N && FK * WK * 32 == K, "four waves");
+  static constexpr int THREADS = 64 * WN * WK;
+  static_assert(FN * WN * 32 == N && FK * WK * 32 == K, "whole products");
   // one buffer of shared memory: dy, codes, scales [STEP][blocks of 128]
   static constexpr int KB = (K + kActBlock - 1) / kActBlock;
   static constexpr int DY = STEP * N * 2, CODE = STEP * K, BYTES = DY + CODE + STEP * KB * 4;
 };
-using Large = Shape<256, 256, 2, 2, 64>;
+using Large = Shape<256, 256, 2, 4, 64>;
 using Middle = Shape<128, 128, 2, 2, 64>;
 using FewRows = Shape<32, 256, 1, 4, 64>;
 using FewCols = Shape<256, 32, 4, 1, 64>;
@@ -94,6 +95,14 @@ __device__ __forceinline__ f32x16 mfma(s16x8 a, s16x8 b, f32x16 c) {
   if (TYPE == PS_TYPE_BF16)
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+// s and the sum of eight values, these added up first so that s takes few steps.
+template <int TYPE>
+__device__ __forceinline__ float add_eight(s16x8 a, float s) {
+  float v[8];
+  widen8<TYPE>(Raw8<TYPE>{{__builtin_bit_cast(u32x4, a)}}, Cols<kWhole>(0, 8), v);
+  return s + (((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7])));
 }
 
 // The 16 bytes from (t, at) of a matrix of `rows` rows of `width` bytes, `pitch`
@@ -201,49 +210,27 @@ struct Tile {
   }
 };
 
-// The order in which the instructions of 16 tokens are issued: between two matrix
-// instructions, whose 32 cycles leave room for seven others, a few conversions,
-// one read of the next fragments, and now and then a write and a load of the
-// tiles to come. One wave a SIMD issues one instruction every four cycles, so
-// what comes in a bunch leaves the matrix cores idle.
-template <class S, bool SCALED>
-__device__ __forceinline__ void interleave() {
-  constexpr int kMfma = S::FN * S::FK, kReads = 2 * S::FN + S::FK + (SCALED ? 2 : 0), kConvert = SCALED ? 16 : 4;
-  constexpr int kEach = (kReads + kMfma - 1) / kMfma;
-  __builtin_amdgcn_sched_group_barrier(0x2, kConvert, 0);
-#pragma unroll
-  for (int m = 0; m < kMfma; ++m) {
-    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);                                // a matrix instruction
-    __builtin_amdgcn_sched_group_barrier(0x100, kEach, 0);                          // reads
-    __builtin_amdgcn_sched_group_barrier(0x2, (kConvert + S::FN - 1) / S::FN, 0);   // vector instructions
-    if (m % 4 == 3) {
-      __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);                            // a write
-      __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);                             // a load
-    }
-  }
-}
-
 // SUMS: the column sums of dy too, for db or add.
 template <int TYPE, bool SCALED, bool SUMS, class S>
-__global__ __launch_bounds__(kThreads, 1) void k_wgrad(WgradArgs p) {
+__global__ __launch_bounds__(S::THREADS, S::THREADS / 256) void k_wgrad(WgradArgs p) {
   __shared__ __attribute__((aligned(16))) char lds[2 * S::BYTES];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const Tile tile(p.cut);
-  const int split = tile.split, n0 = tile.n * S::N, k0 = tile.k * S::K;
-  const int64_t first = (int64_t)split * p.cut.per_split;
-  const int64_t end = min(first + p.cut.per_split, p.tokens);
+  const int split = __builtin_amdgcn_readfirstlane(tile.split), n0 = __builtin_amdgcn_readfirstlane(tile.n) * S::N;
+  const int k0 = __builtin_amdgcn_readfirstlane(tile.k) * S::K;
+  const int tokens = (int)p.tokens, first = split * (int)p.cut.per_split, end = min(first + (int)p.cut.per_split, tokens);
   const int wn = wave / S::WK * (S::FN * 32), wk = wave % S::WK * (S::FK * 32);
   const int k_blocks = (p.k + kActBlock - 1) / kActBlock;
-  const int64_t safe = min(end, min(safe_rows(p.tokens, p.lddy * 2, n0 * 2, S::N * 2, p.n * 2),
-                                    safe_rows(p.tokens, p.k, k0, S::K, p.k)));
+  const int safe = min(end, (int)min(safe_rows(tokens, p.lddy * 2, n0 * 2, S::N * 2, p.n * 2),
+                                     safe_rows(tokens, p.k, k0, S::K, p.k)));
 
   // The next step's tiles on their way: registers between a load and a write. A
   // lane takes the same columns of every kPassA-th or kPassB-th row.
   constexpr int kRowA = S::N / 8, kRowB = S::K / 16;   // chunks of 16 bytes of a row
-  constexpr int kPassA = kThreads / kRowA, kPassB = kThreads / kRowB;
+  constexpr int kPassA = S::THREADS / kRowA, kPassB = S::THREADS / kRowB;
   constexpr int kA = (S::STEP + kPassA - 1) / kPassA, kB = (S::STEP + kPassB - 1) / kPassB;
   static_assert(kA * kPassA == S::STEP && (kB * kPassB == S::STEP || kB == 1), "whole passes");
-  static_assert(S::STEP * S::KB <= kThreads, "a scale for each lane at most");
+  static_assert(S::STEP * S::KB <= S::THREADS, "a scale for each lane at most");
   const int ta = threadIdx.x / kRowA, qa = threadIdx.x % kRowA, tb = threadIdx.x / kRowB, qb = threadIdx.x % kRowB;
   const bool has_b = kB * kPassB == S::STEP || tb < S::STEP;
   const uint32_t from_a = (uint32_t)ta * (uint32_t)(2 * p.lddy) + qa * 16, from_b = (uint32_t)tb * (uint32_t)p.k + qb * 16;
@@ -253,33 +240,24 @@ __global__ __launch_bounds__(kThreads, 1) void k_wgrad(WgradArgs p) {
   const bool has_s = SCALED && threadIdx.x < S::STEP * S::KB;
   u32x4 ra[kA], rb[kB];
   float rs = 0;
-  float sums[8] = {};
-  auto load_a = [&](int i, int64_t t0) __attribute__((always_inline)) {
-    const GLOBAL char* row = scalar_pointer((GLOBAL char*)p.dy + (t0 + i * kPassA) * (2 * p.lddy) + 2 * n0);
+  auto load_a = [&](int i, int t0) __attribute__((always_inline)) {
+    const GLOBAL char* row = scalar_pointer((GLOBAL char*)p.dy + (int64_t)(t0 + i * kPassA) * (2 * p.lddy) + 2 * n0);
     ra[i] = *(const GLOBAL u32x4_any*)(row + from_a);
   };
-  auto load_b = [&](int i, int64_t t0) __attribute__((always_inline)) {
-    const GLOBAL char* row = scalar_pointer((GLOBAL char*)p.code + (t0 + i * kPassB) * p.k + k0);
+  auto load_b = [&](int i, int t0) __attribute__((always_inline)) {
+    const GLOBAL char* row = scalar_pointer((GLOBAL char*)p.code + (int64_t)(t0 + i * kPassB) * p.k + k0);
     if (has_b) rb[i] = *(const GLOBAL u32x4_byte*)(row + from_b);
   };
-  auto load_s = [&](int64_t t0) __attribute__((always_inline)) {
-    if (has_s) rs = p.scale[(t0 + threadIdx.x / S::KB) * k_blocks + scale_block];
-  };
-  auto add_up = [&](const u32x4& w, bool counts) __attribute__((always_inline)) {
-    if (!SUMS) return;
-    float v[8];
-    widen8<TYPE>(Raw8<TYPE>{{w & (counts ? 0xFFFFFFFFu : 0u)}}, Cols<kWhole>(0, 8), v);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sums[j] += v[j];
+  auto load_s = [&](int t0) __attribute__((always_inline)) {
+    if (has_s) rs = p.scale[(int64_t)(t0 + (int)threadIdx.x / S::KB) * k_blocks + scale_block];
   };
   // The i-th part of three: what was loaded goes to the buffer, and the same rows
   // of the step after are loaded.
   constexpr int U = S::STEP / 16, kParts = U - 1;
-  auto renew = [&](char* buf, int part, int64_t t0, bool counts) __attribute__((always_inline)) {
+  auto renew = [&](char* buf, int part, int t0) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = part * kA / kParts; i < (part + 1) * kA / kParts; ++i) {
       *(u32x4*)(buf + to_a + i * kPassA * 2 * S::N) = ra[i];
-      add_up(ra[i], counts);
       load_a(i, t0);
     }
 #pragma unroll
@@ -293,13 +271,12 @@ __global__ __launch_bounds__(kThreads, 1) void k_wgrad(WgradArgs p) {
     }
   };
   // The same for a step at the end of the split or of the matrices.
-  auto load_and_place = [&](char* buf, int64_t t0) __attribute__((always_inline)) {
+  auto load_and_place = [&](char* buf, int t0) __attribute__((always_inline)) {
 #pragma unroll 1
     for (int i = 0; i < kA; ++i) {
       const int64_t t = t0 + i * kPassA + ta;
       const u32x4 w = load16_guarded((const char*)p.dy, t, t < end ? p.tokens : 0, 2 * p.lddy, 2 * n0 + qa * 16, 2 * p.n);
       *(u32x4*)(buf + to_a + i * kPassA * 2 * S::N) = w;
-      add_up(w, true);
     }
 #pragma unroll 1
     for (int i = 0; i < kB; ++i) {
@@ -320,6 +297,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_wgrad(WgradArgs p) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
 
+  float sums[S::FN] = {};   // of a lane's column, over its half of the tokens
   s16x8 a[2][S::FN];
   i32x2 b[2][S::FK];
   f32x4 sc[2][2];
@@ -346,24 +324,27 @@ __global__ __launch_bounds__(kThreads, 1) void k_wgrad(WgradArgs p) {
 #pragma unroll
       for (int i = 0; i < S::FN; ++i) acc[i][j] = mfma<TYPE>(a[from][i], v, acc[i][j]);
     }
+    if (SUMS) {
+#pragma unroll
+      for (int i = 0; i < S::FN; ++i) sums[i] = add_eight<TYPE>(a[from][i], sums[i]);
+    }
   };
 
   // Two buffers: while one is multiplied the other is filled with the tiles that
-  // were loaded a step before. The fragments of 16 tokens are read ahead of the
-  // matrix instructions that use them, the first ones of a step before the last
-  // 16 tokens of the step before are multiplied. The last steps load and place
-  // the last tiles again, so that no branch cuts a step.
-  const int64_t whole = first + (safe > first ? (safe - first) / S::STEP * S::STEP : 0);
-  auto step = [&](char* cur, char* nxt, int64_t t) __attribute__((always_inline)) {
-    const int64_t later = min(t + 2 * S::STEP, whole - S::STEP);
-    const bool more = t + S::STEP < whole;
+  // were loaded a step before. The fragments of 16 tokens are read ahead of the matrix instructions that use them, the first ones of a
+  // step before the last 16 tokens of the step before are multiplied. The last
+  // steps load and place the last tiles again, so that no branch cuts a step.
+  const int whole = __builtin_amdgcn_readfirstlane(first + (safe > first ? (safe - first) / S::STEP * S::STEP : 0));
+  const int last = whole - S::STEP;
+  auto step = [&](char* cur, char* nxt, int t) __attribute__((always_inline)) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (u + 1 == U) __syncthreads();
       read(u + 1 < U ? cur : nxt, (u + 1) % U * 16, (u + 1) & 1);
-      if (u + 1 < U) renew(nxt, u, later, more);
+      if (u + 1 < U) renew(nxt, u, min(t + 2 * S::STEP, last));
+      __builtin_amdgcn_s_setprio(1);
       multiply(u & 1);
-      interleave<S, SCALED>();
+      __builtin_amdgcn_s_setprio(0);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
@@ -375,17 +356,17 @@ __global__ __launch_bounds__(kThreads, 1) void k_wgrad(WgradArgs p) {
     for (int i = 0; i < kB; ++i) load_b(i, first);
     load_s(first);
 #pragma unroll
-    for (int u = 0; u < kParts; ++u) renew(one, u, min(first + S::STEP, whole - S::STEP), true);
+    for (int u = 0; u < kParts; ++u) renew(one, u, min(first + S::STEP, last));
     __syncthreads();
     read(one, 0, 0);
-    int64_t t = first;
+    int t = first;
     for (; t + S::STEP < whole; t += 2 * S::STEP) {
       step(one, two, t);
       step(two, one, t + S::STEP);
     }
     if (t < whole) step(one, two, t);
   }
-  for (int64_t t = whole; t < end; t += S::STEP) {
+  for (int t = whole; t < end; t += S::STEP) {
     __syncthreads();
     load_and_place(lds, t);
     __syncthreads();
@@ -399,21 +380,21 @@ __global__ __launch_bounds__(kThreads, 1) void k_wgrad(WgradArgs p) {
   // Result e of a 32 x 32 product is row 8 (e / 4) + 4 (lane / 32) + e % 4, column
   // lane % 32. A wave's 32 rows go through its part of shared memory, so that
   // rows are stored four columns a lane.
-  constexpr int kCols = S::FK * 32, kLanes = kCols / 4;
-  static_assert(4 * 32 * kCols * 4 + S::N * 4 <= 2 * S::BYTES, "a part for each wave, and the column sums");
+  constexpr int kSide = S::FK < 2 ? S::FK : 2, kCols = kSide * 32, kLanes = kCols / 4;   // products side by side
+  static_assert(S::THREADS / 64 * 32 * kCols * 4 + S::N * 4 <= 2 * S::BYTES, "a part for each wave, and the column sums");
   float* part = (float*)lds + wave * (32 * kCols);
-  float* db = (float*)(lds + 2 * S::BYTES) - S::N;
+  float* db = (float*)(lds + 2 * S::BYTES) - S::N;   // behind the parts
   if (SUMS) {
-    float* rows = (float*)lds;   // [kPassA][N]
-    static_assert(kPassA * S::N * 4 + S::N * 4 <= 2 * S::BYTES, "a row for each pass");
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) rows[ta * S::N + qa * 8 + j] = sums[j];
+    for (int i = 0; i < S::FN; ++i) {
+      const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(sums[i]), __float_as_uint(sums[i]), false, false);
+      const float s = __uint_as_float(x[0]) + __uint_as_float(x[1]);
+      if (wave % S::WK == 0 && lane < 32) db[wn + i * 32 + lane] = s;
+    }
     __syncthreads();
     if (threadIdx.x < S::N) {
-      float s = rows[threadIdx.x];
-      for (int i = 1; i < kPassA; ++i) s += rows[i * S::N + threadIdx.x];
-      db[threadIdx.x] = s;
+      const float s = db[threadIdx.x];
       const int n = n0 + threadIdx.x;
       if (k0 == 0 && n < p.n) {
         if (p.cut.splits > 1)
@@ -424,17 +405,18 @@ __global__ __launch_bounds__(kThreads, 1) void k_wgrad(WgradArgs p) {
     }
   }
 #pragma unroll
-  for (int i = 0; i < S::FN; ++i) {
+  for (int x = 0; x < S::FN * S::FK / kSide; ++x) {
+    const int i = x % S::FN, j0 = x / S::FN * kSide;
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < S::FK; ++j)
+    for (int j = 0; j < kSide; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e)
-        part[(8 * (e / 4) + 4 * (lane / 32) + e % 4) * kCols + j * 32 + lane % 32] = acc[i][j][e];
+        part[(8 * (e / 4) + 4 * (lane / 32) + e % 4) * kCols + j * 32 + lane % 32] = acc[i][j0 + j][e];
     __syncthreads();
 #pragma unroll 1
     for (int c = lane; c < 32 * kLanes; c += 64) {
-      const int row = wn + i * 32 + c / kLanes, n = n0 + row, k = k0 + wk + c % kLanes * 4;
+      const int row = wn + i * 32 + c / kLanes, n = n0 + row, k = k0 + wk + j0 * 32 + c % kLanes * 4;
       if (n >= p.n) break;
       const f32x4 v = *(const f32x4*)(part + c * 4);
       if (p.cut.splits > 1) {
@@ -491,13 +473,13 @@ void product(const WgradArgs& p, hipStream_t s) {
   const dim3 grid(p.cut.tiles_n * p.cut.tiles_k * p.cut.splits);
   const bool sums = p.db || p.add;
   if (p.scale && sums)
-    hipLaunchKernelGGL((k_wgrad<TYPE, true, true, S>), grid, dim3(kThreads), 0, s, p);
+    hipLaunchKernelGGL((k_wgrad<TYPE, true, true, S>), grid, dim3(S::THREADS), 0, s, p);
   else if (p.scale)
-    hipLaunchKernelGGL((k_wgrad<TYPE, true, false, S>), grid, dim3(kThreads), 0, s, p);
+    hipLaunchKernelGGL((k_wgrad<TYPE, true, false, S>), grid, dim3(S::THREADS), 0, s, p);
   else if (sums)
-    hipLaunchKernelGGL((k_wgrad<TYPE, false, true, S>), grid, dim3(kThreads), 0, s, p);
+    hipLaunchKernelGGL((k_wgrad<TYPE, false, true, S>), grid, dim3(S::THREADS), 0, s, p);
   else
-    hipLaunchKernelGGL((k_wgrad<TYPE, false, false, S>), grid, dim3(kThreads), 0, s, p);
+    hipLaunchKernelGGL((k_wgrad<TYPE, false, false, S>), grid, dim3(S::THREADS), 0, s, p);
 }
 
 template <int TYPE>

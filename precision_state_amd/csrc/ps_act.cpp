@@ -190,7 +190,7 @@ WgradLayout wgrad_layout(const WgradCut& c, int64_t n, int64_t k) {
 }
 
 ps_status check_wgrad_shape(int64_t tokens, int64_t n, int64_t k) {
-  if (tokens < 0 || tokens > kMaxRows) return fail(PS_ERR_SHAPE, "tokens %lld out of range", (long long)tokens);
+  if (tokens < 0 || tokens > (int64_t(1) << 30)) return fail(PS_ERR_SHAPE, "tokens %lld out of range", (long long)tokens);
   if (n < 0 || n > kMaxCols) return fail(PS_ERR_SHAPE, "out_features %lld out of range", (long long)n);
   if (k < 0 || k > kMaxCols) return fail(PS_ERR_SHAPE, "in_features %lld out of range", (long long)k);
   if (n * k > (int64_t(1) << 36)) return fail(PS_ERR_SHAPE, "out_features * in_features is more than 2^36");
