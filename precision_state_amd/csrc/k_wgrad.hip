@@ -7,11 +7,14 @@
 // column, which is what a matrix instruction takes, and the codes become bf16
 // or fp16 between that read and the instruction, in the shadow of the matrix
 // instructions before.
+#include <type_traits>
+
 #include "dev_act.h"
 
 namespace ps {
 namespace {
 
+typedef __bf16 bf16pair __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef int i32x2 __attribute__((ext_vector_type(2)));
@@ -97,12 +100,20 @@ __device__ __forceinline__ f32x16 mfma(s16x8 a, s16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-// s and the sum of eight values, these added up first so that s takes few steps.
+// s and the sum of eight values, two to an instruction (products with 1 in fp32).
 template <int TYPE>
 __device__ __forceinline__ float add_eight(s16x8 a, float s) {
-  float v[8];
-  widen8<TYPE>(Raw8<TYPE>{{__builtin_bit_cast(u32x4, a)}}, Cols<kWhole>(0, 8), v);
-  return s + (((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7])));
+  const u32x4 w = __builtin_bit_cast(u32x4, a);
+  float r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t pair = w[i];
+    if (TYPE == PS_TYPE_BF16)
+      r[i] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16pair, pair), __builtin_bit_cast(bf16pair, 0x3F803F80u), i & 1 ? r[i - 1] : 0.0f, false);
+    else
+      r[i] = __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, pair), __builtin_bit_cast(f16x2, 0x3C003C00u), i & 1 ? r[i - 1] : 0.0f, false);
+  }
+  return s + (r[1] + r[3]);
 }
 
 // The 16 bytes from (t, at) of a matrix of `rows` rows of `width` bytes, `pitch`
@@ -230,14 +241,14 @@ __global__ __launch_bounds__(S::THREADS, S::THREADS / 256) void k_wgrad(WgradArg
   constexpr int kPassA = S::THREADS / kRowA, kPassB = S::THREADS / kRowB;
   constexpr int kA = (S::STEP + kPassA - 1) / kPassA, kB = (S::STEP + kPassB - 1) / kPassB;
   static_assert(kA * kPassA == S::STEP && (kB * kPassB == S::STEP || kB == 1), "whole passes");
-  static_assert(S::STEP * S::KB <= S::THREADS, "a scale for each lane at most");
+  static_assert(S::THREADS % (S::STEP * S::KB) == 0, "every scale taken as often");
   const int ta = threadIdx.x / kRowA, qa = threadIdx.x % kRowA, tb = threadIdx.x / kRowB, qb = threadIdx.x % kRowB;
   const bool has_b = kB * kPassB == S::STEP || tb < S::STEP;
   const uint32_t from_a = (uint32_t)ta * (uint32_t)(2 * p.lddy) + qa * 16, from_b = (uint32_t)tb * (uint32_t)p.k + qb * 16;
   const int to_a = chunk_at<2 * S::N, 64>(ta, qa), to_b = S::DY + chunk_at<S::K, 32>(tb, qb);
-  const int scale_block = min(k0 / kActBlock + (int)threadIdx.x % S::KB, k_blocks - 1);
-  const int to_s = S::DY + S::CODE + (threadIdx.x % S::KB * S::STEP + threadIdx.x / S::KB) * 4;
-  const bool has_s = SCALED && threadIdx.x < S::STEP * S::KB;
+  // a scale for each lane; those too many take the same ones again, which costs less than a branch
+  const int ts = (int)threadIdx.x % (S::STEP * S::KB) / S::KB, qs = threadIdx.x % S::KB;
+  const int scale_block = min(k0 / kActBlock + qs, k_blocks - 1), to_s = S::DY + S::CODE + (qs * S::STEP + ts) * 4;
   u32x4 ra[kA], rb[kB];
   float rs = 0;
   auto load_a = [&](int i, int t0) __attribute__((always_inline)) {
@@ -249,7 +260,7 @@ __global__ __launch_bounds__(S::THREADS, S::THREADS / 256) void k_wgrad(WgradArg
     if (has_b) rb[i] = *(const GLOBAL u32x4_byte*)(row + from_b);
   };
   auto load_s = [&](int t0) __attribute__((always_inline)) {
-    if (has_s) rs = p.scale[(int64_t)(t0 + (int)threadIdx.x / S::KB) * k_blocks + scale_block];
+    if (SCALED) rs = p.scale[(int64_t)(t0 + ts) * k_blocks + scale_block];
   };
   // The i-th part of three: what was loaded goes to the buffer, and the same rows
   // of the step after are loaded.
@@ -266,7 +277,7 @@ __global__ __launch_bounds__(S::THREADS, S::THREADS / 256) void k_wgrad(WgradArg
       load_b(i, t0);
     }
     if (part == 0) {
-      if (has_s) *(float*)(buf + to_s) = rs;
+      if (SCALED) *(float*)(buf + to_s) = rs;
       load_s(t0);
     }
   };
@@ -285,8 +296,8 @@ __global__ __launch_bounds__(S::THREADS, S::THREADS / 256) void k_wgrad(WgradArg
         *(u32x4*)(buf + to_b + i * kPassB * S::K) =
             load16_guarded((const char*)p.code, t, t < end ? p.tokens : 0, p.k, k0 + qb * 16, p.k);
     }
-    const int64_t t = t0 + threadIdx.x / S::KB;
-    if (has_s) *(float*)(buf + to_s) = t < end ? p.scale[t * k_blocks + scale_block] : 0.0f;
+    const int64_t t = t0 + ts;
+    if (SCALED) *(float*)(buf + to_s) = t < end ? p.scale[t * k_blocks + scale_block] : 0.0f;
   };
 
   f32x16 acc[S::FN][S::FK];
@@ -298,9 +309,10 @@ __global__ __launch_bounds__(S::THREADS, S::THREADS / 256) void k_wgrad(WgradArg
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
 
   float sums[S::FN] = {};   // of a lane's column, over its half of the tokens
-  s16x8 a[2][S::FN];
-  i32x2 b[2][S::FK];
-  f32x4 sc[2][2];
+  constexpr int kSets = SCALED ? 1 : 2;   // of fragments: with the scales two of them leave too few registers
+  s16x8 a[kSets][S::FN];
+  i32x2 b[kSets][S::FK];
+  f32x4 sc[2];
   auto read = [&](const char* buf, int u, int to) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < S::FN; ++i) a[to][i] = dy_fragment<S::N>(buf, u, wn + i * 32, lane);
@@ -308,15 +320,17 @@ __global__ __launch_bounds__(S::THREADS, S::THREADS / 256) void k_wgrad(WgradArg
     for (int j = 0; j < S::FK; ++j) b[to][j] = code_fragment<S::K>(buf + S::DY, u, wk + j * 32, lane);
     if (SCALED) {
       const float* s = (const float*)(buf + S::DY + S::CODE) + wk / kActBlock * S::STEP + u + lane / 32 * 8;
-      sc[to][0] = *(const f32x4*)s;
-      sc[to][1] = *(const f32x4*)(s + 4);
+      sc[0] = *(const f32x4*)s;
+      sc[1] = *(const f32x4*)(s + 4);
     }
   };
-  auto multiply = [&](int from) __attribute__((always_inline)) {
+  // Only the tiles at the first columns add up dy, or all if each needs the sums.
+  const bool adds = SUMS && (k0 == 0 || (p.add && p.cut.splits == 1));
+  auto multiply = [&](int from, auto sum) __attribute__((always_inline)) {
     float s[8];
     if (SCALED) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[i] = sc[from][i / 4][i % 4];
+      for (int i = 0; i < 8; ++i) s[i] = sc[i / 4][i % 4];
     }
 #pragma unroll
     for (int j = 0; j < S::FK; ++j) {
@@ -324,7 +338,7 @@ __global__ __launch_bounds__(S::THREADS, S::THREADS / 256) void k_wgrad(WgradArg
 #pragma unroll
       for (int i = 0; i < S::FN; ++i) acc[i][j] = mfma<TYPE>(a[from][i], v, acc[i][j]);
     }
-    if (SUMS) {
+    if (decltype(sum)::value) {
 #pragma unroll
       for (int i = 0; i < S::FN; ++i) sums[i] = add_eight<TYPE>(a[from][i], sums[i]);
     }
@@ -336,19 +350,21 @@ __global__ __launch_bounds__(S::THREADS, S::THREADS / 256) void k_wgrad(WgradArg
   // steps load and place the last tiles again, so that no branch cuts a step.
   const int whole = __builtin_amdgcn_readfirstlane(first + (safe > first ? (safe - first) / S::STEP * S::STEP : 0));
   const int last = whole - S::STEP;
-  auto step = [&](char* cur, char* nxt, int t) __attribute__((always_inline)) {
+  auto step = [&](char* cur, char* nxt, int t, auto sum) __attribute__((always_inline)) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (u + 1 == U) __syncthreads();
-      read(u + 1 < U ? cur : nxt, (u + 1) % U * 16, (u + 1) & 1);
+      if (kSets == 1) read(cur, u * 16, 0);
+      if (kSets == 2 && u + 1 == U) __syncthreads();
+      if (kSets == 2) read(u + 1 < U ? cur : nxt, (u + 1) % U * 16, (u + 1) & 1);
       if (u + 1 < U) renew(nxt, u, min(t + 2 * S::STEP, last));
       __builtin_amdgcn_s_setprio(1);
-      multiply(u & 1);
+      multiply(kSets == 1 ? 0 : u & 1, sum);
       __builtin_amdgcn_s_setprio(0);
+      if (kSets == 1 && u + 1 == U) __syncthreads();
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  if (first < whole) {
+  auto steps = [&](auto sum) __attribute__((always_inline)) {
     char *one = lds, *two = lds + S::BYTES;
 #pragma unroll
     for (int i = 0; i < kA; ++i) load_a(i, first);
@@ -358,13 +374,19 @@ __global__ __launch_bounds__(S::THREADS, S::THREADS / 256) void k_wgrad(WgradArg
 #pragma unroll
     for (int u = 0; u < kParts; ++u) renew(one, u, min(first + S::STEP, last));
     __syncthreads();
-    read(one, 0, 0);
+    if (kSets == 2) read(one, 0, 0);
     int t = first;
     for (; t + S::STEP < whole; t += 2 * S::STEP) {
-      step(one, two, t);
-      step(two, one, t + S::STEP);
+      step(one, two, t, sum);
+      step(two, one, t + S::STEP, sum);
     }
-    if (t < whole) step(one, two, t);
+    if (t < whole) step(one, two, t, sum);
+  };
+  if (first < whole) {
+    if (adds)
+      steps(std::integral_constant<bool, SUMS>());
+    else
+      steps(std::false_type());
   }
   for (int t = whole; t < end; t += S::STEP) {
     __syncthreads();
@@ -373,7 +395,7 @@ __global__ __launch_bounds__(S::THREADS, S::THREADS / 256) void k_wgrad(WgradArg
 #pragma unroll 1
     for (int u = 0; u < S::STEP; u += 16) {
       read(lds, u, 0);
-      multiply(0);
+      multiply(0, std::integral_constant<bool, SUMS>());
     }
   }
 
