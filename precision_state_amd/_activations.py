@@ -34,7 +34,7 @@ def _matrix(x, name, shape, dtype, device):
     """Pointer and distance between rows."""
     if x is None:
         return None, 0
-    if x.shape != shape or x.dtype != dtype or x.device != device:
+    if x.shape != shape or x.dtype is not dtype or x.device != device:
         raise ValueError(f"{name} is {x.dtype} {tuple(x.shape)} on {x.device}, not {dtype} {tuple(shape)} on {device}")
     row, col = x.stride()
     if col != 1 and shape[1] > 1:
@@ -57,6 +57,8 @@ _F32 = (torch.float32,)
 
 
 def _code(code, scale, name, shape, device):
+    if code is None and scale is None:
+        return None, None
     return (_whole(code, f"{name}code", shape, _E4M3_DTYPES, device),
             _whole(scale, f"{name}scale", (shape[0], (shape[1] + ACT_BLOCK - 1) // ACT_BLOCK), _F32, device))
 
@@ -132,11 +134,14 @@ def glu_backward(dout, act, a_code, a_scale, da, b_code=None, b_scale=None, db=N
                                     po, ldo, _raw_stream(device, stream)))
 
 
-@dataclass
+@dataclass(frozen=True)
 class BlockNorm:
     """What a block norm is made of (see ps_block_norm in include/ps.h). The vectors have one dtype; gate, and mul and
     add together, are [cols], or [segments, cols] with a vector for each. segments: int32 tensor on the device, where
-    each of the batch's packed sequences starts, and where the last one ends."""
+    each of the batch's packed sequences starts, and where the last one ends.
+
+    The vectors are checked at the first call, and from then on their memory is kept alive by a reference of the norm's
+    own; their values are read at every call. Other vectors need another norm (dataclasses.replace)."""
     pre_norm: int = NORM_RMS
     pre_eps: float = 1e-6
     post_norm: int = NORM_NONE
@@ -150,7 +155,18 @@ class BlockNorm:
     mul_plus_one: bool = False
     segments: object = None
 
-    def c(self, rows, cols, dtype, device):
+    def _record(self, rows, cols, dtype, device):
+        """A record of the call's own: two threads may use one norm."""
+        made = self.__dict__.get("_made")
+        if made is None or made[0] != (cols, dtype, device):
+            made = (cols, dtype, device), bytes(self._make(cols, dtype, device)), \
+                [v.untyped_storage() for v in (self.post_weight, self.gate, self.mul, self.add, self.segments) if v is not None]
+            object.__setattr__(self, "_made", made)
+        rec = CBlockNorm.from_buffer_copy(made[1])
+        rec.rows = rows
+        return rec
+
+    def _make(self, cols, dtype, device):
         segs = 0 if self.segments is None else self.segments.numel() - 1
         flags, vec, ptr = NORM_MUL_PLUS_ONE if self.mul_plus_one else 0, None, []
         for name, v, by_seg in (("post_weight", self.post_weight, 0), ("gate", self.gate, NORM_GATE_BY_SEG),
@@ -169,7 +185,7 @@ class BlockNorm:
         if self.mul is not None and self.add is not None and self.mul.dim() != self.add.dim():
             raise ValueError("mul and add have different shapes")
         starts = _whole(self.segments, "segments", (segs + 1,), (torch.int32,), device)
-        return CBlockNorm(rows, cols, starts, *ptr, self.post_eps, self.pre_eps, self.residual_scale, self.branch_scale,
+        return CBlockNorm(0, cols, starts, *ptr, self.post_eps, self.pre_eps, self.residual_scale, self.branch_scale,
                           _TYPES[dtype], _TYPES[vec or torch.float32], self.post_norm, self.pre_norm, segs, flags)
 
 
@@ -180,7 +196,7 @@ def block_norm_forward(norm: BlockNorm, x, n, y=None, h=None, h_code=None, h_rst
     (ps_block_norm_forward)."""
     shape, dtype, device = _like(x, "x")
     _needed(n=n)
-    rec = norm.c(shape[0], shape[1], dtype, device)
+    rec = norm._record(shape[0], shape[1], dtype, device)
     hc, _ = _code(h_code, None, "h_", shape, device)
     yc, ys = _code(y_code, y_scale, "y_", shape, device)
     io = CBlockNormFwd(*_matrix(x, "x", shape, dtype, device), *_matrix(y, "y", shape, dtype, device),
@@ -208,7 +224,7 @@ def block_norm_backward(norm: BlockNorm, dn, h_code, h_rstd, dx, dh=None, dy=Non
     None for one of the call's own."""
     _needed(h_code=h_code, h_rstd=h_rstd, dx=dx)
     shape, dtype, device = _like(dn, "dn")
-    rec = norm.c(shape[0], shape[1], dtype, device)
+    rec = norm._record(shape[0], shape[1], dtype, device)
     hc, _ = _code(h_code, None, "h_", shape, device)
     yc, ys = _code(y_code, y_scale, "y_", shape, device)
     grads = []

@@ -104,114 +104,96 @@ __device__ __forceinline__ void activation(float a, float& f, float& slope) {
   slope = __builtin_fmaf(f * (1.0f - q), du, q);
 }
 
-template <int TYPE, int ACT, bool GATED, bool SAVE, int END, int K>
+template <int TYPE, int ACT, bool GATED, bool SAVE, int END>
 __global__ __launch_bounds__(kThreads) void k_glu_forward(ActGrid g, GluArgs t) {
-  Raw8<TYPE> ra[K], rb[K];
+  const uint32_t u = unit_of(0, 1);
+  const Place<END> p(g, u);
+  const Raw8<TYPE> ra = load8<TYPE>(row_of<TYPE>(t.a, p.row, t.lda), p.c);
+  float a[8], b[8], o[8], s;
+  if (GATED) widen8<TYPE>(load8<TYPE>(row_of<TYPE>(t.b, p.row, t.ldb), p.c), p.c, b);
+  widen8<TYPE>(ra, p.c, a);
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const Place<END> p(g, unit_of(k, K));
-    ra[k] = load8<TYPE>(row_of<TYPE>(t.a, p.row, t.lda), p.c);
-    if (GATED) rb[k] = load8<TYPE>(row_of<TYPE>(t.b, p.row, t.ldb), p.c);
+  for (int j = 0; j < 8; ++j) {
+    float slope;
+    activation<ACT>(a[j], o[j], slope);
+    if (GATED) o[j] *= b[j];
   }
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const uint32_t u = unit_of(k, K);
-    const Place<END> p(g, u);
-    float a[8], b[8], o[8], s;
-    widen8<TYPE>(ra[k], p.c, a);
-    if (GATED) widen8<TYPE>(rb[k], p.c, b);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float slope;
-      activation<ACT>(a[j], o[j], slope);
-      if (GATED) o[j] *= b[j];
-    }
-    store8<TYPE>(row_of<TYPE>(t.out, p.row, t.ldo), p.col, p.to_store(), o);
-    if (SAVE) {
-      const bool writes = p.in && (threadIdx.x & 15) == 0;
-      const u32x2_any c = encode_block(a, s);
-      store_codes8(codes_of(t.a_code, p.row, g.cols), p.col, p.to_store(), c);
-      if (writes) t.a_scale[u] = s;
-      if (GATED) {
-        const u32x2_any d = encode_block(b, s);
-        store_codes8(codes_of(t.b_code, p.row, g.cols), p.col, p.to_store(), d);
-        if (writes) t.b_scale[u] = s;
-      }
-    }
-  }
+  store8<TYPE>(row_of<TYPE>(t.out, p.row, t.ldo), p.col, p.to_store(), o);
+  if (!SAVE) return;
+  const bool writes = p.in && (threadIdx.x & 15) == 0;
+  const u32x2_any c = encode_block(a, s);
+  store_codes8(codes_of(t.a_code, p.row, g.cols), p.col, p.to_store(), c);
+  if (writes) t.a_scale[u] = s;
+  if (!GATED) return;
+  const u32x2_any d = encode_block(b, s);
+  store_codes8(codes_of(t.b_code, p.row, g.cols), p.col, p.to_store(), d);
+  if (writes) t.b_scale[u] = s;
 }
 
-template <int TYPE, int ACT, bool GATED, int END, int K>
+template <int TYPE, int ACT, bool GATED, int END>
 __global__ __launch_bounds__(kThreads) void k_glu_backward(ActGrid g, GluArgs t) {
-  Raw8<TYPE> rd[K];
-  u32x2_any ca[K], cb[K];
-  float sa[K], sb[K];
+  const uint32_t u = unit_of(0, 1);
+  const Place<END> p(g, u);
+  const uint32_t at = p.in ? u : g.units - 1;
+  const Raw8<TYPE> rd = load8<TYPE>(row_of<TYPE>(t.dout, p.row, t.ldd), p.c);
+  const u32x2_any ca = load_codes8(codes_of(t.a_code, p.row, g.cols), p.c);
+  const float sa = t.a_scale[at];
+  float d[8], a[8], b[8], da[8], db[8], o[8], sb;
+  if (GATED) {
+    const u32x2_any cb = load_codes8(codes_of(t.b_code, p.row, g.cols), p.c);
+    sb = t.b_scale[at];
+    codes_to_f32(cb, p.c, b);
+  }
+  widen8<TYPE>(rd, p.c, d);
+  codes_to_f32(ca, p.c, a);
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const uint32_t u = unit_of(k, K);
-    const Place<END> p(g, u);
-    rd[k] = load8<TYPE>(row_of<TYPE>(t.dout, p.row, t.ldd), p.c);
-    ca[k] = load_codes8(codes_of(t.a_code, p.row, g.cols), p.c);
-    const uint32_t at = p.in ? u : g.units - 1;
-    sa[k] = t.a_scale[at];
+  for (int j = 0; j < 8; ++j) {
+    float f, slope;
+    activation<ACT>(a[j] * sa, f, slope);
     if (GATED) {
-      cb[k] = load_codes8(codes_of(t.b_code, p.row, g.cols), p.c);
-      sb[k] = t.b_scale[at];
+      const float v = b[j] * sb;
+      db[j] = d[j] * f;
+      da[j] = d[j] * v * slope;
+      o[j] = f * v;
+    } else {
+      da[j] = d[j] * slope;
+      o[j] = f;
     }
   }
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const Place<END> p(g, unit_of(k, K));
-    float d[8], a[8], b[8], da[8], db[8], o[8];
-    widen8<TYPE>(rd[k], p.c, d);
-    codes_to_f32(ca[k], p.c, a);
-    if (GATED) codes_to_f32(cb[k], p.c, b);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float f, slope;
-      activation<ACT>(a[j] * sa[k], f, slope);
-      if (GATED) {
-        const float v = b[j] * sb[k];
-        db[j] = d[j] * f;
-        da[j] = d[j] * v * slope;
-        o[j] = f * v;
-      } else {
-        da[j] = d[j] * slope;
-        o[j] = f;
-      }
-    }
-    store8<TYPE>(row_of<TYPE>(t.da, p.row, t.lda), p.col, p.to_store(), da);
-    if (GATED) store8<TYPE>(row_of<TYPE>(t.db, p.row, t.ldb), p.col, p.to_store(), db);
-    if (t.out) store8<TYPE>(row_of<TYPE>(t.out, p.row, t.ldo), p.col, p.to_store(), o);
-  }
+  store8<TYPE>(row_of<TYPE>(t.da, p.row, t.lda), p.col, p.to_store(), da);
+  if (GATED) store8<TYPE>(row_of<TYPE>(t.db, p.row, t.ldb), p.col, p.to_store(), db);
+  if (t.out) store8<TYPE>(row_of<TYPE>(t.out, p.row, t.ldo), p.col, p.to_store(), o);
 }
 
 dim3 grid_of(const ActGrid& g, int k) { return dim3((g.units + kTeams * k - 1) / (kTeams * k)); }
 
-// Blocks on a lane: two, so that four to six loads are under way at a time.
-constexpr int K = 2;
+// The codec's lanes have a part of two blocks (16384 x 12288 bf16 encoded in 93 us;
+// with one block 105, with four 97), those of the activations, which have two to
+// three streams more, of one (8192 x 11008 gated, forward 118 us and backward 143;
+// with two blocks 122 and 151, with four 124 and 156).
+constexpr int kCodecBlocks = 2;
 
 template <int TYPE, int ACT, int END>
 ps_status glu_forward(const ActGrid& g, const GluArgs& p, hipStream_t s) {
   const bool save = p.a_code != nullptr;
-  const dim3 grid = grid_of(g, K), wg(kThreads);
+  const dim3 grid = grid_of(g, 1), wg(kThreads);
   if (p.b && save)
-    hipLaunchKernelGGL((k_glu_forward<TYPE, ACT, true, true, END, K>), grid, wg, 0, s, g, p);
+    hipLaunchKernelGGL((k_glu_forward<TYPE, ACT, true, true, END>), grid, wg, 0, s, g, p);
   else if (p.b)
-    hipLaunchKernelGGL((k_glu_forward<TYPE, ACT, true, false, END, K>), grid, wg, 0, s, g, p);
+    hipLaunchKernelGGL((k_glu_forward<TYPE, ACT, true, false, END>), grid, wg, 0, s, g, p);
   else if (save)
-    hipLaunchKernelGGL((k_glu_forward<TYPE, ACT, false, true, END, K>), grid, wg, 0, s, g, p);
+    hipLaunchKernelGGL((k_glu_forward<TYPE, ACT, false, true, END>), grid, wg, 0, s, g, p);
   else
-    hipLaunchKernelGGL((k_glu_forward<TYPE, ACT, false, false, END, K>), grid, wg, 0, s, g, p);
+    hipLaunchKernelGGL((k_glu_forward<TYPE, ACT, false, false, END>), grid, wg, 0, s, g, p);
   return hip_check(hipGetLastError(), "k_glu_forward launch");
 }
 
 template <int TYPE, int ACT, int END>
 ps_status glu_backward(const ActGrid& g, const GluArgs& p, hipStream_t s) {
   if (p.b_code)
-    hipLaunchKernelGGL((k_glu_backward<TYPE, ACT, true, END, K>), grid_of(g, K), dim3(kThreads), 0, s, g, p);
+    hipLaunchKernelGGL((k_glu_backward<TYPE, ACT, true, END>), grid_of(g, 1), dim3(kThreads), 0, s, g, p);
   else
-    hipLaunchKernelGGL((k_glu_backward<TYPE, ACT, false, END, K>), grid_of(g, K), dim3(kThreads), 0, s, g, p);
+    hipLaunchKernelGGL((k_glu_backward<TYPE, ACT, false, END>), grid_of(g, 1), dim3(kThreads), 0, s, g, p);
   return hip_check(hipGetLastError(), "k_glu_backward launch");
 }
 
@@ -243,22 +225,22 @@ ps_status glu(bool forward, const ActGrid& g, int type, int act, const GluArgs& 
 
 template <int TYPE>
 ps_status encode(const ActGrid& g, const void* x, int64_t ld, uint8_t* code, float* scale, hipStream_t s) {
-  const dim3 grid = grid_of(g, K), wg(kThreads);
+  const dim3 grid = grid_of(g, kCodecBlocks), wg(kThreads);
   switch (end_of(g.cols)) {
-    case kWhole: hipLaunchKernelGGL((k_encode_act<TYPE, kWhole, K>), grid, wg, 0, s, g, x, ld, code, scale); break;
-    case kPart: hipLaunchKernelGGL((k_encode_act<TYPE, kPart, K>), grid, wg, 0, s, g, x, ld, code, scale); break;
-    default: hipLaunchKernelGGL((k_encode_act<TYPE, kShort, K>), grid, wg, 0, s, g, x, ld, code, scale); break;
+    case kWhole: hipLaunchKernelGGL((k_encode_act<TYPE, kWhole, kCodecBlocks>), grid, wg, 0, s, g, x, ld, code, scale); break;
+    case kPart: hipLaunchKernelGGL((k_encode_act<TYPE, kPart, kCodecBlocks>), grid, wg, 0, s, g, x, ld, code, scale); break;
+    default: hipLaunchKernelGGL((k_encode_act<TYPE, kShort, kCodecBlocks>), grid, wg, 0, s, g, x, ld, code, scale); break;
   }
   return hip_check(hipGetLastError(), "k_encode_act launch");
 }
 
 template <int TYPE>
 ps_status decode(const ActGrid& g, const uint8_t* code, const float* scale, void* x, int64_t ld, hipStream_t s) {
-  const dim3 grid = grid_of(g, K), wg(kThreads);
+  const dim3 grid = grid_of(g, kCodecBlocks), wg(kThreads);
   switch (end_of(g.cols)) {
-    case kWhole: hipLaunchKernelGGL((k_decode_act<TYPE, kWhole, K>), grid, wg, 0, s, g, code, scale, x, ld); break;
-    case kPart: hipLaunchKernelGGL((k_decode_act<TYPE, kPart, K>), grid, wg, 0, s, g, code, scale, x, ld); break;
-    default: hipLaunchKernelGGL((k_decode_act<TYPE, kShort, K>), grid, wg, 0, s, g, code, scale, x, ld); break;
+    case kWhole: hipLaunchKernelGGL((k_decode_act<TYPE, kWhole, kCodecBlocks>), grid, wg, 0, s, g, code, scale, x, ld); break;
+    case kPart: hipLaunchKernelGGL((k_decode_act<TYPE, kPart, kCodecBlocks>), grid, wg, 0, s, g, code, scale, x, ld); break;
+    default: hipLaunchKernelGGL((k_decode_act<TYPE, kShort, kCodecBlocks>), grid, wg, 0, s, g, code, scale, x, ld); break;
   }
   return hip_check(hipGetLastError(), "k_decode_act launch");
 }

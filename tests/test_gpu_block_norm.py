@@ -1,4 +1,5 @@
 """GPU tests of the block norms against 64 bits (act_ref)."""
+import dataclasses
 import math
 
 import pytest
@@ -237,7 +238,7 @@ def test_odd_segment_offsets_stay_inside(ps):
     """Offsets outside the rows, or out of order, read and write nothing that is not the call's."""
     t = Case(ps, rows=40, cols=136, starts=[0, 20, 40], post="rms", **ADA)
     for bad in ([-5, 20, 90], [30, 10, 40], [1 << 30, 5, 3], [40, 0, 0], [-1, -1, -1]):
-        t.norm.segments = torch.tensor(bad, dtype=torch.int32).cuda()
+        t.norm = dataclasses.replace(t.norm, segments=torch.tensor(bad, dtype=torch.int32).cuda())
         t.forward().backward()
         assert all(m.outside_is_untouched() for m in (t.o["n"], t.o["h"], t.dx, t.dy))
 
@@ -277,7 +278,7 @@ def test_refusals_of_the_binding(ps):
     for change, says in ((dict(gate=torch.ones(3, 64).cuda().bfloat16()), "gate"), (dict(mul=torch.ones(64).cuda()), "mul"),
                          (dict(post_weight=torch.ones(65).cuda().bfloat16()), "post_weight"), (dict(mul=torch.ones(64).bfloat16()), "mul"),
                          (dict(segments=torch.zeros(2, dtype=torch.int64).cuda()), "segments")):
-        norm = ps.BlockNorm(**{**t.norm.__dict__, **change})
+        norm = dataclasses.replace(t.norm, **change)
         with pytest.raises(ValueError, match=says):
             ps.block_norm_forward(norm, x, n, y=x.clone(), h=n.clone())
     with pytest.raises(ValueError, match="d_add"):
