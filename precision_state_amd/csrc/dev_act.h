@@ -48,14 +48,15 @@ __device__ __forceinline__ u32x4 shift_down(u32x4 w, int n) {
 // (kPart), where a lane with fewer than eight loads the row's last eight, which
 // widen8 moves into place, so that every lane loads alike: no branch around a
 // load, and no lane whose row ends costs more; or before eight (kShort), loaded
-// one by one.
-enum { kWhole = 0, kPart = 1, kShort = 2 };
+// one by one. kEvery is for rows of which every lane of the team has eight.
+enum { kWhole = 0, kPart = 1, kShort = 2, kEvery = 3 };
 inline int end_of(int cols) { return cols < 8 ? kShort : cols % 8 ? kPart : kWhole; }
 template <int END>
 struct Cols {
   int left, start;
   __device__ __forceinline__ Cols(int col, int cols)
-      : left(cols - col), start(END == kShort ? col : __builtin_elementwise_min(col, cols - 8)) {}
+      : left(END == kEvery ? 8 : cols - col),
+        start(END == kShort || END == kEvery ? col : __builtin_elementwise_min(col, cols - 8)) {}
 };
 
 template <int TYPE, bool STREAM = true, int END>

@@ -215,6 +215,12 @@ __device__ __forceinline__ void back_sums(const NormArgs& p, int kind, float r, 
   c = r * (s[0] * p.inv_cols);
 }
 
+// A value that all lanes loaded alike, in a scalar register: its vector register
+// is free for the next row's.
+__device__ __forceinline__ float uniform(float v) {
+  return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(v)));
+}
+
 // What the backward pass finds of the branch: nothing saved, its values (a gate
 // without a norm), or its normalised ones.
 enum { kNoBranch = 0, kPlain = 1, kNormed = 2 };
@@ -226,6 +232,16 @@ enum { kNoBranch = 0, kPlain = 1, kNormed = 2 };
 // whose barriers the load's latency would otherwise add to; a segment's vectors
 // stay in registers, since a load behind those of the next row would wait for
 // them. The widest rows (V > 1) leave no registers for either.
+// Waits for a load count what was issued behind it, the fewest over all ways
+// there, so a branch around a later load or store makes them waits for nearly
+// everything. Rows of a multiple of 512 columns (kEvery) have no such branch:
+// no lane is without columns, an absent dh reads dn's first row instead and is
+// taken as zeros. 16384 x 4096 with both norms 123 -> 120 us.
+// It reaches 5.6 TB/s there and 4.7 with 9216 x 5120 and a gate, where one
+// workgroup of ten waves fills a compute unit (registers): the sums' barrier is
+// what both wait for. Not kept: two rows loaded ahead (9216 x 5120 100 -> 101
+// us), five waves to a SIMD (registers spill, 45 to 70% slower), strips of half
+// the rows (5% slower).
 template <int TYPE, int V, int SAVED, int END>
 __global__ __launch_bounds__(V == 1 ? 1024 : 512) void k_norm_backward(NormArgs p) {
   constexpr bool kAhead = V == 1;
@@ -239,7 +255,6 @@ __global__ __launch_bounds__(V == 1 ? 1024 : 512) void k_norm_backward(NormArgs 
   const int last = p.seg_start ? min(p.rows - first, p.strip) + first : p.rows;
   const int64_t n_part = (int64_t)p.slots * p.cols;
   const int blocks = (p.cols + kActBlock - 1) / kActBlock;
-  const bool branch = p.dy != nullptr;
 
   for (int row = first; row < last;) {
     int seg = 0, end = last;
@@ -299,8 +314,7 @@ __global__ __launch_bounds__(V == 1 ? 1024 : 512) void k_norm_backward(NormArgs 
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const Cols<END> c((v * nt + lane) * 8, p.cols);
-        dh[v] = Raw8<TYPE>{};
-        if (p.dh) dh[v] = load8<TYPE>(scalar_pointer(row_of<TYPE>(p.dh, r, p.lddh)), c);
+        dh[v] = load8<TYPE>(scalar_pointer(p.dh ? row_of<TYPE>(p.dh, r, p.lddh) : row_of<TYPE>(p.dn, 0, 0)), c);
         if (SAVED != kNoBranch) cy[v] = load_codes8(scalar_pointer(codes_of(p.y_code, r, p.cols)), c);
         if (SAVED == kPlain) ys[v] = p.y_scale[(int64_t)r * blocks + min((v * nt + lane) * 8, p.cols - 1) / kActBlock];
       }
@@ -337,7 +351,7 @@ __global__ __launch_bounds__(V == 1 ? 1024 : 512) void k_norm_backward(NormArgs 
           g[v][j] *= km[v][j];
         }
       }
-      const float r1 = h_rstd;
+      const float r1 = uniform(h_rstd);
       if (kAhead) load_first(ahead);
       back_sums<V>(p, p.pre, r1, sum, g, z, c, d);
 #pragma unroll
@@ -346,6 +360,10 @@ __global__ __launch_bounds__(V == 1 ? 1024 : 512) void k_norm_backward(NormArgs 
         const Cols<END> c8(col, p.cols);
         float o[8];
         widen8<TYPE>(dh[v], c8, o);
+        if (!p.dh) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) o[j] = 0.0f;
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           g[v][j] = __builtin_fmaf(-c, z[v][j], __builtin_fmaf(r1, g[v][j], o[j] - d));
@@ -361,9 +379,9 @@ __global__ __launch_bounds__(V == 1 ? 1024 : 512) void k_norm_backward(NormArgs 
           }
         }
       }
-      const float r2 = y_rstd;
+      const float r2 = uniform(y_rstd);
       if (kAhead) load_second(ahead);
-      if (!branch) continue;
+      if (SAVED == kNoBranch && !p.dy) continue;
 #pragma unroll
       for (int v = 0; v < V; ++v)
 #pragma unroll
@@ -481,7 +499,9 @@ ps_status backward(const NormArgs& p, hipStream_t s) {
   constexpr int kWideEnd = END == kShort ? kPart : END;
   const int lanes = (p.cols + 7) / 8;
   const dim3 grid((p.rows + p.strip - 1) / p.strip);
-  if (lanes <= 1024)
+  if (lanes <= 1024 && lanes % 64 == 0 && END == kWhole)
+    hipLaunchKernelGGL((k_norm_backward<TYPE, 1, SAVED, kEvery>), grid, dim3(lanes), 0, s, p);
+  else if (lanes <= 1024)
     hipLaunchKernelGGL((k_norm_backward<TYPE, 1, SAVED, END>), grid, dim3(waves_for(lanes, 1) * 64), 0, s, p);
   else if (lanes <= 1536)
     hipLaunchKernelGGL((k_norm_backward<TYPE, 3, SAVED, kWideEnd>), grid, dim3(waves_for(lanes, 3) * 64), 0, s, p);
