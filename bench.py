@@ -26,6 +26,10 @@ Reported:
              tensors of the set for the NAdam step, here and in the
              per-tensor and offload modes; the whole double block for the
              factored step; 2^24 elements for the standalone kernels)
+
+`--mode` selects other workloads; `--mode activations` steps a feed-forward
+block with 8-bit activation checkpoints (its figures are bf16 tokens/s and each
+kernel's time alone).
 """
 import argparse
 import hashlib
@@ -947,6 +951,110 @@ def bench_elementwise(args):
         "cpu_baseline": baseline}), flush=True)
 
 
+def bench_activations(args):
+    """One training step of a gated feed-forward block whose activations are saved in 8 bits: norm, gate and up
+    products, SiLU, down product, the norms around the residual sum, and back, with the weight gradients taken from the
+    codes (bf16, random weights and inputs). Products with weights are the library's; every other kernel is this one's,
+    timed alone too."""
+    import torch
+
+    import precision_state_amd as ps
+    dev, t, c, f = "cuda:0", args.tokens, args.width, args.hidden
+    gen = torch.Generator(device=dev).manual_seed(args.seed)
+
+    def rand(*s, scale=1.0):
+        return torch.randn(*s, device=dev, generator=gen).mul_(scale).bfloat16()
+
+    def mat(*s, dtype=torch.bfloat16):
+        return torch.empty(*s, dtype=dtype, device=dev)
+
+    def saved(cols):
+        return mat(t, cols, dtype=torch.float8_e4m3fn), mat(t, -(-cols // ps.ACT_BLOCK), dtype=torch.float32)
+
+    w1, post, w2 = (1 + 0.1 * rand(c) for _ in range(3))
+    wgu, wd = rand(2 * f, c, scale=c ** -0.5), rand(c, f, scale=f ** -0.5)
+    before, after = ps.BlockNorm(mul=w1), ps.BlockNorm(post_norm=ps.NORM_RMS, post_weight=post, mul=w2)
+    mul1 = w1.float()
+    x, dn, dh = rand(t, c), rand(t, c, scale=0.01), rand(t, c, scale=0.01)
+    (xc, _), (yc, _), (hc, _), a8, b8, o8 = saved(c), saved(c), saved(c), saved(f), saved(f), saved(f)
+    xr, yr, hr = (mat(t, dtype=torch.float32) for _ in range(3))
+    n, h, n2, dx, dy, dx1, out, gu, dgu = mat(t, c), mat(t, c), mat(t, c), mat(t, c), mat(t, c), mat(t, c), mat(t, f), \
+        mat(t, 2 * f), mat(t, 2 * f)
+    dwgu, dwd = mat(2 * f, c, dtype=torch.float32), mat(c, f, dtype=torch.float32)
+    dw1, dpost, dw2 = (mat(c, dtype=torch.float32) for _ in range(3))
+    room = torch.empty(max(ps.block_norm_workspace_size(after, t, c), ps.linear_wgrad_workspace_size(t, 2 * f, c),
+                           ps.linear_wgrad_workspace_size(t, c, f), 16), dtype=torch.uint8, device=dev)
+    v = {"y": rand(t, c), "do": rand(t, f, scale=0.01), "dnx": rand(t, c, scale=0.01)}
+    block = 4 * (-(-f // ps.ACT_BLOCK))
+    kernels = {   # call, bytes that it cannot do without, flops (matrix products)
+        "norm_forward": (lambda: ps.block_norm_forward(before, x, n, h_code=xc, h_rstd=xr), t * (5 * c + 4), 0),
+        "glu_forward": (lambda: ps.glu_forward(gu[:, :f], out, ps.ACT_SILU, *a8, b=gu[:, f:], b_code=b8[0], b_scale=b8[1]),
+                        t * (8 * f + 2 * block), 0),
+        "norms_forward": (lambda: ps.block_norm_forward(after, x, n2, y=v["y"], h=h, h_code=hc, h_rstd=hr, y_code=yc,
+                                                        y_rstd=yr), t * (10 * c + 8), 0),
+        "norms_backward": (lambda: ps.block_norm_backward(after, dn, hc, hr, dx, dh=dh, dy=dy, y_code=yc, y_rstd=yr,
+                                                          d_post_weight=dpost, d_mul=dw2, workspace=room), t * (10 * c + 8), 0),
+        "glu_backward": (lambda: ps.glu_backward(v["do"], ps.ACT_SILU, *a8, dgu[:, :f], b_code=b8[0], b_scale=b8[1],
+                                                 db=dgu[:, f:], out=out), t * (10 * f + 2 * block), 0),
+        "encode": (lambda: ps.encode_act(out, *o8), t * (3 * f + block), 0),
+        "wgrad_down": (lambda: ps.linear_wgrad(dy, o8[0], dwd, scale=o8[1], workspace=room), 0, 2 * t * c * f),
+        "wgrad_gate_up": (lambda: ps.linear_wgrad(dgu, xc, dwgu, mul=mul1, workspace=room), 0, 4 * t * c * f),
+        "norm_backward": (lambda: ps.block_norm_backward(before, v["dnx"], xc, xr, dx1, dh=dx, d_mul=dw1, workspace=room),
+                          t * (7 * c + 4), 0),
+    }
+    run = {k: fn for k, (fn, _, _) in kernels.items()}
+
+    def step():
+        run["norm_forward"]()
+        torch.mm(n, wgu.t(), out=gu)
+        run["glu_forward"]()
+        torch.mm(out, wd.t(), out=v["y"])
+        run["norms_forward"]()
+        run["norms_backward"]()
+        torch.mm(dy, wd, out=v["do"])
+        run["glu_backward"]()
+        run["encode"]()
+        run["wgrad_down"]()
+        run["wgrad_gate_up"]()
+        torch.mm(dgu, wgu, out=v["dnx"])
+        run["norm_backward"]()
+
+    stream = torch.cuda.current_stream()
+
+    def timed(fn, steps):
+        torch.cuda.synchronize()
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record(stream)
+        for _ in range(steps):
+            fn()
+        b.record(stream)
+        torch.cuda.synchronize()
+        return a.elapsed_time(b) / steps
+
+    for _ in range(args.warmup):
+        step()
+    ms = timed(step, args.steps)
+    res = {}
+    for k, (fn, nbytes, flops) in kernels.items():
+        fn()
+        one = timed(fn, args.steps)
+        res[k] = {"ms": one, **({"tflops": flops / one / 1e9} if flops else {"bytes": nbytes, "gbs": nbytes / one / 1e6})}
+        log(f"[bench] {k}: {one:.4f} ms, " + (f"{flops / one / 1e9:.0f} TFLOP/s" if flops else f"{nbytes / one / 1e6:.0f} GB/s"))
+    log(f"[bench] step: {ms:.3f} ms, of it {sum(r['ms'] for r in res.values()):.3f} ms in this library's kernels")
+    worst = min((k for k in res if "gbs" in res[k]), key=lambda k: res[k]["gbs"])
+    # what one token keeps from the forward to the backward pass: codes and scales, against bf16 of the same values
+    kept = {"8 bit": 3 * c + 12 + 2 * (f + block), "bf16": 2 * (3 * c + 2 * f)}
+    print(json.dumps({
+        "metric": "feed-forward block with 8-bit activation checkpoints: tokens/s of forward and backward with weight "
+                  "gradients", "value": t / (ms * 1e-3), "unit": "tokens/s", "n_gpus": 1, "steps": args.steps,
+        "warmup": args.warmup, "ms_per_step": ms, "higher_is_better": True, "scaling": "weak", "vs_baseline": None,
+        "dtype": "bf16", "data": "synthetic",
+        "config": {"tokens": t, "width": c, "hidden": f, "kernels": res, "bytes_kept_per_token": kept,
+                   "gpu_clocks_after_timing": gpu_clocks()},
+        "roofline": {"bound": "hbm", "achieved": res[worst]["gbs"], "peak": PEAK_HBM_GBS, "unit": "GB/s",
+                     "frac": res[worst]["gbs"] / PEAK_HBM_GBS, "traffic": None, "kernel": worst}}), flush=True)
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -963,11 +1071,16 @@ def main():
                     help="offload mode: distinct pinned host state sets, reused cyclically by the 57 blocks")
     ap.add_argument("--elements", type=int, default=1 << 30,
                     help="elementwise mode: array length")
-    ap.add_argument("--mode", default="nadam", choices=["nadam", "factored", "offload", "per_tensor", "elementwise"],
+    ap.add_argument("--mode", default="nadam",
+                    choices=["nadam", "factored", "offload", "per_tensor", "elementwise", "activations"],
                     help="nadam: the fused (N)AdamW step (headline); factored: the Adafactor-style step "
                          "(factored second moment, update clipping; --beta1, --decay-rate) on the double-block "
                          "shapes; offload: host-resident state over PCIe; per_tensor: one call per tensor, as a "
-                         "gradient hook would step; elementwise: the standalone split/join/encode/decode kernels")
+                         "gradient hook would step; elementwise: the standalone split/join/encode/decode kernels; "
+                         "activations: a feed-forward block's training step with 8-bit activation checkpoints")
+    ap.add_argument("--tokens", type=int, default=8192, help="activations mode: rows of the block's input")
+    ap.add_argument("--width", type=int, default=4096, help="activations mode: columns of the residual stream")
+    ap.add_argument("--hidden", type=int, default=11008, help="activations mode: width of the feed-forward layer")
     ap.add_argument("--offload-mode", default="direct", choices=["direct", "staged"],
                     help="offload mode: the step kernel on the host arrays in place over PCIe (direct) or copies "
                          "through two device staging slots (staged)")
@@ -1021,6 +1134,8 @@ def main():
         return bench_per_tensor(args)
     if args.mode == "elementwise":
         return bench_elementwise(args)
+    if args.mode == "activations":
+        return bench_activations(args)
     shapes = synth.WORKLOADS[args.workload]()
     n_params = synth.total_params(shapes)
     log(f"[bench] {args.workload}: {len(shapes)} tensors, {n_params} params; generating state on {dev}")
