@@ -532,7 +532,7 @@ ps_status ps_glu_backward(int64_t rows, int64_t cols, int32_t type, int32_t act,
  *                rows seg_start[b] .. seg_start[b + 1] - 1 (it may be empty).
  *                Rows of no segment are left as they are in every output and
  *                in no sum. NULL (n_segs 0): all rows are one segment
- * eps >= 0, scales finite; cols <= PS_NORM_MAX_COLS. vec_type: PS_TYPE_* of the
+ * eps >= 0, scales finite; rows <= 2^30, cols <= PS_NORM_MAX_COLS. vec_type: PS_TYPE_* of the
  * four vectors. */
 enum { PS_NORM_NONE = 0, PS_NORM_RMS = 1, PS_NORM_LAYER = 2 };
 enum { PS_NORM_GATE_BY_SEG = 1u << 0, PS_NORM_MOD_BY_SEG = 1u << 1, PS_NORM_MUL_PLUS_ONE = 1u << 2 };
@@ -583,8 +583,9 @@ typedef struct ps_block_norm_fwd {
 
 /* Backward arrays: the gradients dn of n and dh of h from elsewhere (NULL: 0)
  * are read with what the forward pass saved; dx and, with a branch, dy are
- * written (dy NULL: there is none, and the branch's gradients are not made). dx or dy may be dh or dn
- * itself. With xh, yh the decoded values and G the whole gradient of h:
+ * written (dy NULL: there is none, and the branch's gradients are not made).
+ * dx or dy may be dh or dn itself. With xh, yh the decoded values and G the
+ * whole gradient of h:
  *   G  = dh + back(dn * m, xh, h_rstd);  dx = residual_scale * G
  *   p  = branch_scale * G;  dy = back(p * gate * post_weight, yh, y_rstd), or
  *   p * gate with no post_norm
@@ -638,8 +639,9 @@ ps_status ps_block_norm_backward(const ps_block_norm* norm, const ps_block_norm_
  * and sums are fp32, in an order that depends on the sizes only. dw of dw_type
  * (PS_TYPE_*) with distance lddw between rows; db float[out], NULL: not wanted;
  * mul, add float[in]. accumulate 1: dw and db are added to what the arrays
- * hold, in fp32, and rounded once. tokens <= 2^30, lddy <= 2^24. workspace as for a block norm's
- * backward call, ps_linear_wgrad_workspace_size bytes (0 of them: NULL). */
+ * hold, in fp32, and rounded once. tokens <= 2^30, lddy <= 2^24,
+ * out_features * in_features <= 2^36. workspace as for a block norm's backward
+ * call, ps_linear_wgrad_workspace_size bytes (0 of them: NULL). */
 typedef struct ps_linear_wgrad_args {
   int64_t tokens;
   int64_t out_features;

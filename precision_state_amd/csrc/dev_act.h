@@ -20,6 +20,13 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
+// A grid dimension holds less than 2^32 lanes: `n` workgroups, and those that fill
+// up the last of its rows, numbered blockIdx.y * gridDim.x + blockIdx.x < 2^31.
+inline dim3 grid_2d(uint32_t n) {
+  constexpr uint32_t kMost = 1u << 20;
+  return n <= kMost ? dim3(n) : dim3(kMost, (n + kMost - 1) / kMost);
+}
+
 __device__ __forceinline__ uint32_t div_by(uint32_t u, const FastDiv& f) { return (uint32_t)(((uint64_t)u * f.m) >> f.s); }
 
 // Eight values of a row as they lie in memory.

@@ -37,7 +37,7 @@ struct Place {
 };
 
 __device__ __forceinline__ uint32_t unit_of(int k, int per) {
-  return (blockIdx.x * per + k) * (uint32_t)kTeams + threadIdx.x / 16;
+  return ((blockIdx.y * gridDim.x + blockIdx.x) * per + k) * (uint32_t)kTeams + threadIdx.x / 16;
 }
 
 template <int TYPE, int END, int K>
@@ -165,7 +165,7 @@ __global__ __launch_bounds__(kThreads) void k_glu_backward(ActGrid g, GluArgs t)
   if (t.out) store8<TYPE>(row_of<TYPE>(t.out, p.row, t.ldo), p.col, p.to_store(), o);
 }
 
-dim3 grid_of(const ActGrid& g, int k) { return dim3((g.units + kTeams * k - 1) / (kTeams * k)); }
+dim3 grid_of(const ActGrid& g, int k) { return grid_2d((g.units + kTeams * k - 1) / (kTeams * k)); }
 
 // The codec's lanes have a part of two blocks (16384 x 12288 bf16 encoded in 93 us;
 // with one block 105, with four 97), those of the activations, which have two to

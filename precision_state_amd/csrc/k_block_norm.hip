@@ -104,7 +104,8 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_forward(NormArgs p) 
   __shared__ float lds[2][kMostWaves][2];
   const int nt = WAVE ? 64 : blockDim.x, lane = WAVE ? threadIdx.x & 63 : threadIdx.x;
   TeamSum sum{lds, nt / 64};
-  const int row = WAVE ? __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + threadIdx.x / 64) : blockIdx.x;
+  const int group = blockIdx.y * gridDim.x + blockIdx.x;
+  const int row = WAVE ? __builtin_amdgcn_readfirstlane(group * 4 + threadIdx.x / 64) : group;
   if (row >= p.rows) return;   // whole teams leave
   int seg = 0;
   if (p.seg_start) {
@@ -136,7 +137,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void k_norm_forward(NormArgs p) 
     for (int v = 0; v < V; ++v) {
       const int col = (v * nt + lane) * 8;
       const Cols<END> c8(col, p.cols);
-        if (p.y_code) {
+      if (p.y_code) {
         u32x2_any c;
         if (p.post != PS_NORM_NONE) {
           c = pack_codes(z[v]);
@@ -474,13 +475,13 @@ int waves_for(int lanes, int v) { return (lanes + 64 * v - 1) / (64 * v); }
 template <int TYPE, int END>
 ps_status forward(const NormArgs& p, hipStream_t s) {
   const int lanes = (p.cols + 7) / 8;
-  const dim3 four((p.rows + 3) / 4);
+  const dim3 four = grid_2d((p.rows + 3) / 4);
   if (END == kShort || lanes <= 64)
     hipLaunchKernelGGL((k_norm_forward<TYPE, 1, true, END>), four, dim3(256), 0, s, p);
   else if (lanes <= 128)
     hipLaunchKernelGGL((k_norm_forward<TYPE, 2, true, END == kShort ? kPart : END>), four, dim3(256), 0, s, p);
   else
-    hipLaunchKernelGGL((k_norm_forward<TYPE, 2, false, END == kShort ? kPart : END>), dim3(p.rows),
+    hipLaunchKernelGGL((k_norm_forward<TYPE, 2, false, END == kShort ? kPart : END>), grid_2d(p.rows),
                        dim3(waves_for(lanes, 2) * 64), 0, s, p);
   return hip_check(hipGetLastError(), "k_norm_forward launch");
 }

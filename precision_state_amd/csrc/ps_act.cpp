@@ -9,6 +9,7 @@ using namespace ps;
 namespace {
 
 constexpr int64_t kMaxRows = 0x7FFFFFFF, kMaxCols = int64_t(1) << 24, kMaxUnits = 0x7FFFFFFF;
+constexpr int64_t kMaxNormRows = int64_t(1) << 30;   // a row and a step of the grid stay below 2^31
 constexpr size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
 int size_of(int32_t type) { return type == PS_TYPE_F32 ? 4 : 2; }
@@ -128,6 +129,7 @@ ps_status check_norm(const ps_block_norm* p) {
   if (!is_finite(p->residual_scale) || !is_finite(p->branch_scale))
     return fail(PS_ERR_INVALID_ARG, "residual_scale and branch_scale must be finite");
   if (ps_status s = check_shape(p->rows, p->cols)) return s;
+  if (p->rows > kMaxNormRows) return fail(PS_ERR_SHAPE, "rows %lld is more than 2^30", (long long)p->rows);
   if (p->cols > PS_NORM_MAX_COLS)
     return fail(PS_ERR_UNSUPPORTED, "cols %lld is more than %d", (long long)p->cols, PS_NORM_MAX_COLS);
   if (p->n_segs < 0 || p->n_segs > 65535) return fail(PS_ERR_SHAPE, "n_segs %d is not in 0..65535", p->n_segs);
