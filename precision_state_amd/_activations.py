@@ -134,7 +134,7 @@ def glu_backward(dout, act, a_code, a_scale, da, b_code=None, b_scale=None, db=N
                                     po, ldo, _raw_stream(device, stream)))
 
 
-@dataclass(frozen=True)
+@dataclass(frozen=True, eq=False)
 class BlockNorm:
     """What a block norm is made of (see ps_block_norm in include/ps.h). The vectors have one dtype; gate, and mul and
     add together, are [cols], or [segments, cols] with a vector for each. segments: int32 tensor on the device, where
@@ -165,6 +165,10 @@ class BlockNorm:
         rec = CBlockNorm.from_buffer_copy(made[1])
         rec.rows = rows
         return rec
+
+    def __getstate__(self):
+        """Without the record: a copy's vectors lie elsewhere."""
+        return {k: v for k, v in self.__dict__.items() if k != "_made"}
 
     def _make(self, cols, dtype, device):
         segs = 0 if self.segments is None else self.segments.numel() - 1

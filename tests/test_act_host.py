@@ -275,3 +275,31 @@ def test_a_call_with_every_array_is_checked_whole(ps):
     every = dict(d_gate=43 * M, d_add=44 * M)
     for at in (M, 5 * M, 9 * M, 40 * M, 41 * M, 42 * M, 43 * M, 44 * M):
         _refused(ps, 1, _bwd(ps, rec, workspace=at, **every), "overlap")
+
+
+def test_norm_rows_have_a_limit(ps):
+    rec = ps.CBlockNorm(rows=(1 << 30) + 1, cols=1, type=1, vec_type=0, pre_norm=1)
+    _refused(ps, 3, ps.lib().ps_block_norm_forward(rec, ps.CBlockNormFwd(), None), "2^30")
+    _refused(ps, 3, ps.lib().ps_block_norm_backward(rec, ps.CBlockNormBwd(), None), "2^30")
+    _refused(ps, 3, ps.lib().ps_block_norm_workspace_size(rec, ctypes.c_size_t(0)), "2^30")
+
+
+@pytest.mark.parametrize("how", ["deepcopy", "pickle", "replace"])
+def test_a_copied_norm_has_vectors_of_its_own(ps, how):
+    """A used norm keeps the addresses of its vectors; a copy must not take them over."""
+    import copy
+    import dataclasses
+    import pickle
+    norm = ps.BlockNorm(mul=torch.ones(8), gate=torch.ones(8), post_norm=ps.NORM_RMS)
+    first = norm._record(2, 8, torch.bfloat16, torch.device("cpu"))
+    assert first.mul == norm.mul.data_ptr()
+    if how == "deepcopy":
+        other = copy.deepcopy(norm)
+    elif how == "pickle":
+        other = pickle.loads(pickle.dumps(norm))
+    else:
+        other = dataclasses.replace(norm, mul=torch.ones(8), gate=torch.ones(8))
+    rec = other._record(3, 8, torch.bfloat16, torch.device("cpu"))
+    assert (rec.rows, rec.mul, rec.gate) == (3, other.mul.data_ptr(), other.gate.data_ptr())
+    assert other.mul.data_ptr() != norm.mul.data_ptr() and rec.post_norm == ps.NORM_RMS
+    assert norm == norm and norm != other and len({norm, other}) == 2
