@@ -232,7 +232,10 @@ enum { kNoBranch = 0, kPlain = 1, kNormed = 2 };
 // loaded into the registers of this one's as soon as it is used, before the sums
 // whose barriers the load's latency would otherwise add to; a segment's vectors
 // stay in registers, since a load behind those of the next row would wait for
-// them. The widest rows (V > 1) leave no registers for either.
+// them. The widest rows (V > 1) leave no registers for either, and take their
+// vectors when they are needed (4096 x 12288 with both norms 143 -> 128 us); at
+// 16384 columns the sums and two rows' values are still more than the registers
+// hold (33 to 130 of them in scratch memory: 2.0 TB/s with a branch, 4.0 without).
 // Waits for a load count what was issued behind it, the fewest over all ways
 // there, so a branch around a later load or store makes them waits for nearly
 // everything. Rows of a multiple of 512 columns (kEvery) have no such branch:
@@ -269,29 +272,32 @@ __global__ __launch_bounds__(V == 1 ? 1024 : 512) void k_norm_backward(NormArgs 
     }
     // m, and branch_scale * gate * post_weight (0 for columns that do not exist)
     float km[V][8], ky[V][8], acc[3][V][8];
-    auto vectors = [&]() __attribute__((always_inline)) {
+    auto vectors = [&](bool first, bool second) __attribute__((always_inline)) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const Cols<END> c((v * nt + lane) * 8, p.cols);
         const float one = p.flags & PS_NORM_MUL_PLUS_ONE ? 1.0f : 0.0f;
         RawVec rm, rg, rw;
-        if (p.mul) rm = load_vec(p.mul, p.vec_type, seg_offset(p, PS_NORM_MOD_BY_SEG, seg), c);
-        if (p.gate) rg = load_vec(p.gate, p.vec_type, seg_offset(p, PS_NORM_GATE_BY_SEG, seg), c);
-        if (p.w1) rw = load_vec(p.w1, p.vec_type, 0, c);
+        if (first && p.mul) rm = load_vec(p.mul, p.vec_type, seg_offset(p, PS_NORM_MOD_BY_SEG, seg), c);
+        if (second && p.gate) rg = load_vec(p.gate, p.vec_type, seg_offset(p, PS_NORM_GATE_BY_SEG, seg), c);
+        if (second && p.w1) rw = load_vec(p.w1, p.vec_type, 0, c);
         float m[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) km[v][j] = 1.0f, ky[v][j] = j < c.left ? p.beta : 0.0f;
-        if (p.mul) {
+        for (int j = 0; j < 8; ++j) {
+          if (first) km[v][j] = 1.0f;
+          if (second) ky[v][j] = j < c.left ? p.beta : 0.0f;
+        }
+        if (first && p.mul) {
           widen_vec(rm, p.vec_type, c, m);
 #pragma unroll
           for (int j = 0; j < 8; ++j) km[v][j] = one + m[j];
         }
-        if (p.gate) {
+        if (second && p.gate) {
           widen_vec(rg, p.vec_type, c, m);
 #pragma unroll
           for (int j = 0; j < 8; ++j) ky[v][j] *= m[j];
         }
-        if (p.w1) {
+        if (second && p.w1) {
           widen_vec(rw, p.vec_type, c, m);
 #pragma unroll
           for (int j = 0; j < 8; ++j) ky[v][j] *= m[j];
@@ -323,7 +329,7 @@ __global__ __launch_bounds__(V == 1 ? 1024 : 512) void k_norm_backward(NormArgs 
     if (kAhead) {
       load_first(row);
       load_second(row);
-      vectors();
+      vectors(true, true);
     }
 #pragma unroll
     for (int i = 0; i < 3; ++i)
@@ -336,7 +342,7 @@ __global__ __launch_bounds__(V == 1 ? 1024 : 512) void k_norm_backward(NormArgs 
       if (!kAhead) {
         load_first(row);
         load_second(row);
-        vectors();
+        vectors(true, false);
       }
       const int ahead = row + step < end ? row + step : row;   // the last row is loaded twice
       float g[V][8], z[V][8], c, d;
@@ -383,6 +389,7 @@ __global__ __launch_bounds__(V == 1 ? 1024 : 512) void k_norm_backward(NormArgs 
       const float r2 = uniform(y_rstd);
       if (kAhead) load_second(ahead);
       if (SAVED == kNoBranch && !p.dy) continue;
+      if (!kAhead) vectors(false, true);
 #pragma unroll
       for (int v = 0; v < V; ++v)
 #pragma unroll
@@ -480,6 +487,9 @@ ps_status forward(const NormArgs& p, hipStream_t s) {
     hipLaunchKernelGGL((k_norm_forward<TYPE, 1, true, END>), four, dim3(256), 0, s, p);
   else if (lanes <= 128)
     hipLaunchKernelGGL((k_norm_forward<TYPE, 2, true, END == kShort ? kPart : END>), four, dim3(256), 0, s, p);
+  else if (lanes > 512 && lanes <= 1024)   // 8192 x 5120 with two norms 104 -> 93 us, 8192 x 8192 136 -> 134
+    hipLaunchKernelGGL((k_norm_forward<TYPE, 1, false, END == kShort ? kPart : END>), grid_2d(p.rows),
+                       dim3(waves_for(lanes, 1) * 64), 0, s, p);
   else
     hipLaunchKernelGGL((k_norm_forward<TYPE, 2, false, END == kShort ? kPart : END>), grid_2d(p.rows),
                        dim3(waves_for(lanes, 2) * 64), 0, s, p);

@@ -345,9 +345,10 @@ __global__ __launch_bounds__(S::THREADS, S::THREADS / 256) void k_wgrad(WgradArg
   };
 
   // Two buffers: while one is multiplied the other is filled with the tiles that
-  // were loaded a step before. The fragments of 16 tokens are read ahead of the matrix instructions that use them, the first ones of a
-  // step before the last 16 tokens of the step before are multiplied. The last
-  // steps load and place the last tiles again, so that no branch cuts a step.
+  // were loaded a step before. The fragments of 16 tokens are read ahead of the
+  // matrix instructions that use them, the first ones of a step before the last 16
+  // tokens of the step before are multiplied. The last steps load and place the
+  // last tiles again, so that no branch cuts a step.
   const int whole = __builtin_amdgcn_readfirstlane(first + (safe > first ? (safe - first) / S::STEP * S::STEP : 0));
   const int last = whole - S::STEP;
   auto step = [&](char* cur, char* nxt, int t, auto sum) __attribute__((always_inline)) {
