@@ -183,3 +183,19 @@ def test_refusals_of_the_binding(ps):
             ps.encode_act(a["x"], a["code"], a["scale"])
     with pytest.raises(ps.PSError, match="overlap"):
         ps.glu_forward(x, x, ps.ACT_SILU)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_activations_over_their_whole_range(ps, act):
+    """fp32 against 64 bits from where f leaves 0 to where it is a; its tails go to 0 and a."""
+    kind = {"silu": ps.ACT_SILU, "gelu": ps.ACT_GELU, "gelu_tanh": ps.ACT_GELU_TANH}[act]
+    end = 80.0 if act == "silu" else 12.5 if act == "gelu" else 8.5     # f(-end) is above 2^-126
+    a = torch.linspace(-end, end, 1 << 16, device="cuda").view(64, 1024)
+    out = torch.empty_like(a)
+    ps.glu_forward(a, out, kind)
+    want, err = ref.glu(act, a.double().cpu(), None)
+    ref.check(out, want, err, act)
+    a = torch.tensor([[0.0, -0.0, 200.0, 1e30, 3e38, -200.0, -1e30, -3e38]], device="cuda")
+    out = torch.empty_like(a)
+    ps.glu_forward(a, out, kind)
+    assert torch.equal(out, a.clamp(min=0))
