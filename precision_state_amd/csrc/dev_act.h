@@ -248,6 +248,19 @@ __device__ __forceinline__ void codes_to_f32(u32x2_any c, const Cols<END>& at, f
   e4m3_unpack4(c[1], d + 4);
 }
 
+// A decoded value, code times scale. The code of a finite x may be rounded up to
+// what its type does not hold: 2^16 of an fp16 x from 63488 on, and of others
+// 2^128, infinite in fp32, from 1.9375 * 2^127 on. Those are the type's largest
+// value, which is the nearer one to x too. Greater products (an fp16 result from
+// values of another type) overflow as they would in any conversion.
+template <int TYPE>
+__device__ __forceinline__ float decoded(float code, float s) {
+  constexpr float kPast = TYPE == PS_TYPE_F16 ? 0x1p16f : __builtin_inff();
+  constexpr float kMost = TYPE == PS_TYPE_F16 ? 65504.0f : TYPE == PS_TYPE_BF16 ? 0x1.FEp127f : 0x1.FFFFFEp127f;
+  const float x = code * s;
+  return __builtin_fabsf(x) == kPast ? __builtin_copysignf(kMost, x) : x;
+}
+
 // Eight values of a vector of any type (uniform), kept in the caches: loaded, and
 // later widened, so that several vectors are under way at a time.
 typedef Raw8<PS_TYPE_F32> RawVec;

@@ -80,7 +80,7 @@ __global__ __launch_bounds__(kThreads) void k_decode_act(ActGrid g, const uint8_
     float v[8];
     codes_to_f32(c[k], p.c, v);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] *= s[k];
+    for (int j = 0; j < 8; ++j) v[j] = decoded<TYPE>(v[j], s[k]);
     store8<TYPE>(row_of<TYPE>(x, p.row, ld), p.col, p.to_store(), v);
   }
 }
@@ -163,9 +163,9 @@ __global__ __launch_bounds__(kThreads) void k_glu_backward(ActGrid g, GluArgs t)
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     float f, slope;
-    activation<ACT>(a[j] * sa, f, slope);
+    activation<ACT>(decoded<TYPE>(a[j], sa), f, slope);
     if (GATED) {
-      const float v = b[j] * sb;
+      const float v = decoded<TYPE>(b[j], sb);
       db[j] = d[j] * f;
       da[j] = d[j] * v * slope;
       o[j] = f * v;
