@@ -637,7 +637,12 @@ ps_status ps_block_norm_backward(const ps_block_norm* norm, const ps_block_norm_
  * of a block norm and its vectors as mul and add (NULL: 1 and 0; a mul that
  * means 1 + mul has to be given so), x is the norm's output n.
  * dy_type is PS_TYPE_BF16 or PS_TYPE_F16; z is multiplied in that type: bf16
- * holds it whole if scales are powers of two, fp16 within its range. Products
+ * holds it whole if scales are powers of two (2^128, which codes of 3.3e38 and
+ * more stand for, is infinite), fp16 from 2^-21 on (below, it is rounded to a
+ * multiple of 2^-24, which the codes of an fp16 x are already) up to 65504,
+ * beyond which it is infinite. 2^16, which codes of an fp16 x from 63488 on stand
+ * for, is 65504 as ps_decode_act has it; to that end a power of two in a block
+ * whose scale is 2^8 or more is taken one step of fp16 lower. Products
  * and sums are fp32, in an order that depends on the sizes only. dw of dw_type
  * (PS_TYPE_*) with distance lddw between rows; db float[out], NULL: not wanted;
  * mul, add float[in]. accumulate 1: dw and db are added to what the arrays

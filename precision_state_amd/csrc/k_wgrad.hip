@@ -95,6 +95,20 @@ __device__ __forceinline__ s16x8 values(i32x2 c, const float* s) {
   return __builtin_bit_cast(s16x8, w);
 }
 
+// A block's scale as codes are multiplied by it. The code of a finite fp16 x from
+// 63488 on stands for 2^16, which fp16 does not hold: with scales that reach so far
+// made smaller by a little more than half a step of fp16 at a power of two, that
+// product rounds to 65504. Of the others, powers of two round to the value one step
+// below (2^-11 of it: no more than a rounding may be off), the rest as they would
+// have, since a code's four bits leave them less than half a step away (1.875 / 2
+// of it at most); greater ones are infinite as before. It is done where a lane has
+// one scale of a step, not for each value between the matrix instructions. bf16
+// reaches as far as fp32: only an x of 3.3e38 and more leaves it, and with it dw.
+template <int TYPE>
+__device__ __forceinline__ float scale_for(float s) {
+  return TYPE == PS_TYPE_F16 && s >= 0x1p8f ? s * (1.0f - 0x1p-12f - 0x1p-20f) : s;
+}
+
 template <int TYPE>
 __device__ __forceinline__ f32x16 mfma(s16x8 a, s16x8 b, f32x16 c) {
   if (TYPE == PS_TYPE_BF16)
@@ -266,7 +280,10 @@ __global__ __launch_bounds__(S::THREADS, S::THREADS / 256) void k_wgrad(WgradArg
   };
   // The i-th part of three: what was loaded goes to the buffer, and the same rows
   // of the step after are loaded.
-  constexpr int U = S::STEP / 16, kParts = U - 1;
+  // The scales go with the first part, but those of fp16, which scale_for makes
+  // wait, with the last one (16384 x 8192 x 8192 2093 -> 2043 us; with the column
+  // sums 2077 -> 2091, so not there).
+  constexpr int U = S::STEP / 16, kParts = U - 1, kScalePart = TYPE == PS_TYPE_F16 && !SUMS ? kParts - 1 : 0;
   auto renew = [&](char* buf, int part, int t0) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = part * kA / kParts; i < (part + 1) * kA / kParts; ++i) {
@@ -278,8 +295,8 @@ __global__ __launch_bounds__(S::THREADS, S::THREADS / 256) void k_wgrad(WgradArg
       if (has_b) *(u32x4*)(buf + to_b + i * kPassB * S::K) = rb[i];
       load_b(i, t0);
     }
-    if (part == 0) {
-      if (SCALED) *(float*)(buf + to_s) = rs;
+    if (part == kScalePart) {
+      if (SCALED) *(float*)(buf + to_s) = scale_for<TYPE>(rs);
       load_s(t0);
     }
   };
@@ -299,7 +316,7 @@ __global__ __launch_bounds__(S::THREADS, S::THREADS / 256) void k_wgrad(WgradArg
             load16_guarded((const char*)p.code, t, t < end ? p.tokens : 0, p.k, k0 + qb * 16, p.k);
     }
     const int64_t t = t0 + ts;
-    if (SCALED) *(float*)(buf + to_s) = t < end ? p.scale[t * k_blocks + scale_block] : 0.0f;
+    if (SCALED) *(float*)(buf + to_s) = t < end ? scale_for<TYPE>(p.scale[t * k_blocks + scale_block]) : 0.0f;
   };
 
   f32x16 acc[S::FN][S::FK];

@@ -2,7 +2,8 @@
 finite value that was saved is finite when it is read.
 
 The largest codes of a block are rounded up past the type's largest value: of
-fp16 from 63488 on (to 2^16), of bf16 and fp32 from 1.9375 * 2^127 on (to 2^128).
+fp16 from 63488 on (to 2^16), of bf16 and fp32 from 1.9375 * 2^127 on (to 2^128;
+the weight gradient leaves those infinite).
 Infinities are compared as they are."""
 import math
 
@@ -98,3 +99,40 @@ def test_activations_of_the_largest_values(ps, dtype, act):
     ps.glu_backward(d, kind, saved[0], saved[1], da, out=again)
     assert torch.equal(da.cpu()[large], t(0.25 * (va > 0)))
     assert torch.equal(again.cpu()[large], t(va.clamp(min=0)))
+
+
+@pytest.mark.parametrize("t,n,k", [(1, 8, 200), (64, 40, 256), (200, 33, 330), (1030, 12, 300), (700, 300, 20), (192, 1024, 1152)])
+def test_weight_gradients_of_the_largest_values(ps, t, n, k):
+    """One token alone has a gradient for each row of dw, so that dw is its z: rows that end a step or a tile, and
+    those that whole steps take. In fp16 z is code times scale, or one step less for powers of two in blocks whose scales
+    reach the border, and finite."""
+    dtype, f = "f16", torch.finfo(torch.float16)
+    x = top(dtype)[0, 40:48].repeat(t, -(-k // 8))[:, :k].contiguous()
+    x[:, 1::5] *= 0.001                                         # smaller values beside the largest
+    c, s = codes(t, k), scales(t, k)
+    ps.encode_act(x.cuda(), c, s)
+    dy = torch.zeros(t, n, dtype=torch.float16)
+    at = [(i * 37 + t - 1) % t for i in range(n)]
+    dy[at, range(n)] = 1.0
+    w, b = torch.empty(n, k, device="cuda"), torch.empty(n, device="cuda")
+    for db in (None, b):
+        ps.linear_wgrad(dy.cuda(), c, w, scale=s, db=db)
+        z, got = want_of(c, s, dtype)[at], w.cpu().double()
+        assert got.isfinite().all()
+        same = got == z.half().double()
+        power = (torch.frexp(z.abs())[0] == 0.5) & (s.cpu()[at].repeat_interleave(128, 1)[:, :k] >= 256)
+        assert (same | (power & (got == z * (1 - f.eps / 2)))).all()
+        assert (got.abs() == f.max).any()
+    assert (b == dy.double().sum(0).cuda()).all()
+
+
+def test_fp16_weight_gradients_of_wider_values(ps):
+    """Saved values beyond fp16 are infinite in a product with an fp16 dy, not cut to its largest value."""
+    x = torch.zeros(1, 128)
+    x[0, :4] = torch.tensor([1e6, 8e4, 65e3, 5e4])
+    c, s = codes(1, 128), scales(1, 128)
+    ps.encode_act(x.cuda(), c, s)
+    w = torch.empty(8, 128, device="cuda")
+    ps.linear_wgrad(torch.ones(1, 8, dtype=torch.float16, device="cuda"), c, w, scale=s)
+    z = ref.value(c, s)[0]
+    assert (w[:, :2] == math.inf).all() and (w[:, 2] == 65504).all() and (w[:, 3].cpu() == z[3]).all() and (w[:, 4:] == 0).all()
