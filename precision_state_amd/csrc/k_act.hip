@@ -113,9 +113,12 @@ __device__ __forceinline__ void activation(float a, float& f, float& slope) {
   const float z = __builtin_amdgcn_fmed3f(a, -64.0f, 64.0f);   // q is 0 or 1 there, and z^2 stays finite
   const float u = ACT == PS_ACT_SILU ? a : 2.0f * c * z * __builtin_fmaf(c3, z * z, 1.0f);
   const float du = ACT == PS_ACT_SILU ? 1.0f : 2.0f * c * __builtin_fmaf(3.0f * c3, z * z, 1.0f);
-  const float q = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(u * -kLog2e));
+  // 1 - q is e q, which keeps its places where q is next to 1 and f and du are large
+  // (1 - q itself: slopes of tanh's form off by up to 2.0e-6, so by 2.4e-7); e is
+  // infinite where q is 0
+  const float e = __builtin_amdgcn_exp2f(u * -kLog2e), q = __builtin_amdgcn_rcpf(1.0f + e);
   f = a * q;
-  slope = __builtin_fmaf(f * (1.0f - q), du, q);
+  slope = __builtin_fmaf(f * (__builtin_amdgcn_fmed3f(e, 0.0f, 0x1p126f) * q), du, q);
 }
 
 template <int TYPE, int ACT, bool GATED, bool SAVE, int END>
