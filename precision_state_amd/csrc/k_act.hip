@@ -79,8 +79,7 @@ __global__ __launch_bounds__(kThreads) void k_decode_act(ActGrid g, const uint8_
     const Place<END> p(g, unit_of(k, K));
     float v[8];
     codes_to_f32(c[k], p.c, v);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = decoded<TYPE>(v[j], s[k]);
+    decode8<TYPE, false>(v, s[k]);
     store8<TYPE>(row_of<TYPE>(x, p.row, ld), p.col, p.to_store(), v);
   }
 }
@@ -161,17 +160,18 @@ __global__ __launch_bounds__(kThreads) void k_glu_backward(ActGrid g, GluArgs t)
     sb = t.b_scale[at];
     codes_to_f32(cb, p.c, b);
   }
-  widen8<TYPE>(rd, p.c, d);
   codes_to_f32(ca, p.c, a);
+  decode8<TYPE, !GATED && TYPE != PS_TYPE_F32>(a, sa);
+  if (GATED) decode8<TYPE, false>(b, sb);
+  widen8<TYPE>(rd, p.c, d);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     float f, slope;
-    activation<ACT>(decoded<TYPE>(a[j], sa), f, slope);
+    activation<ACT>(a[j], f, slope);
     if (GATED) {
-      const float v = decoded<TYPE>(b[j], sb);
       db[j] = d[j] * f;
-      da[j] = d[j] * v * slope;
-      o[j] = f * v;
+      da[j] = d[j] * b[j] * slope;
+      o[j] = f * b[j];
     } else {
       da[j] = d[j] * slope;
       o[j] = f;
