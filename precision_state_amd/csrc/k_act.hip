@@ -88,9 +88,13 @@ __global__ __launch_bounds__(kThreads) void k_decode_act(ActGrid g, const uint8_
 // SILU, Phi for GELU, and for its tanh form (1 + tanh u) / 2, which is the
 // logistic function of 2 u and loses nothing where tanh u comes near -1.
 // Phi(-z) exp(z^2 / 2) for z >= 0 falls like 1 / z; in t = 1 / (1 + 0.35 z) it is
-// t times a polynomial, fitted here to a relative error of 3.2e-8 up to z = 14.5,
-// beyond which the exponential is 0 in fp32. The exponential serves f' too (the
-// math library's erfc: 8192 x 11008 bf16 forward 132 us, this 78).
+// t times a polynomial (the form of Hastings, Approximations for Digital
+// Computers, 1955), fitted here: a relative error of 3.2e-8, and 5.9e-8 with the
+// coefficients in fp32, up to z = 14.5, beyond which the exponential is 0 in fp32.
+// That is one rounding; f' is off by 5e-8 in the 2-norm for normal a, which is that
+// of its fp32 steps (a fit to the rounded coefficients, 3.4e-8, gains 1% of it).
+// The exponential serves f' too (the math library's erfc: 8192 x 11008 bf16
+// forward 132 us, this 66 to 70).
 template <int ACT>
 __device__ __forceinline__ void activation(float a, float& f, float& slope) {
   constexpr float kLog2e = 1.44269504f;

@@ -51,3 +51,33 @@ def test_logistic_slopes_keep_their_places(ps, act, size):
     err = ref.F * (q * eq + (a * q * p * du).abs() * (eq + ep + 8) + want.abs()) + 2.0 ** -125 * (1 + (a * du).abs())
     off = (got - want).abs()
     assert (off <= err).all(), (float((off / err).max()), a[off > err][:4].tolist())
+
+
+@pytest.mark.parametrize("size", [0.3, 2.0, 4.0])
+def test_gelu_and_its_slope(ps, size):
+    """w = Phi(-|a|) is e t P(t), e = exp(-a^2 / 2), t = 1 / (1 + 0.35 |a|), P of nine coefficients. In units of F: the
+    exponent has two products and a constant, which move e by 1.5 a^2, and exp2 is within 2; t is off by 4 (a constant,
+    a sum, the reciprocal within 2), which P takes with the factor sum i |c_i| t^i / P; each step of P adds one of its
+    own size, at most 2 sum |c_i| t^i / P together; two more products, and one of the fit. q is w, or 1 - w with one
+    rounding; f = a q has one more, and f' = q + a e / sqrt(2 pi) a product and a constant beside e's error, and its
+    own. Below 2^-120 there may be nothing left."""
+    g = gen(int(10 * size) + 1)
+    got, want, a = slopes(ps, "gelu", torch.randn(256, 1024, generator=g) * size, g)
+    out = torch.empty(256, 1024, device="cuda")
+    ps.glu_forward(a.float().cuda(), out, ps.ACT_GELU)
+    z = a.abs()
+    t = 1 / (1 + 0.35 * z)
+    c = [0.1396, 0.1399, 0.1198, 0.1056, 0.0232, 0.1593, 0.2558, 0.1440, 0.0292]       # sizes
+    p = 0.5 * torch.special.erfcx(z / 2 ** 0.5) / t
+    spread = sum(i * v * t ** i for i, v in enumerate(c)) / p
+    size_p = sum(v * t ** i for i, v in enumerate(c)) / p
+    ee = 1.5 * z * z + 2
+    ew = ee + 4 + 4 * spread + 2 * size_p + 2 + 1
+    w = 0.5 * torch.special.erfc(z / 2 ** 0.5)
+    q = torch.where(a < 0, w, 1 - w)
+    eq = ref.F * (ew * w + q)
+    phi = torch.exp(-z * z / 2) / (2 * torch.pi) ** 0.5
+    for name, g_, w_, err in (("f", out.cpu().double(), a * q, z * eq + ref.F * (a * q).abs()),
+                              ("slope", got, want, eq + ref.F * (z * phi * (ee + 3) + want.abs()))):
+        off = (g_ - w_).abs()
+        assert (off <= err + 2.0 ** -120 * (1 + z)).all(), (name, float((off / err).max()))
