@@ -20,14 +20,16 @@ _TYPES = {torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16, torch.float16: TYP
 
 
 def _like(x, name):
-    """Shape, type and device that the other matrices of a call have to have: those of x."""
-    if x.dim() != 2:
-        raise ValueError(f"{name} has {x.dim()} dimensions, not 2")
-    if x.dtype not in _TYPES:
-        raise ValueError(f"{name} has dtype {x.dtype}, not float32, bfloat16 or float16")
-    if x.device.type != "cuda":
+    """x as the first matrix of a call: shape, type and device that the others have to have, and pointer and distance
+    between rows."""
+    shape, dtype, device = x.shape, x.dtype, x.device
+    if len(shape) != 2:
+        raise ValueError(f"{name} has {len(shape)} dimensions, not 2")
+    if dtype not in _TYPES:
+        raise ValueError(f"{name} has dtype {dtype}, not float32, bfloat16 or float16")
+    if device.type != "cuda":
         raise ValueError(f"{name} is not on a GPU")
-    return x.shape, x.dtype, x.device
+    return shape, dtype, device, _rows(x, name, shape)
 
 
 def _matrix(x, name, shape, dtype, device):
@@ -36,6 +38,10 @@ def _matrix(x, name, shape, dtype, device):
         return None, 0
     if x.shape != shape or x.dtype is not dtype or x.device != device:
         raise ValueError(f"{name} is {x.dtype} {tuple(x.shape)} on {x.device}, not {dtype} {tuple(shape)} on {device}")
+    return _rows(x, name, shape)
+
+
+def _rows(x, name, shape):
     row, col = x.stride()
     if col != 1 and shape[1] > 1:
         raise ValueError(f"the rows of {name} are not contiguous")
@@ -86,8 +92,7 @@ def _room(workspace, size, device, stream):
 def encode_act(x, code, scale, stream=None):
     """A matrix -> e4m3 codes and a power-of-two scale for each 128 columns of a row (ps_encode_act)."""
     _needed(code=code, scale=scale)
-    shape, dtype, device = _like(x, "x")
-    p, ld = _matrix(x, "x", shape, dtype, device)
+    shape, dtype, device, (p, ld) = _like(x, "x")
     c, s = _code(code, scale, "", shape, device)
     with _on(device):
         _check(_lib.ps_encode_act(p, _TYPES[dtype], shape[0], shape[1], ld, c, s, _raw_stream(device, stream)))
@@ -96,8 +101,7 @@ def encode_act(x, code, scale, stream=None):
 def decode_act(code, scale, x, stream=None):
     """The matrix that codes and scales stand for (ps_decode_act)."""
     _needed(code=code, scale=scale)
-    shape, dtype, device = _like(x, "x")
-    p, ld = _matrix(x, "x", shape, dtype, device)
+    shape, dtype, device, (p, ld) = _like(x, "x")
     c, s = _code(code, scale, "", shape, device)
     with _on(device):
         _check(_lib.ps_decode_act(c, s, p, _TYPES[dtype], shape[0], shape[1], ld, _raw_stream(device, stream)))
@@ -106,8 +110,7 @@ def decode_act(code, scale, x, stream=None):
 def glu_forward(a, out, act, a_code=None, a_scale=None, b=None, b_code=None, b_scale=None, stream=None):
     """out = f(a) * b, or f(a) without b, f one of ACT_*; a and b saved in codes and scales if these are given
     (ps_glu_forward)."""
-    shape, dtype, device = _like(a, "a")
-    pa, lda = _matrix(a, "a", shape, dtype, device)
+    shape, dtype, device, (pa, lda) = _like(a, "a")
     pb, ldb = _matrix(b, "b", shape, dtype, device)
     _needed(out=out)
     po, ldo = _matrix(out, "out", shape, dtype, device)
@@ -122,8 +125,7 @@ def glu_backward(dout, act, a_code, a_scale, da, b_code=None, b_scale=None, db=N
     """The gradients of a, and of b if it is gated, from the saved codes; and the output once more, if `out` is given
     (ps_glu_backward)."""
     _needed(a_code=a_code, a_scale=a_scale, da=da)
-    shape, dtype, device = _like(dout, "dout")
-    pd, ldd = _matrix(dout, "dout", shape, dtype, device)
+    shape, dtype, device, (pd, ldd) = _like(dout, "dout")
     ca, sa = _code(a_code, a_scale, "a_", shape, device)
     cb, sb = _code(b_code, b_scale, "b_", shape, device)
     pa, lda = _matrix(da, "da", shape, dtype, device)
@@ -140,8 +142,9 @@ class BlockNorm:
     add together, are [cols], or [segments, cols] with a vector for each. segments: int32 tensor on the device, where
     each of the batch's packed sequences starts, and where the last one ends.
 
-    The vectors are checked at the first call, and from then on their memory is kept alive by a reference of the norm's
-    own; their values are read at every call. Other vectors need another norm (dataclasses.replace)."""
+    Each call reads the vectors as they are then: a vector may be given other memory (`.data = ...`, a module that moves,
+    a storage that is released and comes back) between calls. Checks are repeated where a vector's address, type or
+    shape is not what it was."""
     pre_norm: int = NORM_RMS
     pre_eps: float = 1e-6
     post_norm: int = NORM_NONE
@@ -158,16 +161,21 @@ class BlockNorm:
     def _record(self, rows, cols, dtype, device):
         """A record of the call's own: two threads may use one norm."""
         made = self.__dict__.get("_made")
-        if made is None or made[0] != (cols, dtype, device):
-            made = (cols, dtype, device), bytes(self._make(cols, dtype, device)), \
-                [v.untyped_storage() for v in (self.post_weight, self.gate, self.mul, self.add, self.segments) if v is not None]
+        now = [cols, dtype, device]
+        for v in (self.post_weight, self.gate, self.mul, self.add, self.segments):
+            if v is None:
+                now.append(None)
+            else:    # an address is one device's
+                now += v.data_ptr(), v.dtype, v.shape, v.is_contiguous()
+        if made is None or made[0] != now:
+            made = now, bytes(self._make(cols, dtype, device))
             object.__setattr__(self, "_made", made)
         rec = CBlockNorm.from_buffer_copy(made[1])
         rec.rows = rows
         return rec
 
     def __getstate__(self):
-        """Without the record: a copy's vectors lie elsewhere."""
+        """Without the record, which is this norm's alone."""
         return {k: v for k, v in self.__dict__.items() if k != "_made"}
 
     def _make(self, cols, dtype, device):
@@ -198,12 +206,12 @@ def block_norm_forward(norm: BlockNorm, x, n, y=None, h=None, h_code=None, h_rst
     """h = residual_scale x + branch_scale gate N1(y) post_weight and n = N2(h) mul + add, with what the backward pass
     needs saved in h_code, h_rstd and, with a post norm or a gate, y_code and y_rstd or y_scale
     (ps_block_norm_forward)."""
-    shape, dtype, device = _like(x, "x")
+    shape, dtype, device, first = _like(x, "x")
     _needed(n=n)
     rec = norm._record(shape[0], shape[1], dtype, device)
     hc, _ = _code(h_code, None, "h_", shape, device)
     yc, ys = _code(y_code, y_scale, "y_", shape, device)
-    io = CBlockNormFwd(*_matrix(x, "x", shape, dtype, device), *_matrix(y, "y", shape, dtype, device),
+    io = CBlockNormFwd(*first, *_matrix(y, "y", shape, dtype, device),
                        *_matrix(h, "h", shape, dtype, device), *_matrix(n, "n", shape, dtype, device),
                        hc, _whole(h_rstd, "h_rstd", shape[:1], _F32, device), yc, ys,
                        _whole(y_rstd, "y_rstd", shape[:1], _F32, device))
@@ -227,7 +235,7 @@ def block_norm_backward(norm: BlockNorm, dn, h_code, h_rstd, dx, dh=None, dy=Non
     gradients of the vectors that are given (ps_block_norm_backward). workspace: block_norm_workspace_size bytes, or
     None for one of the call's own."""
     _needed(h_code=h_code, h_rstd=h_rstd, dx=dx)
-    shape, dtype, device = _like(dn, "dn")
+    shape, dtype, device, first = _like(dn, "dn")
     rec = norm._record(shape[0], shape[1], dtype, device)
     hc, _ = _code(h_code, None, "h_", shape, device)
     yc, ys = _code(y_code, y_scale, "y_", shape, device)
@@ -244,7 +252,7 @@ def block_norm_backward(norm: BlockNorm, dn, h_code, h_rstd, dx, dh=None, dy=Non
             workspace, room = _room(None, size.value, device, stream)
         else:
             workspace, room = _room(workspace, 0, device, stream)
-        io = CBlockNormBwd(*_matrix(dn, "dn", shape, dtype, device), *_matrix(dh, "dh", shape, dtype, device), hc,
+        io = CBlockNormBwd(*first, *_matrix(dh, "dh", shape, dtype, device), hc,
                            _whole(h_rstd, "h_rstd", shape[:1], _F32, device), yc, ys,
                            _whole(y_rstd, "y_rstd", shape[:1], _F32, device), *_matrix(dx, "dx", shape, dtype, device),
                            *_matrix(dy, "dy", shape, dtype, device), *grads, workspace.data_ptr(), room, int(accumulate))
@@ -264,12 +272,11 @@ def linear_wgrad(dy, code, dw, scale=None, db=None, mul=None, add=None, accumula
     of its bias, db (ps_linear_wgrad). mul, add, db: float32. workspace: linear_wgrad_workspace_size bytes, or None for
     one of the call's own."""
     _needed(code=code, dw=dw)
-    shape, dtype, device = _like(dy, "dy")
+    shape, dtype, device, (pd, ldd) = _like(dy, "dy")
     if code.dim() != 2:
         raise ValueError(f"code has {code.dim()} dimensions, not 2")
     tokens, n = shape
     k = code.shape[1]
-    pd, ldd = _matrix(dy, "dy", shape, dtype, device)
     c, s = _code(code, scale, "", (tokens, k), device)
     if dw.dtype not in _TYPES:
         raise ValueError(f"dw has dtype {dw.dtype}, not float32, bfloat16 or float16")
