@@ -45,7 +45,20 @@ def _rows(x, name, shape):
     row, col = x.stride()
     if col != 1 and shape[1] > 1:
         raise ValueError(f"the rows of {name} are not contiguous")
-    return x.data_ptr(), row if shape[0] > 1 else max(row, shape[1])
+    at = x.data_ptr()
+    if at < _LOW:
+        _released(x, name)
+    return at, row if shape[0] > 1 else max(row, shape[1])
+
+
+# A tensor whose storage was released has its offset for an address: NULL would mean that there is no such array, and
+# nothing lies at the others. No allocation lies so low; the storage itself is looked at there only.
+_LOW = 1 << 36
+
+
+def _released(x, name):
+    if x.numel() and not x.untyped_storage().nbytes():
+        raise ValueError(f"the storage of {name} was released")
 
 
 def _whole(x, name, shape, dtypes, device):
@@ -56,7 +69,10 @@ def _whole(x, name, shape, dtypes, device):
         raise ValueError(f"{name} is {x.dtype} {tuple(x.shape)} on {x.device}, not {dtypes[0]} {tuple(shape)} on {device}")
     if not x.is_contiguous():
         raise ValueError(f"{name} is not contiguous")
-    return x.data_ptr()
+    at = x.data_ptr()
+    if at < _LOW:
+        _released(x, name)
+    return at
 
 
 _F32 = (torch.float32,)
@@ -86,6 +102,8 @@ def _room(workspace, size, device, stream):
                 workspace = torch.empty(size, dtype=torch.uint8, device=device)
     elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace has to be contiguous on {device}")
+    elif workspace.data_ptr() < _LOW:
+        _released(workspace, "workspace")
     return workspace, workspace.numel() * workspace.element_size()
 
 

@@ -64,3 +64,36 @@ def test_an_order_that_changed_in_place_is_seen(ps):
     norm.gate.as_strided_((3, 8), (1, 3))
     with pytest.raises(ValueError, match="gate is not contiguous"):
         norm._record(2, 8, BF16, CPU)
+
+
+@pytest.mark.parametrize("name", ["post_weight", "gate", "mul", "add", "segments"])
+def test_a_vector_without_memory_is_refused(ps, name):
+    """A released storage has the address NULL, which would mean that there is no such vector."""
+    norm = vectors(ps)
+    norm._record(2, 8, BF16, CPU)
+    v = getattr(norm, name)
+    v.untyped_storage().resize_(0)
+    with pytest.raises(ValueError, match=f"storage of {name} was released"):
+        norm._record(2, 8, BF16, CPU)
+
+
+@pytest.mark.parametrize("part", [slice(0, 4), slice(4, 8)], ids=["from the start", "with an offset"])
+def test_arrays_without_memory_are_refused(ps, part):
+    """Matrices and contiguous arrays, whole or parts of what was released (whose addresses are their offsets)."""
+    act = ps._activations
+    wide = torch.ones(4, 8)
+    x, rows = wide[:, part], wide[1:3]
+    assert act._matrix(x, "x", x.shape, torch.float32, CPU) == (x.data_ptr(), 8)
+    assert act._whole(rows, "rows", rows.shape, act._F32, CPU) == rows.data_ptr()
+    wide.untyped_storage().resize_(0)
+    with pytest.raises(ValueError, match="storage of x was released"):
+        act._matrix(x, "x", x.shape, torch.float32, CPU)
+    with pytest.raises(ValueError, match="storage of rows was released"):
+        act._whole(rows, "rows", rows.shape, act._F32, CPU)
+    w = torch.ones(64, dtype=torch.uint8)
+    assert act._room(w[16:], 0, CPU, None)[1] == 48
+    w.untyped_storage().resize_(0)
+    with pytest.raises(ValueError, match="storage of workspace was released"):
+        act._room(w[16:], 0, CPU, None)
+    empty = torch.empty(0, 8)                              # nothing to read: no memory needed
+    assert act._matrix(empty, "x", empty.shape, torch.float32, CPU) == (empty.data_ptr(), 8)
