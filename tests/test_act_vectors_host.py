@@ -90,10 +90,10 @@ def test_arrays_without_memory_are_refused(ps, part):
         act._matrix(x, "x", x.shape, torch.float32, CPU)
     with pytest.raises(ValueError, match="storage of rows was released"):
         act._whole(rows, "rows", rows.shape, act._F32, CPU)
-    w = torch.ones(64, dtype=torch.uint8)
-    assert act._room(w[16:], 0, CPU, None)[1] == 48
-    w.untyped_storage().resize_(0)
+    room = torch.ones(64, dtype=torch.uint8)[16:]
+    assert act._room(room, 0, CPU, None)[1] == 48
+    room.untyped_storage().resize_(0)
     with pytest.raises(ValueError, match="storage of workspace was released"):
-        act._room(w[16:], 0, CPU, None)
+        act._room(room, 0, CPU, None)
     empty = torch.empty(0, 8)                              # nothing to read: no memory needed
     assert act._matrix(empty, "x", empty.shape, torch.float32, CPU) == (empty.data_ptr(), 8)
