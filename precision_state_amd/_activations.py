@@ -97,7 +97,12 @@ def _room(workspace, size, device, stream):
         if stream is None:
             workspace = torch.empty(size, dtype=torch.uint8, device=device)
         else:    # the allocator hands it out again in that stream's order
-            obj = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
+            if not isinstance(stream, int):
+                obj = stream
+            elif stream == 0:    # ExternalStream(0) would be a new stream
+                obj = torch.cuda.default_stream(device)
+            else:
+                obj = torch.cuda.ExternalStream(stream, device=device)
             with torch.cuda.stream(obj):
                 workspace = torch.empty(size, dtype=torch.uint8, device=device)
     elif workspace.device != device or not workspace.is_contiguous():

@@ -1,4 +1,5 @@
-"""GPU tests of block norms whose vectors move between calls."""
+"""GPU tests of the memory that the activation checkpoints' calls use: vectors that
+move between calls, workspaces of a call's own."""
 import pytest
 import torch
 
@@ -49,3 +50,34 @@ def test_vectors_are_read_where_they_are(ps, how):
     want = run(ps.BlockNorm(post_norm=ps.NORM_RMS, **{k: new[k] for k in names}))
     got = run(norm)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_a_workspace_belongs_to_the_stream_of_its_call(ps, monkeypatch):
+    """Given back, it may be handed out again in that stream's order only; the default stream's number is 0."""
+    device = torch.device("cuda", 0)
+    side = torch.cuda.Stream()
+    seen = []
+    empty = torch.empty
+
+    def record(*a, **kw):
+        seen.append(torch.cuda.current_stream(device).cuda_stream)
+        return empty(*a, **kw)
+    dy, code = torch.ones(2000, 96, dtype=torch.bfloat16, device=device), torch.full((2000, 640), 0x38, dtype=torch.uint8, device=device)
+    w = torch.empty(96, 640, device=device)
+    torch.cuda.synchronize()
+    monkeypatch.setattr(torch, "empty", record)
+    default = torch.cuda.default_stream(device).cuda_stream
+    for stream, want in ((0, default), (None, default), (torch.cuda.default_stream(device), default),
+                         (side, side.cuda_stream), (side.cuda_stream, side.cuda_stream)):
+        w.zero_()
+        torch.cuda.synchronize()
+        seen.clear()
+        ps.linear_wgrad(dy, code, w, stream=stream)
+        torch.cuda.synchronize()
+        assert seen == [want], stream
+        assert (w == 2000).all()
+    with torch.cuda.stream(side):                       # 0 is the default stream, not the current one
+        seen.clear()
+        ps.linear_wgrad(dy, code, w, stream=0)
+        assert seen == [default]
+    torch.cuda.synchronize()
