@@ -48,7 +48,7 @@ def _rows(x, name, shape):
     at = x.data_ptr()
     if at < _LOW:
         _released(x, name)
-    return at, row if shape[0] > 1 else max(row, shape[1])
+    return at, row if shape[0] > 1 else shape[1]    # a single row has no distance to another
 
 
 # A tensor whose storage was released has its offset for an address: NULL would mean that there is no such array, and

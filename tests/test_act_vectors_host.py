@@ -97,3 +97,11 @@ def test_arrays_without_memory_are_refused(ps, part):
         act._room(room, 0, CPU, None)
     empty = torch.empty(0, 8)                              # nothing to read: no memory needed
     assert act._matrix(empty, "x", empty.shape, torch.float32, CPU) == (empty.data_ptr(), 8)
+
+
+def test_a_single_row_has_no_distance_to_another(ps):
+    """One token's part of a matrix wider than a distance between rows may be (2^24 for dy) is a row like any other."""
+    x = torch.empty(1, 1 << 25, dtype=torch.uint8)[:, 5:105]
+    assert ps._activations._matrix(x, "x", x.shape, torch.uint8, CPU) == (x.data_ptr(), 100)
+    x = torch.empty(2, 300, dtype=torch.uint8)[:, 5:105]
+    assert ps._activations._matrix(x, "x", x.shape, torch.uint8, CPU) == (x.data_ptr(), 300)
