@@ -27,7 +27,7 @@ def _like(x, name):
         raise ValueError(f"{name} has {len(shape)} dimensions, not 2")
     if dtype not in _TYPES:
         raise ValueError(f"{name} has dtype {dtype}, not float32, bfloat16 or float16")
-    if device.type != "cuda":
+    if not x.is_cuda:
         raise ValueError(f"{name} is not on a GPU")
     return shape, dtype, device, _rows(x, name, shape)
 
@@ -184,16 +184,14 @@ class BlockNorm:
     def _record(self, rows, cols, dtype, device):
         """A record of the call's own: two threads may use one norm."""
         made = self.__dict__.get("_made")
+        vectors = made[0] if made else [v for v in (self.post_weight, self.gate, self.mul, self.add, self.segments) if v is not None]
         now = [cols, dtype, device]
-        for v in (self.post_weight, self.gate, self.mul, self.add, self.segments):
-            if v is None:
-                now.append(None)
-            else:    # an address is one device's
-                now += v.data_ptr(), v.dtype, v.shape, v.is_contiguous()
-        if made is None or made[0] != now:
-            made = now, bytes(self._make(cols, dtype, device))
+        for v in vectors:    # an address is one device's
+            now += v.data_ptr(), v.dtype, v.shape, v.is_contiguous()
+        if made is None or made[1] != now:
+            made = vectors, now, bytes(self._make(cols, dtype, device))
             object.__setattr__(self, "_made", made)
-        rec = CBlockNorm.from_buffer_copy(made[1])
+        rec = CBlockNorm.from_buffer_copy(made[2])
         rec.rows = rows
         return rec
 
