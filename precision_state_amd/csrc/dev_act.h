@@ -255,7 +255,8 @@ __device__ __forceinline__ void codes_to_f32(u32x2_any c, const Cols<END>& at, f
 // values of another type) overflow as they would in any conversion. Only scales
 // from 2^8 or 2^120 on reach so far, and SKIP passes other blocks by: that is for
 // kernels with as much arithmetic as memory traffic (8192 x 11008, one 16-bit input,
-// slope of SiLU or tanh's GELU 71.5 to 74.5 -> 71 us); the others are better off
+// slope of SiLU or tanh's GELU 71.5 to 74.5 -> 71 us; 524288 x 64 bf16 decoded,
+// where half of the lanes have nothing, 23.1 -> 22.0); the others are better off
 // without a branch (fp32, two inputs: 323 -> 300 us).
 template <int TYPE, bool SKIP>
 __device__ __forceinline__ void decode8(float* d, float s) {

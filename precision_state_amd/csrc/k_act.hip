@@ -79,7 +79,7 @@ __global__ __launch_bounds__(kThreads) void k_decode_act(ActGrid g, const uint8_
     const Place<END> p(g, unit_of(k, K));
     float v[8];
     codes_to_f32(c[k], p.c, v);
-    decode8<TYPE, false>(v, s[k]);
+    decode8<TYPE, TYPE != PS_TYPE_F32>(v, s[k]);
     store8<TYPE>(row_of<TYPE>(x, p.row, ld), p.col, p.to_store(), v);
   }
 }
