@@ -566,6 +566,7 @@ typedef struct ps_block_norm {
  *   h_code, h_rstd  N2(h) as e4m3 (|N2(h)| <= sqrt(cols), no scale), r of N2
  *   y_code, y_rstd  with a post_norm: N1(y) as e4m3, r of N1
  *   y_code, y_scale with a gate and no post_norm: y as ps_encode_act codes it
+ *                   (code * scale in fp32 is what the backward pass reads)
  * rstd arrays are float[rows]. */
 typedef struct ps_block_norm_fwd {
   const void* x;

@@ -94,7 +94,7 @@ __global__ __launch_bounds__(kThreads) void k_decode_act(ActGrid g, const uint8_
 // That is one rounding; f' is off by 5e-8 in the 2-norm for normal a, which is that
 // of its fp32 steps (a fit to the rounded coefficients, 3.4e-8, gains 1% of it).
 // The exponential serves f' too (the math library's erfc: 8192 x 11008 bf16
-// forward 132 us, this 66 to 70).
+// forward 132 us, this 78).
 template <int ACT>
 __device__ __forceinline__ void activation(float a, float& f, float& slope) {
   constexpr float kLog2e = 1.44269504f;
@@ -117,7 +117,7 @@ __device__ __forceinline__ void activation(float a, float& f, float& slope) {
   const float u = ACT == PS_ACT_SILU ? a : 2.0f * c * z * __builtin_fmaf(c3, z * z, 1.0f);
   const float du = ACT == PS_ACT_SILU ? 1.0f : 2.0f * c * __builtin_fmaf(3.0f * c3, z * z, 1.0f);
   // 1 - q is e q, which keeps its places where q is next to 1 and f and du are large
-  // (1 - q itself: slopes of tanh's form off by up to 2.0e-6, so by 2.4e-7); e is
+  // (1 - q itself: slopes of tanh's form off by up to 2.0e-6, so by 2.1e-7); e is
   // infinite where q is 0
   const float e = __builtin_amdgcn_exp2f(u * -kLog2e), q = __builtin_amdgcn_rcpf(1.0f + e);
   f = a * q;

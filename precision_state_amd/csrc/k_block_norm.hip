@@ -7,8 +7,9 @@
 // one pass over memory. The variance of a LayerNorm is the mean square about
 // the mean (a second reduction over registers), not a difference of sums.
 // Memory bounds the forward pass (16384 x 4096 bf16 with two norms 114 us, 5.9
-// TB/s), memory and the barriers of a row's sums the backward one (125 us with
-// the join of its column sums, 5.4 TB/s).
+// TB/s, the vectors in bf16; in fp32, twice as much from the L2 for each row, 125),
+// memory and the barriers of a row's sums the backward one (125 us with the join
+// of its column sums, 5.4 TB/s).
 #include "dev_act.h"
 
 namespace ps {
@@ -236,9 +237,11 @@ enum { kNoBranch = 0, kPlain = 1, kNormed = 2 };
 // whose barriers the load's latency would otherwise add to; a segment's vectors
 // stay in registers, since a load behind those of the next row would wait for
 // them. The widest rows (V > 1) leave no registers for either, and take their
-// vectors when they are needed (4096 x 12288 with both norms 143 -> 128 us); at
-// 16384 columns the sums and two rows' values are still more than the registers
-// hold (33 to 130 of them in scratch memory: 2.0 TB/s with a branch, 4.0 without).
+// vectors when they are needed (4096 x 12288 with both norms 143 -> 128 us). The
+// sums and two rows' values are still more than the registers hold: with four
+// parts a lane 25 to 170 of them are in scratch memory (16384 columns 16-bit: 2.0
+// TB/s with a branch, 4.1 without; 9001 columns 2.5 and 3.2), with three 4 to 23 with
+// a branch; with one part 2 to 5 in fp32 with a branch, but for kEvery.
 // Waits for a load count what was issued behind it, the fewest over all ways
 // there, so a branch around a later load or store makes them waits for nearly
 // everything. Rows of a multiple of 512 columns (kEvery) have no such branch:

@@ -8,7 +8,9 @@
 // or fp16 between that read and the instruction, in the shadow of the matrix
 // instructions before. 16384 tokens, 11008 x 4096: 1175 to 1260 us (1.17 to 1.26
 // PFLOP/s); the matrix units are busy 72% of the time, and shared memory's
-// bandwidth and the last round of tiles bound the rest.
+// bandwidth and the last round of tiles bound the rest. The largest tiles take all
+// 256 registers and keep 2 to 23 more in scratch memory (with scales 2, with the
+// column sums too 8; without scales 9 and 23).
 #include <type_traits>
 
 #include "dev_act.h"
