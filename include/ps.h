@@ -492,9 +492,9 @@ ps_status ps_decode_fp8(const uint8_t* code, const float* scale, float* x, int64
  * s = the smallest power of two >= 2^-126 with max|x| <= 448 s over the finite
  * x; code = x / s rounded to the nearest e4m3 value, ties to even, NaN for an
  * infinite or NaN x. Decode: x = code * s (exact in fp32 and bf16, rounded to
- * fp16), whatever the finite scale. A finite x decodes to a finite one: 2^16 for
- * fp16 and 2^128 for the other types, which codes of the largest values stand
- * for, are the type's largest value. */
+ * fp16), whatever the finite scale. Decoded to its own type a finite x is
+ * finite: 2^16 for fp16 and 2^128 for the other types, which codes of the largest
+ * values stand for, become the type's largest value. */
 ps_status ps_encode_act(const void* x, int32_t type, int64_t rows, int64_t cols, int64_t ld, uint8_t* code,
                         float* scale, ps_stream_t stream);
 ps_status ps_decode_act(const uint8_t* code, const float* scale, void* x, int32_t type, int64_t rows, int64_t cols,
